@@ -419,6 +419,123 @@ int h2o_prompt_scores_noalloc(const void* Q, const void* K, int batch, int heads
  */
 int h2o_selftest_wait_timeout(h2o_handle h);
 
+/*
+ * Paged caches -- the calls h2o_page_tables, h2o_page_write,
+ * h2o_page_attend and h2o_prefix_attend keep every token and read what a
+ * query needs, where the handles above keep a budget and forget the rest.
+ * The pages have no counterpart for them.  They hold no state and allocate
+ * nothing: the caller owns all buffers and gives the stream with each call;
+ * every call may be captured into a CUDA graph.  Calls that share a buffer
+ * one of them writes must be ordered by the caller.  There is no handle and
+ * so no h2o_sync: what a device-side check finds is told by the outputs, as
+ * said below.
+ *
+ *  - A pool has num_pages pages of page_size tokens (16, 32, 64 or 128), for
+ *    kv_heads heads: K, V [num_pages][kv_heads][page_size][head_dim] and
+ *    bounds [num_pages][kv_heads][2][head_dim], each channel's smallest, then
+ *    largest key value of a full page; head_dim 64 or 128, of dtype H2O_F32
+ *    or H2O_BF16 (H2O_KV8 / H2O_KV4: H2O_ERR_UNSUPPORTED).
+ *    num_pages * kv_heads * page_size < 2^31.
+ *  - A request's block table lists its pages in order: token t of request i
+ *    is at offset t % page_size of page table[i][t / page_size].  Its slot is
+ *    that page * page_size + offset.  table_width <= 16384.
+ *  - A call works on `rows` query or key rows of any mix of requests: row r
+ *    belongs to request row_seq[r].
+ *  - Rows of q, k, v and out lie `stride` elements apart (heads and channels
+ *    of a row are contiguous; the stride a multiple of 16 bytes), so slices of
+ *    a fused projection can be given.  Pointers to int arrays are 4-byte, all
+ *    others 16-byte aligned.
+ */
+
+/*
+ * h2o_page_tables -- the pages and slots of a step's new tokens.  Request i
+ * has len_before[i] tokens in the cache and gets n_new[i] (>= 0) more; it
+ * owns ceil(len_before / page_size) pages already and takes the further ones
+ * that len_before + n_new tokens need from the front of free_pages [n_free],
+ * requests in order:
+ *   table     [requests][table_width]: the taken pages are written into their
+ *             places, every other entry is left as it was;
+ *   len_after [requests]: len_before + n_new;
+ *   row_start [requests + 1]: the first row of each request, then their count;
+ *   row_seq, row_pos, slot [rows_cap]: request, position and slot of each
+ *             new token, requests in order; -1 in the rows past the last
+ *             (slot is also -1 where a table or free-list entry is no page
+ *             number);
+ *   status    [4]: {rows, pages taken, longest len_after, error bits}.
+ * All arrays are device int32; none of the outputs overlaps an input.
+ * free_pages is only read: the caller drops
+ * the first status[1] of it.  All or nothing: with an error bit (1: a
+ * negative count, 2: more than rows_cap rows, 4: more than n_free pages,
+ * 8: a request longer than table_width pages) no page is taken, len_after is
+ * len_before and there are no rows.  1 <= requests <= 16384.
+ */
+int h2o_page_tables(const int* len_before, const int* n_new, int requests, const int* free_pages, int n_free,
+                    int page_size, int* table, int table_width, int* len_after, int* row_start, int* row_seq,
+                    int* row_pos, int* slot, int rows_cap, int* status, void* cuda_stream);
+
+/*
+ * h2o_page_write -- key and value rows k, v [rows][kv_heads][head_dim] into
+ * their slots.  A row whose slot is outside the pool (-1: a padding row) is
+ * skipped.  The row that is written to the last offset of a page also leaves
+ * the page's bounds, made from all its keys (a NaN key gives NaN): those of
+ * this call and those the page held before it.  Rows of this call that go to
+ * one page are adjacent and in the order of their slots, as h2o_page_tables
+ * lists them, and no slot comes twice.
+ */
+int h2o_page_write(const void* k, const void* v, long long k_stride, long long v_stride, const int* slot, int rows,
+                   void* K, void* V, void* bounds, int num_pages, int kv_heads, int page_size, int head_dim, int dtype,
+                   void* cuda_stream);
+
+/*
+ * h2o_page_attend -- attention over at most `budget` pages a query row, those
+ * that matter most by a score that reads a page's bounds and not its keys.
+ * Row r sees the tokens 0..row_pos[r] of its request, on n = row_pos / page_size
+ * + 1 pages.  With n <= budget all are read; otherwise, for each cache head,
+ * the `recent` (1 <= recent <= budget) newest pages and the budget - recent
+ * others of the largest
+ *   s_b = sum_g sum_e max(q_ge bounds_b0e, q_ge bounds_b1e),
+ * the sum over the head's `groups` query heads of the largest dot product
+ * that keys within page b's bounds allow (by the exact value of s_b, ties to
+ * the lower page; a NaN ranks first).  Only full pages older than the row's
+ * own are ranked.  out = softmax(scale q.K) V over the tokens of those pages.
+ *   q, out [rows][kv_heads * groups][head_dim] of dtype (sums in fp32; bf16
+ *   weights and outputs are rounded once), query head h * groups + g to cache
+ *   head h; 1 <= groups <= 16.
+ *   bounds may be NULL when budget >= table_width; otherwise budget <= 4096.
+ *   picked: int32 [rows][kv_heads][budget] or NULL, receives the pages read,
+ *   as indexes into the request's table, ascending, -1 behind them.
+ * row_seq[r] < 0 marks a padding row: its rows of out and picked are left as
+ * they were.  A row with row_pos < 0, or all of whose logits are -inf, is
+ * zero.  A row whose row_seq or row_pos is outside the table, or that reads a
+ * table entry outside the pool, is NaN.
+ */
+int h2o_page_attend(const void* q, long long q_stride, const int* row_seq, const int* row_pos, int rows, const void* K,
+                    const void* V, const void* bounds, int num_pages, int kv_heads, int groups, int page_size,
+                    int head_dim, int dtype, const int* table, int requests, int table_width, int budget, int recent,
+                    double scale, void* out, long long out_stride, int* picked, void* cuda_stream);
+
+/*
+ * h2o_prefix_attend -- attention of a batch whose requests share a prefix:
+ * row r attends to the prefix's prefix_len >= 0 tokens, which are on the pages
+ * prefix_table lists, and to the tokens 0..row_pos[r] of its request's own
+ * table (positions and lengths count from the prefix's end; row_pos -1: none).
+ * The prefix is read once for all rows, whatever their number, as a product
+ * over all queries of a cache head.  With prefix_len 0 (prefix_table NULL)
+ * this is attention over whole paged caches.  Other arguments, padding rows
+ * and bad entries as h2o_page_attend (a bad prefix page: NaN in every row).
+ *   work: device buffer of h2o_prefix_work_bytes for the same sizes; what it
+ *   holds before and after does not matter, and calls that may overlap need
+ *   one each.
+ */
+int h2o_prefix_attend(const void* q, long long q_stride, const int* row_seq, const int* row_pos, int rows, const void* K,
+                      const void* V, int num_pages, int kv_heads, int groups, int page_size, int head_dim, int dtype,
+                      const int* prefix_table, int prefix_len, const int* table, int requests, int table_width,
+                      double scale, void* out, long long out_stride, void* work, long long work_bytes,
+                      void* cuda_stream);
+
+/* Bytes of h2o_prefix_attend's workspace (negative: an h2o_status). */
+long long h2o_prefix_work_bytes(int rows, int kv_heads, int groups, int head_dim, int prefix_len, int dtype);
+
 /* Thread-local description of the last failure in this thread ("" if none). */
 const char* h2o_last_error(void);
 

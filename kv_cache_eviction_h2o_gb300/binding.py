@@ -13,6 +13,10 @@ type, query heads per unit, last prompt length) from the calls that made it,
 and checks the type and size of every host array, and of every tensor it
 is given, before the library writes into or reads from it; a raw integer
 pointer is passed through unchecked.
+
+The paged-cache calls (``h2o_page_*``, ``h2o_prefix_*``) have no handle: they
+take torch tensors only, read every size from the tensors' shapes and check
+them against one another.
 """
 import ctypes
 import os
@@ -38,6 +42,7 @@ H2O_KV4 = 4
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _d = ctypes.c_double
+_ll = ctypes.c_longlong
 SIGNATURES = {
     "h2o_init": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i, _i, _i, _i, _d, _vp]),
     "h2o_init_gqa": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i, _i, _i, _i, _i, _d, _vp]),
@@ -65,6 +70,13 @@ SIGNATURES = {
     "fg_prefill": (_i, [_vp, _vp, _vp, _vp, _i]),
     "fg_decode_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp]),
     "fg_get_policy": (_i, [_vp, _vp, _vp, _vp]),
+    "h2o_page_tables": (_i, [_vp, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp]),
+    "h2o_page_write": (_i, [_vp, _vp, _ll, _ll, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "h2o_page_attend": (_i, [_vp, _ll, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _i, _i, _d,
+                             _vp, _ll, _vp, _vp]),
+    "h2o_prefix_attend": (_i, [_vp, _ll, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _vp, _i, _i, _d,
+                               _vp, _ll, _vp, _ll, _vp]),
+    "h2o_prefix_work_bytes": (_ll, [_i, _i, _i, _i, _i, _i]),
 }
 
 H2O_NOALLOC_MAX_TOKENS = 1 << 20
@@ -358,3 +370,143 @@ def h2o_prompt_scores_noalloc(Q, K, batch, heads, T, head_dim, dtype, scale, c, 
     _dev(c, batch * heads * int(T) * 8, "c", ("float64",))
     _check(lib().h2o_prompt_scores_noalloc(_ptr(Q), _ptr(K), batch, heads, int(T), head_dim, dtype,
                                            float(scale), _ptr(c), _stream(stream)))
+
+
+# ------------------------------------------------------------- paged caches
+
+_CODES = {"torch.bfloat16": H2O_BF16, "torch.float32": H2O_F32}
+
+
+def _tensor(x, what, dtype, shape, device):
+    """x is a contiguous tensor of `dtype` and `shape` (None: any size) on `device`."""
+    if not hasattr(x, "data_ptr"):
+        raise TypeError("%s must be a tensor" % what)
+    if x.dtype is not dtype:
+        raise TypeError("%s must be of dtype %s (got %s)" % (what, dtype, x.dtype))
+    if x.device != device:
+        raise ValueError("%s must be on %s (got %s)" % (what, device, x.device))
+    if len(x.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
+        raise ValueError("%s must have shape %s (got %s)" % (what, list(shape), list(x.shape)))
+    if not x.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return x.data_ptr()
+
+
+def _head_rows(x, what, dtype, shape, device):
+    """Pointer and row stride of [rows][heads][channels] whose rows may lie apart."""
+    if not hasattr(x, "data_ptr"):
+        raise TypeError("%s must be a tensor" % what)
+    if x.dtype is not dtype:
+        raise TypeError("%s must be of dtype %s (got %s)" % (what, dtype, x.dtype))
+    if x.device != device:
+        raise ValueError("%s must be on %s (got %s)" % (what, device, x.device))
+    if tuple(x.shape) != shape:
+        raise ValueError("%s must have shape %s (got %s)" % (what, list(shape), list(x.shape)))
+    width = shape[1] * shape[2]
+    s = x.stride()
+    if s[2] != 1 or (shape[1] > 1 and s[1] != shape[2]):
+        raise ValueError("%s must have contiguous heads and channels" % what)
+    return x.data_ptr(), s[0] if shape[0] > 1 else width
+
+
+def _pool(K, V):
+    """(device, element type, its code, pages, heads, page size, channels) of a page pool."""
+    code = _CODES.get(str(getattr(K, "dtype", None)))
+    if code is None:
+        raise TypeError("K must be a tensor of dtype float32 or bfloat16 (got %s)" % getattr(K, "dtype", type(K)))
+    if K.dim() != 4:
+        raise ValueError("K must be [pages][kv_heads][page_size][head_dim] (got %s)" % list(K.shape))
+    device, shape = K.device, tuple(K.shape)
+    _on_current(device)
+    _tensor(K, "K", K.dtype, shape, device)
+    _tensor(V, "V", K.dtype, shape, device)
+    return (device, K.dtype, code) + shape
+
+
+def _on_current(device):
+    import torch
+    if device.type != "cuda":
+        raise ValueError("tensors must be on the GPU (got %s)" % device)
+    if device.index != torch.cuda.current_device():
+        raise ValueError("tensors are on %s, which is not the current device" % device)
+
+
+def h2o_page_tables(len_before, n_new, free_pages, page_size, table, len_after, row_start, row_seq, row_pos, slot, status,
+                    stream=None):
+    """Pages and slots of a step's new tokens; see include/h2o.h.  All int32:
+    len_before, n_new, len_after [requests], free_pages [any], table
+    [requests][width], row_start [requests + 1], row_seq, row_pos, slot
+    [rows_cap], status [4]."""
+    import torch
+    i32, n, dev = torch.int32, len_before.shape[0], len_before.device
+    _on_current(dev)
+    p = [_tensor(len_before, "len_before", i32, (n,), dev), _tensor(n_new, "n_new", i32, (n,), dev),
+         _tensor(free_pages, "free_pages", i32, (None,), dev), _tensor(table, "table", i32, (n, None), dev),
+         _tensor(len_after, "len_after", i32, (n,), dev), _tensor(row_start, "row_start", i32, (n + 1,), dev)]
+    cap = slot.shape[0]
+    q = [_tensor(row_seq, "row_seq", i32, (cap,), dev), _tensor(row_pos, "row_pos", i32, (cap,), dev),
+         _tensor(slot, "slot", i32, (cap,), dev)]
+    _check(lib().h2o_page_tables(p[0], p[1], n, p[2], free_pages.shape[0], page_size, p[3], table.shape[1], p[4], p[5],
+                                 q[0], q[1], q[2], cap, _tensor(status, "status", i32, (4,), dev), _stream(stream)))
+
+
+def h2o_page_write(k, v, slot, K, V, bounds, stream=None):
+    """Key and value rows [rows][kv_heads][head_dim] into their slots; see include/h2o.h."""
+    import torch
+    dev, dt, code, pages, heads, ps, d = _pool(K, V)
+    rows = slot.shape[0]
+    kp, ks = _head_rows(k, "k", dt, (rows, heads, d), dev)
+    vp, vs = _head_rows(v, "v", dt, (rows, heads, d), dev)
+    _check(lib().h2o_page_write(kp, vp, ks, vs, _tensor(slot, "slot", torch.int32, (rows,), dev), rows, K.data_ptr(),
+                                V.data_ptr(), _tensor(bounds, "bounds", dt, (pages, heads, 2, d), dev), pages, heads, ps, d,
+                                code, _stream(stream)))
+
+
+def _query_rows(q, row_seq, row_pos, table, out, pool):
+    import torch
+    dev, dt, _, _, heads, _, d = pool
+    rows, i32 = row_seq.shape[0], torch.int32
+    hq = q.shape[1] if q.dim() == 3 else 0
+    if hq < 1 or hq % heads:
+        raise ValueError("q must be [rows][kv_heads * groups][head_dim] (got %s for %d cache heads)" % (list(q.shape), heads))
+    qp, qs = _head_rows(q, "q", dt, (rows, hq, d), dev)
+    op, os_ = _head_rows(out, "out", dt, (rows, hq, d), dev)
+    return (qp, qs, _tensor(row_seq, "row_seq", i32, (rows,), dev), _tensor(row_pos, "row_pos", i32, (rows,), dev), rows,
+            hq // heads, _tensor(table, "table", i32, (None, None), dev), op, os_)
+
+
+def h2o_page_attend(q, row_seq, row_pos, K, V, bounds, table, budget, recent, scale, out, picked=None, stream=None):
+    """Attention over the `recent` newest pages and the best-scoring others;
+    see include/h2o.h."""
+    import torch
+    pool = _pool(K, V)
+    dev, dt, code, pages, heads, ps, d = pool
+    qp, qs, sp, pp, rows, groups, tp, op, os_ = _query_rows(q, row_seq, row_pos, table, out, pool)
+    bp = None if bounds is None else _tensor(bounds, "bounds", dt, (pages, heads, 2, d), dev)
+    kp = None if picked is None else _tensor(picked, "picked", torch.int32, (rows, heads, budget), dev)
+    _check(lib().h2o_page_attend(qp, qs, sp, pp, rows, K.data_ptr(), V.data_ptr(), bp, pages, heads, groups, ps, d, code, tp,
+                                 table.shape[0], table.shape[1], budget, recent, float(scale), op, os_, kp, _stream(stream)))
+
+
+def h2o_prefix_work_bytes(rows, kv_heads, groups, head_dim, prefix_len, dtype):
+    n = lib().h2o_prefix_work_bytes(rows, kv_heads, groups, head_dim, prefix_len, dtype)
+    if n < 0:
+        raise H2OError(int(n), h2o_last_error())
+    return n
+
+
+def h2o_prefix_attend(q, row_seq, row_pos, K, V, prefix_table, prefix_len, table, scale, out, work, stream=None):
+    """Attention over a prefix that all rows share and each request's own
+    pages; work: a uint8 tensor of h2o_prefix_work_bytes.  See include/h2o.h."""
+    import torch
+    pool = _pool(K, V)
+    dev, dt, code, pages, heads, ps, d = pool
+    qp, qs, sp, pp, rows, groups, tp, op, os_ = _query_rows(q, row_seq, row_pos, table, out, pool)
+    xp = None
+    if prefix_table is not None:
+        xp = _tensor(prefix_table, "prefix_table", torch.int32, (None,), dev)
+        if prefix_table.shape[0] * ps < prefix_len:
+            raise ValueError("prefix_table lists %d pages of %d tokens, prefix_len is %d" % (prefix_table.shape[0], ps, prefix_len))
+    _check(lib().h2o_prefix_attend(qp, qs, sp, pp, rows, K.data_ptr(), V.data_ptr(), pages, heads, groups, ps, d, code, xp,
+                                   prefix_len, tp, table.shape[0], table.shape[1], float(scale), op, os_,
+                                   _tensor(work, "work", torch.uint8, (None,), dev), work.shape[0], _stream(stream)))

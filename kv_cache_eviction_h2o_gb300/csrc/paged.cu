@@ -1,0 +1,293 @@
+// paged.cu -- bookkeeping and writing of the paged cache: which pages and
+// slots a step's new tokens take, and their key and value rows into them.
+#include <algorithm>
+#include <climits>
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace h2o {
+
+namespace {
+
+// ------------------------------------------------------------ block tables
+//
+// With b_i tokens before and t_i new ones, request i owns o_i = ceil(b_i / ps)
+// pages and takes n_i = ceil((b_i + t_i) / ps) - o_i more from the free list,
+// so with P_i = sum_{j<i} n_j and R_i = sum_{j<i} t_j
+//   table[i][o_i + j] = free[P_i + j],   row R_i + x: pos = b_i + x,
+//   slot = table[i][pos / ps] * ps + pos % ps.
+// Every CTA makes both running sums over all requests for itself (8 bytes a
+// request, read from L2) and then writes its share of the rows and pages, so
+// one launch does it with no order between CTAs.  A slot is taken from the
+// free list, not from the table entry another CTA may be writing.  Bound:
+// launch latency for a decode step, the maps' 12 bytes a row for prompts.
+
+enum TableError : int { kTableCount = 1, kTableRows = 2, kTablePages = 4, kTableWidth = 8 };
+
+struct TableSums {
+    long long rows, pages;
+};
+
+__device__ __forceinline__ TableSums sums_up(TableSums x, int d, int lane)
+{
+    const long long r = __shfl_up_sync(0xffffffffu, x.rows, d), p = __shfl_up_sync(0xffffffffu, x.pages, d);
+    if (lane >= d) { x.rows += r; x.pages += p; }
+    return x;
+}
+
+// the last i in [0, n) with start[i] <= x (start ascending, start[0] <= x)
+__device__ __forceinline__ int owner_of(const int* start, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void page_tables_kernel(const TablesArgs a)
+{
+    extern __shared__ int sm[];
+    int* start = sm;                   // [n + 1] first row of each request
+    int* first = sm + a.n + 1;         // [n + 1] first free-list entry of each
+    __shared__ TableSums warp_sum[32];
+    __shared__ int warp_max[32], flags;
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int sh = __ffs(a.ps) - 1;
+    const int per = (a.n + nt - 1) / nt, i0 = min(a.n, tid * per), i1 = min(a.n, i0 + per);
+    if (tid == 0) flags = 0;
+    __syncthreads();
+
+    TableSums mine{0, 0};
+    int longest = 0, bad = 0;
+    for (int i = i0; i < i1; ++i) {
+        const long long b = a.before[i], t = a.fresh[i];
+        if (b < 0 || t < 0) { bad |= kTableCount; continue; }
+        const long long want = (b + t + a.ps - 1) >> sh;
+        if (want > a.width) bad |= kTableWidth;
+        mine.rows += t;
+        mine.pages += want - ((b + a.ps - 1) >> sh);
+        longest = max(longest, (int)min(b + t, (long long)INT_MAX));
+    }
+    if (bad) atomicOr(&flags, bad);
+    TableSums upto = mine;
+    for (int d = 1; d < 32; d <<= 1) upto = sums_up(upto, d, lane);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) warp_sum[warp] = upto;
+    if (lane == 0) warp_max[warp] = longest;
+    __syncthreads();
+    if (warp == 0) {
+        const bool in = lane < (nt >> 5);
+        TableSums w = in ? warp_sum[lane] : TableSums{0, 0};
+        longest = __reduce_max_sync(0xffffffffu, in ? warp_max[lane] : 0);
+        for (int d = 1; d < 32; d <<= 1) w = sums_up(w, d, lane);
+        if (in) warp_sum[lane] = w;
+        if (lane == 0) warp_max[0] = longest;
+    }
+    __syncthreads();
+    const TableSums all = warp_sum[(nt >> 5) - 1];
+    int err = flags;
+    if (all.rows > a.cap) err |= kTableRows;
+    if (all.pages > a.n_free) err |= kTablePages;
+    const int rows = err ? 0 : (int)all.rows, pages = err ? 0 : (int)all.pages;
+
+    // all or nothing: with an error no request gets rows or pages
+    long long r = upto.rows - mine.rows + (warp ? warp_sum[warp - 1].rows : 0);
+    long long p = upto.pages - mine.pages + (warp ? warp_sum[warp - 1].pages : 0);
+    for (int i = i0; i < i1; ++i) {
+        const int b = a.before[i], t = err ? 0 : a.fresh[i];
+        start[i] = err ? 0 : (int)r;
+        first[i] = err ? 0 : (int)p;
+        if (!err) {
+            r += t;
+            p += ((b + t + a.ps - 1) >> sh) - ((b + a.ps - 1) >> sh);
+        }
+        if (blockIdx.x == 0) {
+            a.after[i] = b + t;
+            a.row_start[i] = start[i];
+        }
+    }
+    if (tid == 0) {
+        start[a.n] = rows;
+        first[a.n] = pages;
+        if (blockIdx.x == 0) {
+            a.row_start[a.n] = rows;
+            a.status[0] = rows;
+            a.status[1] = pages;
+            a.status[2] = err ? 0 : warp_max[0];
+            a.status[3] = err;
+        }
+    }
+    __syncthreads();
+
+    const int g = blockIdx.x * nt + tid, stride = gridDim.x * nt;
+    for (int x = g; x < pages; x += stride) {
+        const int i = owner_of(first, a.n, x);
+        a.table[(size_t)i * a.width + ((a.before[i] + a.ps - 1) >> sh) + (x - first[i])] = a.free_pages[x];
+    }
+    // four rows a thread, written as 16 bytes where the maps lie on them
+    const bool wide = (((size_t)a.row_seq | (size_t)a.row_pos | (size_t)a.slot) & 15) == 0;
+    for (int x0 = g; x0 < (a.cap + 3) / 4; x0 += stride) {
+        int seq[4], pos[4], slot[4];
+        int i = x0 * 4 < rows ? owner_of(start, a.n, x0 * 4) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int x = x0 * 4 + j;
+            seq[j] = pos[j] = slot[j] = -1;
+            if (x >= rows) continue;
+            while (start[i + 1] <= x) ++i;
+            const int b = a.before[i], at = b + (x - start[i]), owned = (b + a.ps - 1) >> sh, pg = at >> sh;
+            const int page = pg < owned ? a.table[(size_t)i * a.width + pg] : a.free_pages[first[i] + pg - owned];
+            seq[j] = i;
+            pos[j] = at;
+            // a table or free-list entry that is no page gives no slot
+            slot[j] = page >= 0 && page <= ((INT_MAX - a.ps) >> sh) ? (page << sh) + (at & (a.ps - 1)) : -1;
+        }
+        if (wide && x0 * 4 + 4 <= a.cap) {
+            reinterpret_cast<int4*>(a.row_seq)[x0] = make_int4(seq[0], seq[1], seq[2], seq[3]);
+            reinterpret_cast<int4*>(a.row_pos)[x0] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            reinterpret_cast<int4*>(a.slot)[x0] = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (x0 * 4 + j >= a.cap) break;
+                a.row_seq[x0 * 4 + j] = seq[j];
+                a.row_pos[x0 * 4 + j] = pos[j];
+                a.slot[x0 * 4 + j] = slot[j];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------- page writes
+//
+// A row goes to page slot / ps, offset slot % ps, as it is; the row with a
+// page's last offset also leaves the page's bounds, the smallest and largest
+// value of each channel over its ps keys (NaN where one is NaN).  Bounds are
+// made when a page fills, from all its keys, and not kept up to date row by
+// row: a page that is not full is never ranked, and a page that was rolled
+// back and filled again gets bounds of what it holds.  Keys of rows in this
+// call are read from k (the rows before this one, when their slots run up to
+// it), older ones from the page.  Bound: HBM.
+
+template <typename T> struct Vec16;
+template <> struct Vec16<float> {
+    float x[4];
+    __device__ __forceinline__ void load(const void* p)
+    {
+        const float4 w = *static_cast<const float4*>(p);
+        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+    }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]); }
+    __device__ __forceinline__ void low(const Vec16& o)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("min.NaN.f32 %0, %0, %1;" : "+f"(x[i]) : "f"(o.x[i]));
+    }
+    __device__ __forceinline__ void high(const Vec16& o)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(x[i]) : "f"(o.x[i]));
+    }
+};
+template <> struct Vec16<__nv_bfloat16> {
+    uint32_t x[4];
+    __device__ __forceinline__ void load(const void* p)
+    {
+        const uint4 w = *static_cast<const uint4*>(p);
+        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+    }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]); }
+    __device__ __forceinline__ void low(const Vec16& o)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(o.x[i]));
+    }
+    __device__ __forceinline__ void high(const Vec16& o)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(o.x[i]));
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) page_write_kernel(const PagePool p, const T* __restrict__ k, const T* __restrict__ v,
+                                                         long long k_stride, long long v_stride,
+                                                         const int* __restrict__ slot, int rows)
+{
+    constexpr int E = 16 / sizeof(T), VPR = D / E;        // elements of a vector, vectors of a row
+    const int sh = __ffs(p.ps) - 1;
+    const long long slots = (long long)p.pages * p.ps;
+    const long long total = (long long)rows * p.heads * VPR;
+    T* K = static_cast<T*>(p.K);
+    T* V = static_cast<T*>(p.V);
+    for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < total; x += (long long)gridDim.x * blockDim.x) {
+        const int e = (int)(x % VPR) * E;
+        const long long rh = x / VPR;
+        const int h = (int)(rh % p.heads), r = (int)(rh / p.heads);
+        const int s = slot[r];
+        if (s < 0 || s >= slots) continue;
+        const int page = s >> sh, at = s & (p.ps - 1);
+        const size_t base = ((size_t)page * p.heads + h) * p.ps * D + e;
+        Vec16<T> kv, vv;
+        kv.load(k + r * k_stride + (size_t)h * D + e);
+        vv.load(v + r * v_stride + (size_t)h * D + e);
+        kv.store(K + base + (size_t)at * D);
+        vv.store(V + base + (size_t)at * D);
+        if (at == p.ps - 1) {
+            // how many rows before this one hold the slots before it
+            int run = 0;
+            while (run < at && r - run > 0 && slot[r - run - 1] == s - run - 1) ++run;
+            Vec16<T> lo = kv, hi = kv;
+            for (int o = 1; o <= at; ++o) {
+                Vec16<T> w;
+                if (o <= run) w.load(k + (r - o) * k_stride + (size_t)h * D + e);
+                else w.load(K + base + (size_t)(at - o) * D);
+                lo.low(w);
+                hi.high(w);
+            }
+            T* b = static_cast<T*>(p.bounds) + ((size_t)page * p.heads + h) * 2 * D + e;
+            lo.store(b);
+            hi.store(b + D);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t st)
+{
+    const long long work = std::max<long long>(a.n, ((long long)a.cap + 3) / 4);
+    const int threads = work <= 256 ? 256 : 1024;
+    const int grid = (int)std::min<long long>(152, std::max<long long>(1, (work + threads - 1) / threads));
+    const size_t smem = 2 * sizeof(int) * ((size_t)a.n + 1);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   2 * (int)sizeof(int) * (kMaxPageRequests + 1));
+        if (e != cudaSuccess) return e;
+    }
+    page_tables_kernel<<<grid, threads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_page_write(const PagePool& p, const void* k, const void* v, long long k_stride, long long v_stride,
+                              const int* slot, int rows, cudaStream_t st)
+{
+    const int vpr = p.D * (p.dtype ? 2 : 4) / 16;
+    const long long total = (long long)rows * p.heads * vpr;
+    const unsigned grid = (unsigned)std::min<long long>((total + 255) / 256, 1 << 20);
+    auto go = [&](auto t, auto d) {
+        using T = decltype(t);
+        page_write_kernel<T, decltype(d)::value><<<grid, 256, 0, st>>>(p, static_cast<const T*>(k), static_cast<const T*>(v),
+                                                                       k_stride, v_stride, slot, rows);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (p.dtype) p.D == 64 ? go(__nv_bfloat16(), D64()) : go(__nv_bfloat16(), D128());
+    else p.D == 64 ? go(float(), D64()) : go(float(), D128());
+    return cudaGetLastError();
+}
+
+}  // namespace h2o
