@@ -64,6 +64,7 @@ int check_rows(const PagePool& p, const PageRows& r, double scale)
     if (r.width < 1 || r.width > kMaxTableWidth)
         return set_last_error(H2O_ERR_ARG, "table_width must be in [1, %d] (got %d)", kMaxTableWidth, r.width);
     if (!(scale > 0.0) || !std::isfinite(scale)) return set_last_error(H2O_ERR_ARG, "scale must be finite and > 0");
+    if (!(r.qscale > 0.f) || !std::isfinite(r.qscale)) return set_last_error(H2O_ERR_ARG, "scale is out of fp32's range");
     if ((long long)r.rows * p.heads > (1 << 24) / r.G)
         return set_last_error(H2O_ERR_ARG, "rows * kv_heads * groups must be at most 2^24");
     if (!r.table) return set_last_error(H2O_ERR_ARG, "table must be non-NULL");

@@ -54,6 +54,10 @@ struct PrefixPart {
     int splits;
 };
 
+// the same on the tensor cores (bf16); keys of each range
+int prefix_tc_range(int rows, int heads, int G, int prefix_len);
+cudaError_t launch_prefix_tc(const PagePool& p, const PageRows& r, const int* prefix_table, int prefix_len,
+                             const PrefixPart& part, cudaStream_t st);
 cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t st);
 cudaError_t launch_page_write(const PagePool& p, const void* k, const void* v, long long k_stride, long long v_stride,
                               const int* slot, int rows, cudaStream_t st);

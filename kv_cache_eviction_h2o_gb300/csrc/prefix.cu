@@ -14,10 +14,8 @@ namespace {
 
 constexpr int kSMs = 152;
 
-// --------------------------------------------------------------- CUDA cores
-//
-// 64 query rows x 64 keys a step, fp32 throughout: 16 x 16 threads, 4 x 4
-// logits and 4 x D / 16 output channels each.
+// fp32 on the CUDA cores (bf16: prefix_tc.cu).  64 query rows x 64 keys a step: 16 x 16
+// threads, 4 x 4 logits and 4 x D / 16 output channels each.
 
 constexpr int kRows = 64, kCols = 64;
 
@@ -29,31 +27,28 @@ struct SimtSmem {
 };
 
 // prefix positions [j0, j1) of one cache head into S.kv, zeros past j1
-template <typename T, int D>
-__device__ __forceinline__ void load_rows(float (*dst)[D + 4], const T* src, const PagePool& pool, const int* table, int h,
+template <int D>
+__device__ __forceinline__ void load_rows(float (*dst)[D + 4], const float* src, const PagePool& pool, const int* table, int h,
                                           int j0, int j1, bool& bad)
 {
-    constexpr int N = 16 / sizeof(T), VPR = D / N;
+    constexpr int N = 4, VPR = D / N;
     const int sh = __ffs(pool.ps) - 1;
     for (int i = threadIdx.x; i < kCols * VPR; i += 256) {
         const int r = i / VPR, e = (i % VPR) * N, j = j0 + r;
-        float x[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (j < j1) {
             const int pg = table[j >> sh];
             if ((unsigned)pg < (unsigned)pool.pages)
-                load_vec<T, N>(src + (((size_t)pg * pool.heads + h) * pool.ps + (j & (pool.ps - 1))) * D + e, x);
+                x = *reinterpret_cast<const float4*>(src + (((size_t)pg * pool.heads + h) * pool.ps + (j & (pool.ps - 1))) * D + e);
             else
                 bad = true;
         }
-#pragma unroll
-        for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(&dst[r][e + k]) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        *reinterpret_cast<float4*>(&dst[r][e]) = x;
     }
 }
 
 // grid: (query tile, split, cache head)
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, const PageRows R, const int* __restrict__ table,
                                                           const int prefix_len, const int per, const PrefixPart part)
 {
@@ -65,7 +60,7 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, c
     bool bad = false;
     for (int i = tid; i < kRows * D; i += 256) {
         const int r = i / D, e = i % D, x = x0 + r;
-        S.q[r][e] = x < nx ? Elem<T>::to_f(static_cast<const T*>(R.q)[(size_t)(x / G) * R.q_stride + (size_t)(h * G + x % G) * D + e]) : 0.f;
+        S.q[r][e] = x < nx ? static_cast<const float*>(R.q)[(size_t)(x / G) * R.q_stride + (size_t)(h * G + x % G) * D + e] : 0.f;
     }
     constexpr int NJ = D / 64;
     float m[4], l[4], o[4][NJ][4];
@@ -80,7 +75,7 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, c
     }
     for (int j = j0; j < j1; j += kCols) {
         __syncthreads();
-        load_rows<T, D>(S.kv, static_cast<const T*>(pool.K), pool, table, h, j, j1, bad);
+        load_rows<D>(S.kv, static_cast<const float*>(pool.K), pool, table, h, j, j1, bad);
         __syncthreads();
         float z[4][4] = {};
 #pragma unroll 4
@@ -126,7 +121,7 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, c
                 for (int k = 0; k < 4; ++k) o[i][n][k] *= a;
         }
         __syncthreads();
-        load_rows<T, D>(S.kv, static_cast<const T*>(pool.V), pool, table, h, j, j1, bad);
+        load_rows<D>(S.kv, static_cast<const float*>(pool.V), pool, table, h, j, j1, bad);
         __syncthreads();
 #pragma unroll 2
         for (int c = 0; c < kCols; c += 4) {
@@ -179,28 +174,25 @@ int range_keys(int rows, int heads, int G, int prefix_len)
 int prefix_splits(int rows, int heads, int G, int D, int prefix_len, int dtype)
 {
     if (rows < 1 || prefix_len < 1) return 0;
-    const int per = range_keys(rows, heads, G, prefix_len);
+    const int per = dtype ? prefix_tc_range(rows, heads, G, prefix_len) : range_keys(rows, heads, G, prefix_len);
     return (prefix_len + per - 1) / per;
 }
 
 cudaError_t launch_prefix(const PagePool& p, const PageRows& r, const int* prefix_table, int prefix_len,
                           const PrefixPart& part, cudaStream_t st)
 {
+    if (p.dtype) return launch_prefix_tc(p, r, prefix_table, prefix_len, part, st);
     const int per = range_keys(r.rows, p.heads, r.G, prefix_len);
     const dim3 grid((unsigned)((r.rows * (long long)r.G + kRows - 1) / kRows), (unsigned)part.splits, (unsigned)p.heads);
-    auto go = [&](auto t, auto d) {
-        using T = decltype(t);
+    auto go = [&](auto d) {
         constexpr int D = decltype(d)::value;
         const int smem = (int)sizeof(SimtSmem<D>);
-        const cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        prefix_simt_kernel<T, D><<<grid, 256, smem, st>>>(p, r, prefix_table, prefix_len, per, part);
+        prefix_simt_kernel<D><<<grid, 256, smem, st>>>(p, r, prefix_table, prefix_len, per, part);
         return cudaGetLastError();
     };
-    using D64 = std::integral_constant<int, 64>;
-    using D128 = std::integral_constant<int, 128>;
-    if (p.dtype) return p.D == 64 ? go(__nv_bfloat16(), D64()) : go(__nv_bfloat16(), D128());
-    return p.D == 64 ? go(float(), D64()) : go(float(), D128());
+    return p.D == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
 }
 
 }  // namespace h2o

@@ -1,0 +1,454 @@
+// prefix_tc.cu -- the shared prefix's part of h2o_prefix_attend on the
+// 5th-generation tensor cores (bf16).
+//
+// Query rows of one cache head (row r's G query heads are rows r G .. r G + G - 1)
+// go in tiles of 128, keys in tiles of 128, and a CTA sweeps a range of the
+// prefix with two score streams:
+//   S = Q K^T      (SMEM x SMEM -> TMEM, M = N = 128, K = D)
+//   P = 2^(c S - m)  (128 threads a stream, thread = TMEM lane = query row)
+//   O += P V       (TMEM x SMEM -> TMEM, M = 128, N = D, K = 128)
+// so that one stream's exponentials run under the other's products.  With more
+// than 128 query rows left the streams are two query tiles over the same keys
+// (each key tile is read once for 256 rows); with fewer they are the even and
+// the odd key tiles of one query tile, joined at the end.
+//
+// One CTA per SM: TMEM holds S and O of both streams (P overwrites S: the
+// tensor pipe works in the order of issue, and S of the next tile is issued
+// after the product that reads P).  Warp 0 loads key and value tiles with TMA
+// (a box per page and 64 channels, so pages lie anywhere), lane 0 of warp 1
+// issues the products, warps 4..7 and 8..11 are the streams.  A row's maximum
+// m is raised, and O scaled, only when a logit passes it by more than 2^8: the
+// weights are relative to m in any case, and l stays in fp32.  P is rounded
+// to bf16 for the product (2^-9 relative a weight, as the output is), the sums
+// l are of the unrounded weights.  Waits are bounded; one that runs out leaves
+// NaN sums.
+#include <algorithm>
+
+#include "paged.h"
+#include "tc.cuh"
+
+namespace h2o {
+
+namespace {
+
+constexpr int kSMs = 152;
+constexpr int kT = 128;
+constexpr int kThreads = 384;
+constexpr uint32_t kBox = kT * 64 * 2;             // 128 rows x 64 channels: 16 KB
+constexpr float kRaise = 8.f;
+
+template <int D> struct Cfg {
+    static constexpr int kBoxes = D / 64;
+    static constexpr uint32_t kTile = kBoxes * kBox;
+    static constexpr int kSlots = D == 128 ? 5 : 8;    // K and V tiles in flight
+};
+
+template <int D>
+struct alignas(1024) Smem {
+    uint8_t q[2][Cfg<D>::kTile];
+    uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
+    float2 xml[kT];
+    uint64_t full[Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
+    uint64_t q_ready, s_ready[2], p_ready[2], pv_done[2], last;
+    uint32_t tmem;
+    int abort, bad;
+};
+static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "one CTA's shared memory");
+
+// accumulator fp32, bf16 A and B, A K-major, B K-major or (bit 16) N-major
+template <int N, bool BMN>
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((BMN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kT >> 4) << 24);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"(acc)
+                 : "memory");
+}
+
+// descriptor of the value tile as the K x N operand, N (channels) contiguous:
+// 64-channel boxes 16 KB apart (leading offset), 8 keys every 1024 B
+__device__ __forceinline__ uint64_t value_desc(const void* p)
+{
+    return (uint64_t)((smem_u32(p) & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// The ring's order of use: K(0) .. K(L - 1), then V(t), K(t + L) for t = 0, 1, ..
+// (L = 1: both streams read each tile; 2: the streams take turns); V(t)'s place:
+__device__ __forceinline__ int v_at(int t, int n, int L) { return t + min(n, t + L); }
+
+template <int D>
+__device__ __forceinline__ bool wait(Smem<D>& S, uint64_t* bar, int count)
+{
+    // the barrier's phase number `count` (from 0)
+    if (mbar_wait(bar, (uint32_t)count & 1u)) return *(volatile int*)&S.abort == 0;
+    *(volatile int*)&S.abort = 1;
+    return false;
+}
+
+// grid: (pair of query tiles, range of the prefix, cache head)
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV, const PagePool pool,
+                     const PageRows R, const int* __restrict__ table, const int prefix_len, const int per, const PrefixPart part)
+{
+    using C = Cfg<D>;
+    constexpr int NS = C::kSlots;
+    extern __shared__ unsigned char raw[];
+    Smem<D>& S = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = R.G, nx = R.rows * G, h = blockIdx.z, x0 = blockIdx.x * 2 * kT;
+    const bool two = x0 + kT < nx;                   // two query tiles
+    const int L = two ? 1 : 2;
+    const int j0 = blockIdx.y * per, j1 = min(prefix_len, j0 + per);
+    const int n = (j1 - j0 + kT - 1) / kT;           // key tiles, at least one
+    auto valid_of = [&](int t) { return min(kT, j1 - j0 - t * kT); };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&S.full[s], 1);
+            mbar_init(&S.empty[s], 1);
+        }
+        mbar_init(&S.q_ready, two ? 8 : 4);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&S.s_ready[s], 1);
+            mbar_init(&S.p_ready[s], 4);
+            mbar_init(&S.pv_done[s], 1);
+        }
+        mbar_init(&S.last, 1);
+        S.abort = S.bad = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&S.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    auto tS = [&](int s) { return tmem + (uint32_t)(s * kT); };
+    auto tO = [&](int s) { return tmem + (uint32_t)(2 * kT + s * D); };
+
+    if (warp == 0) {
+        // ------------------------------------------------ loads
+        const int ps = pool.ps;
+        const uint32_t page_bytes = (uint32_t)ps * 128u;   // of one box
+        int at = 0;
+        bool ok = true;
+        auto load = [&](const CUtensorMap* map, int t) {
+            if (!ok) return;
+            const int s = at % NS;
+            if (at >= NS) ok = __all_sync(0xffffffffu, wait(S, &S.empty[s], at / NS - 1));
+            if (!ok) return;
+            const int pages = (valid_of(t) + ps - 1) / ps;
+            if (lane == 0) mbar_arrive_expect_tx(&S.full[s], (uint32_t)pages * page_bytes * C::kBoxes);
+            __syncwarp();
+            if (lane < pages * C::kBoxes) {
+                const int i = lane / C::kBoxes, b = lane % C::kBoxes;
+                int pg = table[(j0 + t * kT) / ps + i];
+                if ((unsigned)pg >= (unsigned)pool.pages) { pg = 0; *(volatile int*)&S.bad = 1; }
+                tma_load_2d(S.ring[s] + b * kBox + i * page_bytes, map, b * 64, (pg * pool.heads + h) * ps, &S.full[s]);
+            }
+            __syncwarp();
+            ++at;
+        };
+        for (int t = 0; t < min(L, n); ++t) load(&mapK, t);
+        for (int t = 0; t < n; ++t) {
+            load(&mapV, t);
+            if (t + L < n) load(&mapK, t + L);
+        }
+        // a load that was never used (an aborted sweep) lands before the shared memory is given up
+        if (lane == 0 && *(volatile int*)&S.abort)
+            for (int i = max(0, at - NS); i < at; ++i) mbar_wait(&S.full[i % NS], (uint32_t)(i / NS) & 1u);
+    } else if (warp == 1) {
+        // ------------------------------------------------ products
+        if (lane == 0) {
+            bool ok = wait(S, &S.q_ready, 0);
+            auto slot_full = [&](int i) {
+                if (ok) ok = wait(S, &S.full[i % NS], i / NS);
+            };
+            auto score = [&](int s, int i) {
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t a = sw128_desc(S.q[two ? s : 0]), b = sw128_desc(S.ring[i % NS]);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t off = (uint64_t)(((uint32_t)(k / 4) * kBox + (uint32_t)(k % 4) * 32u) >> 4);
+                    mma_ss(tS(s), a + off, b + off, kIdesc<kT, false>, k > 0);
+                }
+                tc_commit(&S.s_ready[s]);
+            };
+            auto values = [&](int s, int step, int i, int valid) {
+                if (ok) ok = wait(S, &S.p_ready[s], step);
+                slot_full(i);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t b = value_desc(S.ring[i % NS]);
+                const int nk = (valid + 15) / 16;
+                for (int k = 0; k < nk; ++k)
+                    mma_ts(tO(s), tS(s) + 8u * (uint32_t)k, b + (uint64_t)((uint32_t)k * 2048u >> 4), kIdesc<D, true>, step > 0 || k > 0);
+                tc_commit(&S.pv_done[s]);
+            };
+            auto release = [&](int i) {
+                if (ok) tc_commit(&S.empty[i % NS]);
+            };
+            if (two) {
+                slot_full(0);
+                score(0, 0);
+                score(1, 0);
+                release(0);
+                for (int t = 0; t < n; ++t) {
+                    const int v = v_at(t, n, 1), k = v + 1;
+                    values(0, t, v, valid_of(t));
+                    if (t + 1 < n) { slot_full(k); score(0, k); }
+                    values(1, t, v, valid_of(t));
+                    release(v);
+                    if (t + 1 < n) { score(1, k); release(k); }
+                }
+            } else {
+                for (int t = 0; t < min(2, n); ++t) { slot_full(t); score(t, t); release(t); }
+                for (int t = 0; t < n; ++t) {
+                    const int s = t & 1, v = v_at(t, n, 2), k = v + 1;
+                    values(s, t >> 1, v, valid_of(t));
+                    release(v);
+                    if (t + 2 < n) { slot_full(k); score(s, k); release(k); }
+                }
+            }
+            // everything issued is done before TMEM is given back
+            tc_commit(&S.last);
+            mbar_wait(&S.last, 0);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------ softmax
+        const int s = (warp - 4) >> 2, w = warp & 3, row = w * 32 + lane;
+        const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        if (two || s == 0) {
+            // this stream's query row into the swizzled tile
+            const int x = x0 + s * kT + row;
+            uint8_t* dst = S.q[s] + row * 128;
+            const uint4* src = nullptr;
+            if (x < nx)
+                src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(R.q) + (size_t)(x / G) * R.q_stride +
+                                                     (size_t)(h * G + x % G) * D);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(dst + (c / 8) * kBox + (((c & 7) ^ (row & 7)) << 4)) = src ? src[c] : make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.q_ready);
+        }
+        const float c2 = R.qscale;
+        const int steps = two ? n : (n + 1 - s) / 2;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < steps && ok; ++i) {
+            const int t = two ? i : 2 * i + s, valid = valid_of(t);
+            ok = wait(S, &S.s_ready[s], i);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t z[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc_ld32_issue(tS(s) + lanes + 32u * c, z[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc_ld32_wait(z[c]);
+            if (valid < kT) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c * 32 + k >= valid) z[c][k] = 0xff800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                mx[c] = __uint_as_float(z[c][0]);
+#pragma unroll
+                for (int k = 1; k < 31; k += 2) mx[c] = max3f(mx[c], __uint_as_float(z[c][k]), __uint_as_float(z[c][k + 1]));
+                mx[c] = fmaxf(mx[c], __uint_as_float(z[c][31]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+            const bool raise = top > m + kRaise;                 // (m = -inf: any finite logit)
+            if (__any_sync(0xffffffffu, raise)) {
+                const float a = raise ? ex2_fast(m - top) : 1.f;
+                if (raise) {
+                    m = top;
+                    l *= a;
+                }
+                if (i > 0) {
+                    ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s], i - 1));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tc_ld16_issue(tO(s) + lanes + (uint32_t)c, o);
+                        tc_ld16_wait(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                        tc_st16(tO(s) + lanes + (uint32_t)c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            const float2 cc = make_float2(c2, c2), nb = make_float2(-base, -base);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t p[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float2 e = __ffma2_rn(make_float2(__uint_as_float(z[c][2 * k]), __uint_as_float(z[c][2 * k + 1])), cc, nb);
+                    const float2 x = make_float2(ex2_fast(e.x), ex2_fast(e.y));
+                    sum[k & 1] = __fadd2_rn(sum[k & 1], x);
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[k]) : "f"(x.y), "f"(x.x));
+                }
+                tc_st16(tS(s) + lanes + 16u * c, p);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (t == n - 1 && valid < kT && (two ? s == 0 : true)) {
+                // the value rows behind the range's last key in its group of 16: their weights are 0, but what lies there may be NaN
+                const int v = v_at(t, n, L), end = (valid + 15) & ~15;
+                ok = __all_sync(0xffffffffu, wait(S, &S.full[v % NS], v / NS));
+                if (!ok) break;
+                for (int x = row; x < (end - valid) * C::kBoxes * 8; x += kT)
+                    *reinterpret_cast<uint4*>(S.ring[v % NS] + (x >> 3) % C::kBoxes * kBox + (valid + (x >> 3) / C::kBoxes) * 128 + (x & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            tc_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_ready[s]);
+        }
+        if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s], steps - 1));
+        tc_fence_after();
+
+        // ------------------------------------------------ results
+        // one query tile: stream 1 hands its sums over in the ring (nothing is in flight there: both streams are through)
+        bool all = true;
+        if (!two) {
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            all = __all_sync(0xffffffffu, ok && *(volatile int*)&S.abort == 0);
+            float* xo = reinterpret_cast<float*>(S.ring[0]);
+            if (s == 1) {
+                S.xml[row] = make_float2(m, l);
+                if (all && steps > 0)
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tc_ld16_issue(tO(1) + lanes + (uint32_t)c, o);
+                        tc_ld16_wait(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) xo[(c + k) * kT + row] = __uint_as_float(o[k]);
+                    }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+        const int x = x0 + s * kT + row;
+        if (two || s == 0) {
+            float a = 1.f, b = 0.f;                              // of this stream's sums, of the other's
+            const float* xo = reinterpret_cast<const float*>(S.ring[0]);
+            const bool join = !two && n > 1;
+            if (join) {
+                const float2 y = S.xml[row];
+                const float mm = fmaxf(m, y.x), base = mm == -INFINITY ? 0.f : mm;
+                a = ex2_fast(m - base);
+                b = ex2_fast(y.x - base);
+                l = l * a + y.y * b;
+                m = mm;
+            }
+            const bool fine = __all_sync(0xffffffffu, ok && all && *(volatile int*)&S.abort == 0);
+            const size_t qr = ((size_t)blockIdx.y * R.rows * pool.heads + (size_t)(x / G) * pool.heads + h) * G + x % G;
+            if (x < nx) part.ml[qr] = make_float2(m, fine && *(volatile int*)&S.bad == 0 ? l : NAN);
+            if (fine)
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tc_ld16_issue(tO(s) + lanes + (uint32_t)c, o);
+                    tc_ld16_wait(o);
+                    float f[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        f[k] = __uint_as_float(o[k]) * a;
+                        if (join) f[k] = fmaf(b, xo[(c + k) * kT + row], f[k]);
+                    }
+                    if (x < nx)
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<float4*>(part.o + qr * D + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+                }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(S.tmem, 512);
+}
+
+// [pages * heads * ps][D] bf16, boxes of a page's rows x 64 channels, 128-byte swizzle
+bool page_map(CUtensorMap* m, const void* base, const PagePool& p)
+{
+    EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.pages * p.heads * p.ps};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.D * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)p.ps};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t go(const PagePool& p, const PageRows& r, const int* table, int prefix_len, const PrefixPart& part, cudaStream_t st)
+{
+    CUtensorMap mk, mv;
+    if (!page_map(&mk, p.K, p) || !page_map(&mv, p.V, p)) return cudaErrorInvalidValue;
+    const int per = prefix_tc_range(r.rows, p.heads, r.G, prefix_len);
+    const dim3 grid((unsigned)(((long long)r.rows * r.G + 2 * kT - 1) / (2 * kT)), (unsigned)part.splits, (unsigned)p.heads);
+    const int smem = (int)sizeof(Smem<D>) + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    prefix_tc_kernel<D><<<grid, kThreads, smem, st>>>(mk, mv, p, r, table, prefix_len, per, part);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Keys of each CTA's range, a multiple of 128: the number of ranges that makes
+// the shortest sequence of waves, a CTA costing its key tiles and about two
+// more for its start, its query tiles and its sums.
+int prefix_tc_range(int rows, int heads, int G, int prefix_len)
+{
+    const long long units = ((long long)rows * G + 2 * kT - 1) / (2 * kT) * heads;
+    const int tiles = (prefix_len + kT - 1) / kT;
+    int best = tiles;
+    long long cost = -1;
+    for (int s = 1; s <= std::min(tiles, 64); ++s) {
+        const int each = (tiles + s - 1) / s;
+        const long long ctas = units * ((tiles + each - 1) / each);
+        const long long c = (ctas + kSMs - 1) / kSMs * (each + 2);
+        if (cost < 0 || c < cost) { cost = c; best = each; }
+    }
+    return best * kT;
+}
+
+cudaError_t launch_prefix_tc(const PagePool& p, const PageRows& r, const int* table, int prefix_len, const PrefixPart& part,
+                             cudaStream_t st)
+{
+    return p.D == 64 ? go<64>(p, r, table, prefix_len, part, st) : go<128>(p, r, table, prefix_len, part, st);
+}
+
+}  // namespace h2o
