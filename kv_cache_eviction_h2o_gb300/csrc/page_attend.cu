@@ -11,8 +11,8 @@
 // bounds can have; summing the queries first makes it one product of length
 // 2 D a page whatever G is.  The page ranks are those of the exact s: scores
 // are made in fp32, whose error is at most eps = 2^-18 max_b sum |w||bound|
-// (at most 32 fused multiply-adds a lane, 3 adds, 15 adds in w: 50 roundings
-// of 2^-24), a page more than 2 eps from the k-th largest is decided by that,
+// (32 fused multiply-adds a lane, 3 adds, one rounding of w: 36 roundings of
+// 2^-24, and those of the bound itself), a page more than 2 eps from the k-th largest is decided by that,
 // and the few nearer ones are scored again in fp64 and ranked by that, ties
 // to the lowest page.
 #include <algorithm>
@@ -29,6 +29,7 @@ constexpr int kWarps = 4;              // warps of a CTA
 constexpr int kNT = kWarps * 32;
 constexpr int kKeys = 16;              // keys of a tile (page sizes are its multiples)
 constexpr float kEps = 3.814697e-6f;   // 2^-18
+constexpr int kSMs = 152;
 // tiles in flight per warp
 template <typename T> constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
 
@@ -56,34 +57,43 @@ __device__ __forceinline__ uint32_t tile_at(int row, int byte)
 
 // -------------------------------------------------------------- picking
 
+constexpr int kHold = 16;              // scores a thread keeps in registers (kHold * kNT pages)
+
 struct PickSmem {
-    int warp_i[2][kWarps];
-    unsigned warp_u[2][kWarps];
+    unsigned long long warp[2][kWarps];
     unsigned amax;                     // bits of the largest sum |w||bound| (of the whole cluster)
+    int count[kMaxTableWidth / 32];    // picked pages of each 32
 };
 
-// sum over the CTA, in every thread
-__device__ __forceinline__ int cta_sum(PickSmem& P, int v, int& phase)
+// sum over the CTA, in every thread; halves of 32 bits do not carry
+__device__ __forceinline__ unsigned long long cta_sum(PickSmem& P, unsigned lo, unsigned hi, int& phase)
 {
-    v = __reduce_add_sync(0xffffffffu, v);
+    lo = __reduce_add_sync(0xffffffffu, lo);
+    hi = __reduce_add_sync(0xffffffffu, hi);
     phase ^= 1;
-    if ((threadIdx.x & 31) == 0) P.warp_i[phase][threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) P.warp[phase][threadIdx.x >> 5] = (unsigned long long)hi << 32 | lo;
     __syncthreads();
-    int s = 0;
+    unsigned long long s = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += P.warp_i[phase][w];
+    for (int w = 0; w < kWarps; ++w) s += P.warp[phase][w];
     return s;
 }
-__device__ __forceinline__ unsigned cta_min(PickSmem& P, unsigned v, int& phase)
+// (smallest a, largest b) over the CTA
+__device__ __forceinline__ uint2 cta_range(PickSmem& P, unsigned a, unsigned b, int& phase)
 {
-    v = __reduce_min_sync(0xffffffffu, v);
+    a = __reduce_min_sync(0xffffffffu, a);
+    b = __reduce_max_sync(0xffffffffu, b);
     phase ^= 1;
-    if ((threadIdx.x & 31) == 0) P.warp_u[phase][threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) P.warp[phase][threadIdx.x >> 5] = (unsigned long long)b << 32 | a;
     __syncthreads();
-    unsigned s = ~0u;
+    a = ~0u;
+    b = 0u;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s = min(s, P.warp_u[phase][w]);
-    return s;
+    for (int w = 0; w < kWarps; ++w) {
+        a = min(a, (unsigned)P.warp[phase][w]);
+        b = max(b, (unsigned)(P.warp[phase][w] >> 32));
+    }
+    return make_uint2(a, b);
 }
 
 // order-preserving map of an fp64 value to an unsigned key; NaN above all
@@ -99,6 +109,32 @@ __device__ __forceinline__ float ord_value(unsigned k)
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
+// f(key, j) for this thread's pages j = tid, tid + kNT, ..: from registers where all scores fit them
+struct Held {
+    unsigned k[kHold];
+    const float* s;
+    int n;
+    bool regs;
+    __device__ __forceinline__ Held(const float* s_, int n_) : s(s_), n(n_), regs(n_ <= kHold * kNT)
+    {
+        if (regs)
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+                const int j = (int)threadIdx.x + i * kNT;
+                k[i] = j < n ? ord_key(s[j]) : 0u;         // (0: below every score)
+            }
+    }
+    template <class F> __device__ __forceinline__ void each(F f) const
+    {
+        if (regs) {
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) f(k[i]);
+        } else {
+            for (int j = threadIdx.x; j < n; j += kNT) f(ord_key(s[j]));
+        }
+    }
+};
+
 // Leaves s[j] >= the returned bound exactly for the `take` best of the n
 // pages' scores s (0 < take < n).  `again(j)` is page j's score in fp64, made
 // by a whole warp.  big: room for n keys of 64 bits; s may be overwritten.
@@ -111,36 +147,40 @@ __device__ float pick_bound(PickSmem& P, float* s, int n, int take, unsigned lon
     float above = INFINITY, below = -INFINITY;             // decided: s > above is in, s < below is out
     int in = 0;                                            // pages decided to be in
     if (amax < FLT_MAX) {                                  // (an infinity or NaN among the factors decides nothing)
-        unsigned lo = ~0u, hi = 0u;
-        for (int j = tid; j < n; j += kNT) {
-            const unsigned k = ord_key(s[j]);
-            lo = min(lo, k);
-            hi = max(hi, k);
+        const Held held(s, n);
+        unsigned a = ~0u, b = 0u;
+        held.each([&](unsigned k) { if (k) { a = min(a, k); b = max(b, k); } });
+        const uint2 r = cta_range(P, a, b, ph);
+        // count(key >= lo) >= take > count(key >= hi): three keys between them a step
+        unsigned long long lo = r.x, hi = (unsigned long long)r.y + 1;
+        while (hi - lo > 1) {
+            const unsigned long long gap = hi - lo;
+            const unsigned k1 = (unsigned)(lo + max(1ull, gap / 4)), k2 = (unsigned)(lo + max(1ull, gap / 2)),
+                           k3 = (unsigned)(lo + max(1ull, gap - gap / 4 - (gap < 4 ? 1 : 0)));
+            unsigned c1 = 0, c2 = 0, c3 = 0;
+            held.each([&](unsigned k) { c1 += k >= k1; c2 += k >= k2; c3 += k >= k3; });
+            const unsigned long long c = cta_sum(P, c1 | c2 << 16, c3, ph);
+            const int n1 = (int)(c & 0xffff), n2 = (int)(c >> 16 & 0xffff), n3 = (int)(c >> 32);
+            if (n3 >= take) lo = k3;
+            else if (n2 >= take) { lo = k2; hi = k3; }
+            else if (n1 >= take) { lo = k1; hi = k2; }
+            else hi = k1;
+            if (n1 == take || n2 == take || n3 == take) {
+                lo = n1 == take ? k1 : n2 == take ? k2 : k3;   // just the best: the border lies below the smallest of them
+                break;
+            }
         }
-        lo = cta_min(P, lo, ph);
-        hi = ~cta_min(P, ~hi, ph);
-        // the largest key that `take` keys reach
-        while (lo < hi) {
-            const unsigned mid = lo + (hi - lo) / 2 + 1;
-            int c = 0;
-            for (int j = tid; j < n; j += kNT) c += ord_key(s[j]) >= mid;
-            c = cta_sum(P, c, ph);
-            if (c >= take) lo = mid; else hi = mid - 1;
-            if (c == take) break;
-        }
-        unsigned kth = ~0u;
-        for (int j = tid; j < n; j += kNT) {
-            const unsigned k = ord_key(s[j]);
-            if (k >= lo) kth = min(kth, k);
-        }
-        const float t = ord_value(cta_min(P, kth, ph)), e2 = __fmaf_ru(2.f * kEps, amax, 1e-37f);
+        a = ~0u;                                           // the take-th score
+        held.each([&](unsigned k) { if (k >= lo) a = min(a, k); });
+        const float t = ord_value(cta_range(P, a, 0u, ph).x), e2 = __fmaf_ru(2.f * kEps, amax, 1e-37f);
         above = __fadd_ru(t, e2);
         below = __fadd_rd(t, -e2);
-        int c = 0;                                         // (in, in or open)
-        for (int j = tid; j < n; j += kNT) c += (s[j] > above ? 1 : 0) + (s[j] >= below ? 1 << 16 : 0);
-        c = cta_sum(P, c, ph);
-        in = c & 0xffff;
-        if ((c >> 16) == take) return below;
+        unsigned ci = 0, co = 0;                           // in; in or open
+        const unsigned ka = ord_key(above), kb = ord_key(below);
+        held.each([&](unsigned k) { ci += k > ka; co += k >= kb; });
+        const unsigned long long c = cta_sum(P, ci, co, ph);
+        in = (int)(c & 0xffffffffu);
+        if ((int)(c >> 32) == take) return below;
     }
     // the open pages by their fp64 scores
     for (int j = warp; j < n; j += kWarps) {
@@ -157,17 +197,25 @@ __device__ float pick_bound(PickSmem& P, float* s, int n, int take, unsigned lon
         const unsigned long long mid = lo + (hi - lo) / 2 + 1;
         int c = 0;
         for (int j = tid; j < n; j += kNT) c += big[j] >= mid;
-        if (cta_sum(P, c, ph) >= want) lo = mid; else hi = mid - 1;
+        c = (int)cta_sum(P, (unsigned)c, 0u, ph);
+        if (c >= want) lo = mid; else hi = mid - 1;
+        if (c == want) break;
     }
     int c = 0;
-    for (int j = tid; j < n; j += kNT) c += big[j] > lo;
-    const int ties = want - cta_sum(P, c, ph);             // of the pages with just that key, the first ones
-    int jl = 0, jh = n - 1;                                // the smallest j up to which there are `ties` of them
-    while (jl < jh) {
-        const int mid = (jl + jh) / 2;
+    for (int j = tid; j < n; j += kNT) c += big[j] >= lo;
+    int jl = n;                                            // pages of just the key lo are in up to jl
+    if ((int)cta_sum(P, (unsigned)c, 0u, ph) != want) {
         c = 0;
-        for (int j = tid; j <= mid; j += kNT) c += big[j] == lo;
-        if (cta_sum(P, c, ph) >= ties) jh = mid; else jl = mid + 1;
+        for (int j = tid; j < n; j += kNT) c += big[j] > lo;
+        const int ties = want - (int)cta_sum(P, (unsigned)c, 0u, ph);
+        jl = 0;
+        int jh = n - 1;                                    // the smallest j up to which there are `ties` of them
+        while (jl < jh) {
+            const int mid = (jl + jh) / 2;
+            c = 0;
+            for (int j = tid; j <= mid; j += kNT) c += big[j] == lo;
+            if ((int)cta_sum(P, (unsigned)c, 0u, ph) >= ties) jh = mid; else jl = mid + 1;
+        }
     }
     for (int j = tid; j < n; j += kNT) {
         const unsigned long long k = big[j];
@@ -185,10 +233,17 @@ __device__ float pick_bound(PickSmem& P, float* s, int n, int take, unsigned lon
 template <typename T, int D, int GP>
 struct CoreSimt {
     static constexpr int E = D / 32;
+    struct Shared {
+        float q[GP * D];
+        float p[kWarps][GP * kKeys];
+    };
     float o[GP][E], m[GP], l[GP];
 
-    __device__ __forceinline__ void init()
+    // qrow: the G queries; the whole CTA calls it
+    __device__ __forceinline__ void init(Shared& S, const T* qrow, int G)
     {
+        for (int i = threadIdx.x; i < GP * D; i += kNT) S.q[i] = i < G * D ? Elem<T>::to_f(qrow[i]) : 0.f;
+        __syncthreads();
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             m[g] = -INFINITY;
@@ -198,9 +253,11 @@ struct CoreSimt {
         }
     }
 
-    __device__ __forceinline__ void tile(const unsigned char* kt, const unsigned char* vt, int valid, const float* q,
-                                         float* pb, float qscale, int lane)
+    __device__ __forceinline__ void tile(const unsigned char* kt, const unsigned char* vt, int valid, Shared& S, float qscale,
+                                         int lane, int G)
     {
+        const float* q = S.q;
+        float* pb = S.p[threadIdx.x >> 5];
         constexpr int N = 16 / sizeof(T);
         const int key = lane & 15, half = lane >> 4;
         float z[GP];
@@ -266,15 +323,139 @@ struct CoreSimt {
         __syncwarp();
     }
 
-    // o to out [GP][D], (m, l) to ml [GP]
-    __device__ __forceinline__ void finish(float* out, float2* ml, int lane, bool bad)
+    // o to out [G][D], (m, l) to ml [G]
+    __device__ __forceinline__ void finish(float* out, float2* ml, int lane, int G, bool bad)
     {
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             const float s = warp_sum(l[g]);
+            if (g >= G) continue;
 #pragma unroll
             for (int e = 0; e < E; ++e) out[g * D + lane * E + e] = o[g][e];
             if (lane == 0) ml[g] = make_float2(m[g], bad ? NAN : s);
+        }
+    }
+};
+
+// The same on the tensor cores (bf16): the G queries are the rows of 16-row
+// products, S = Q K^T with 16 keys and O += P V with P from S's registers.
+// 32 products of 16 x 8 x 16 a tile, a small part of the time its 4 KB of
+// keys and 4 KB of values (head_dim 128) take to arrive; tcgen05's 128 rows
+// would be seven eighths padding here.  P is rounded to bf16 (2^-9 relative a
+// weight, as the output is); l sums the unrounded weights.  The maximum is
+// raised only when a logit passes it by 2^8.
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+struct CoreMma {
+    using T = __nv_bfloat16;
+    struct Shared {};
+    static constexpr float kRaise = 8.f;
+    uint32_t q[D / 16][4];
+    float o[D / 8][4], m[2], l[2];     // rows lane / 4 and lane / 4 + 8
+
+    __device__ __forceinline__ void init(Shared&, const T* qrow, int G)
+    {
+        const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
+        const uint32_t* p0 = reinterpret_cast<const uint32_t*>(qrow + (size_t)r * D + c);
+        const uint32_t* p1 = p0 + 4 * D;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            q[k][0] = r < G ? p0[k * 8] : 0u;
+            q[k][1] = r + 8 < G ? p1[k * 8] : 0u;
+            q[k][2] = r < G ? p0[k * 8 + 4] : 0u;
+            q[k][3] = r + 8 < G ? p1[k * 8 + 4] : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+
+    __device__ __forceinline__ void tile(const unsigned char* kt, const unsigned char* vt, int valid, Shared&, float qscale, int lane, int G)
+    {
+        const int mat = lane >> 3, r8 = lane & 7;
+        float z[2][4] = {};
+        const uint32_t ka = smem_u32(kt) + (uint32_t)((mat >> 1) * 8 + r8) * (D * 2);
+        const uint32_t va = smem_u32(vt) + (uint32_t)((mat & 1) * 8 + r8) * (D * 2);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t b[4];
+            ldsm4(b, ka + (uint32_t)(((k * 2 + (mat & 1)) ^ r8) << 4));
+            mma16816(z[0], q[k], b[0], b[1]);
+            mma16816(z[1], q[k], b[2], b[3]);
+        }
+        if (valid < kKeys) {
+            const int c = (lane & 3) * 2;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i * 8 + c + (e & 1) >= valid) z[i][e] = -INFINITY;
+        }
+        uint32_t p[4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            p[x] = p[x + 2] = 0u;
+            if (x == 1 && G <= 8) break;                   // rows of padding
+            float t = fmaxf(fmaxf(z[0][2 * x], z[0][2 * x + 1]), fmaxf(z[1][2 * x], z[1][2 * x + 1]));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2)) * qscale;
+            const bool raise = t > m[x] + kRaise;
+            if (__any_sync(0xffffffffu, raise)) {
+                const float a = raise ? ex2_approx(m[x] - t) : 1.f;
+                if (raise) m[x] = t;
+                l[x] *= a;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][2 * x] *= a;
+                    o[i][2 * x + 1] *= a;
+                }
+            }
+            const float base = m[x] == -INFINITY ? 0.f : m[x];
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaf(z[i >> 1][2 * x + (i & 1)], qscale, -base));
+            l[x] += (e[0] + e[1]) + (e[2] + e[3]);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[x]) : "f"(e[1]), "f"(e[0]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[x + 2]) : "f"(e[3]), "f"(e[2]));
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t b[4];
+            ldsm4_t(b, va + (uint32_t)(((k * 2 + (mat >> 1)) ^ r8) << 4));
+            mma16816(o[2 * k], p, b[0], b[1]);
+            mma16816(o[2 * k + 1], p, b[2], b[3]);
+        }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void finish(float* out, float2* ml, int lane, int G, bool bad)
+    {
+        const int r = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float s = l[x];
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            const int g = r + 8 * x;
+            if (g >= G) continue;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(out + g * D + i * 8 + c) = make_float2(o[i][2 * x], o[i][2 * x + 1]);
+            if ((lane & 3) == 0) ml[g] = make_float2(m[x], bad ? NAN : s);
         }
     }
 };
@@ -283,14 +464,12 @@ template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-template <typename T, int D, int GP>
+template <int D, class Core>
 struct alignas(16) AttendSmem {
     double w64[2 * D];                 // the page weights, minima's then maxima's
-    float w[2 * D];
-    float q[GP * D];                   // the queries; later this CTA's sum of values
-    float p[kWarps][GP * kKeys];
-    float2 wml[kWarps][GP];
-    float2 ml[GP];
+    typename Core::Shared core;
+    float2 wml[kWarps][kMaxPageGroups];
+    float2 ml[kMaxPageGroups];
     PickSmem pick;
 };
 
@@ -299,13 +478,14 @@ struct alignas(16) AttendSmem {
 template <typename T, int D> constexpr int kTileBytes = kKeys * D * (int)sizeof(T);
 template <typename T, int D> constexpr int kRingBytes = kStages<T> * 2 * kTileBytes<T, D>;   // a warp's
 
-template <typename T, int D, int GP>
-__global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, const PageRows R, const int budget,
-                                                          const int recent, int* __restrict__ picked,
-                                                          const PrefixPart part, const int front, const int wpad)
+// Two CTAs an SM (bf16): while one ranks its pages the other reads keys.
+template <typename T, int D, class Core>
+__global__ void __launch_bounds__(kNT, sizeof(T) == 2 ? 2 : 1)
+    page_attend_kernel(const PagePool pool, const PageRows R, const int budget, const int recent, int* __restrict__ picked,
+                       const PrefixPart part, const int front, const int wpad)
 {
     extern __shared__ __align__(128) unsigned char raw[];
-    using S_t = AttendSmem<T, D, GP>;
+    using S_t = AttendSmem<D, Core>;
     constexpr int NS = kStages<T>, TB = kTileBytes<T, D>;
     S_t& S = *reinterpret_cast<S_t*>(raw + front);
     float* scores = reinterpret_cast<float*>(raw + front + sizeof(S_t));
@@ -315,9 +495,8 @@ __global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
     const int u = blockIdx.x / C, row = u / pool.heads, h = u - row * pool.heads;
-    const int seq = R.seq[row];
+    const int seq = R.seq[row], pos = R.pos[row];
     if (seq < 0) return;                                   // a row that is not there, for the whole cluster
-    const int pos = R.pos[row];
     const int sh = __ffs(pool.ps) - 1;
     const int G = R.G;
     int npages = pos < 0 ? 0 : (pos >> sh) + 1;
@@ -325,111 +504,140 @@ __global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, c
     if (bad) npages = 0;
     const int* table = R.table + (size_t)(bad ? 0 : seq) * R.width;
     const T* qrow = static_cast<const T*>(R.q) + (size_t)row * R.q_stride + (size_t)h * G * D;
-    for (int i = tid; i < GP * D; i += kNT) S.q[i] = i < G * D ? Elem<T>::to_f(qrow[i]) : 0.f;
-    if (tid == 0) S.pick.amax = 0u;
-    __syncthreads();
 
     int nlist = npages;
     const int* src = table;                                // physical page of each entry
     const int ncand = npages - recent, take = budget - recent;
     if (budget > 0 && npages > budget) {
-        for (int i = tid; i < 2 * D; i += kNT) {
-            double s = 0.0;
-            float f = 0.f;
-            const bool lo = i < D;
-            for (int g = 0; g < G; ++g) {
-                const float x = S.q[g * D + (lo ? i : i - D)];
-                const float y = lo ? (x < 0.f || x != x ? x : 0.f) : (x > 0.f || x != x ? x : 0.f);
-                s += (double)y;
-                f += y;
+        int* pick_out = picked && rank == 0 ? picked + (size_t)u * budget : nullptr;
+        if (take > 0) {                                    // (else the newest pages are all)
+            if (tid == 0) S.pick.amax = 0u;
+            for (int i = tid; i < 2 * D; i += kNT) {
+                double s = 0.0;
+                const bool lo = i < D;
+                for (int g = 0; g < G; ++g) {
+                    const float x = Elem<T>::to_f(qrow[g * D + (lo ? i : i - D)]);
+                    s += (double)(lo ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x));
+                }
+                S.w64[i] = s;
             }
-            S.w64[i] = s;
-            S.w[i] = f;
-        }
-        __syncthreads();
-        cluster_arrive();
-        cluster_wait();                                    // every CTA has set its maximum
-        constexpr int N = 16 / sizeof(T), NV = 2 * D / 8 / N;
-        const T* bounds = static_cast<const T*>(pool.bounds);
-        // eight lanes a page, four pages a warp
-        float w[NV][N];
-        const int sub = lane & 7;
+            __syncthreads();
+            cluster_arrive();
+            constexpr int N = 16 / sizeof(T), NV = 2 * D / 8 / N;
+            constexpr int UN = sizeof(T) == 2 ? 4 : 2;         // pages a lane has in flight
+            const T* bounds = static_cast<const T*>(pool.bounds);
+            // eight lanes a page
+            float w[NV][N];
+            const int sub = lane & 7;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < N; ++e) w[i][e] = S.w[(i * 8 + sub) * N + e];
-        unsigned amax = 0u;
-        for (int j0 = (rank * kWarps + warp) * 4; j0 < ncand; j0 += C * kWarps * 4) {
-            const int j = j0 + (lane >> 3);
-            const int pg = j < ncand ? table[j] : 0;
-            const bool ok = (unsigned)pg < (unsigned)pool.pages;
-            const T* b = bounds + ((size_t)(ok ? pg : 0) * pool.heads + h) * 2 * D;
-            float s = 0.f, a = 0.f;
+                for (int e = 0; e < N; ++e) w[i][e] = (float)S.w64[(i * 8 + sub) * N + e];
+            unsigned amax = 0u;
+            const int step = C * kWarps * 4 * UN;
+            int pg[UN];
+            auto pages_of = [&](int j0) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float x[N];
-                load_vec<T, N>(b + (i * 8 + sub) * N, x);
+                for (int x = 0; x < UN; ++x) {
+                    const int j = j0 + x * 4 + (lane >> 3);
+                    pg[x] = j < ncand ? table[j] : 0;
+                }
+            };
+            int j0 = (rank * kWarps + warp) * 4 * UN;
+            pages_of(j0);
+            cluster_wait();                                    // every CTA has set its maximum
+            for (; j0 < ncand; j0 += step) {
+                uint4 v[UN][NV];
+                bool ok[UN];
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    s = fmaf(w[i][e], x[e], s);
-                    a = fmaf(fabsf(w[i][e]), fabsf(x[e]), a);
+                for (int x = 0; x < UN; ++x) {
+                    ok[x] = (unsigned)pg[x] < (unsigned)pool.pages;
+                    const T* b = bounds + ((size_t)(ok[x] ? pg[x] : 0) * pool.heads + h) * 2 * D;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) v[x][i] = *reinterpret_cast<const uint4*>(b + (i * 8 + sub) * N);
+                }
+                pages_of(j0 + step);
+#pragma unroll
+                for (int x = 0; x < UN; ++x) {
+                    float s = 0.f, a = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        float f[N];
+                        load_vec<T, N>(reinterpret_cast<const T*>(&v[x][i]), f);
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            s = fmaf(w[i][e], f[e], s);
+                            a = fmaf(fabsf(w[i][e]), fabsf(f[e]), a);
+                        }
+                    }
+#pragma unroll
+                    for (int d = 4; d > 0; d >>= 1) {
+                        s += __shfl_xor_sync(0xffffffffu, s, d);
+                        a += __shfl_xor_sync(0xffffffffu, a, d);
+                    }
+                    if (!ok[x]) { s = NAN; a = NAN; }          // no such page: picked, and its row is NaN
+                    const int j = j0 + x * 4 + (lane >> 3);
+                    if (j < ncand) {
+                        amax = max(amax, __float_as_uint(fabsf(a)));
+                        for (int c = sub; c < C; c += 8) st_cluster_f32(map_to_rank(scores + j, c), s);
+                    }
                 }
             }
+            amax = __reduce_max_sync(0xffffffffu, amax);
+            if (lane < C) cluster_max_u32(map_to_rank(&S.pick.amax, lane), amax);
+            cluster_arrive();
+            cluster_wait();
+            const float bound = pick_bound(S.pick, scores, ncand, take, big, [&](int j) {
+                const int p = table[j];
+                if ((unsigned)p >= (unsigned)pool.pages) return (double)NAN;
+                const T* b = bounds + ((size_t)p * pool.heads + h) * 2 * D;
+                double s = 0.0;
+                if (__uint_as_float(S.pick.amax) < FLT_MAX) {
+                    for (int e = lane; e < 2 * D; e += 32) s += S.w64[e] * (double)Elem<T>::to_f(b[e]);
+                } else {
+                    // an infinite bound on the side that no query takes counts for nothing: the maxima themselves
+                    for (int e = lane; e < D; e += 32)
+                        for (int g = 0; g < G; ++g) {
+                            const double x = Elem<T>::to_f(qrow[g * D + e]);
+                            const double y0 = x * (double)Elem<T>::to_f(b[e]), y1 = x * (double)Elem<T>::to_f(b[D + e]);
+                            s += y0 != y0 || y1 != y1 ? (double)NAN : fmax(y0, y1);
+                        }
+                }
+                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                return s;
+            });
+            // the picked pages in order: counts of each 32, their running sums, places
+            const int n32 = (ncand + 31) >> 5;
+            for (int i = warp; i < n32; i += kWarps) {
+                const int j = i * 32 + lane;
+                const unsigned in = __ballot_sync(0xffffffffu, j < ncand && scores[j] >= bound);
+                if (lane == 0) S.pick.count[i] = __popc(in);
+            }
+            __syncthreads();
+            if (warp == 0)
+                for (int i0 = 0, sum = 0; i0 < n32; i0 += 32) {
+                    const int c = i0 + lane < n32 ? S.pick.count[i0 + lane] : 0;
+                    int x = c;
 #pragma unroll
-            for (int d = 4; d > 0; d >>= 1) {
-                s += __shfl_xor_sync(0xffffffffu, s, d);
-                a += __shfl_xor_sync(0xffffffffu, a, d);
-            }
-            if (!ok) { s = NAN; a = NAN; }                 // no such page: picked, and its row is NaN
-            if (j < ncand) {
-                amax = max(amax, __float_as_uint(fabsf(a)));
-                for (int c = sub; c < C; c += 8) st_cluster_f32(map_to_rank(scores + j, c), s);
-            }
-        }
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        if (lane < C) cluster_max_u32(map_to_rank(&S.pick.amax, lane), amax);
-        cluster_arrive();
-        cluster_wait();
-        const float bound = pick_bound(S.pick, scores, ncand, take, big, [&](int j) {
-            const int pg = table[j];
-            if ((unsigned)pg >= (unsigned)pool.pages) return (double)NAN;
-            const T* b = bounds + ((size_t)pg * pool.heads + h) * 2 * D;
-            double s = 0.0;
-            if (__uint_as_float(S.pick.amax) < FLT_MAX) {
-                for (int e = lane; e < 2 * D; e += 32) s += S.w64[e] * (double)Elem<T>::to_f(b[e]);
-            } else {
-                // an infinite bound on the side that no query takes counts for nothing: the maxima themselves
-                for (int e = lane; e < D; e += 32)
-                    for (int g = 0; g < G; ++g) {
-                        const double x = S.q[g * D + e], y0 = x * (double)Elem<T>::to_f(b[e]), y1 = x * (double)Elem<T>::to_f(b[D + e]);
-                        s += y0 != y0 || y1 != y1 ? (double)NAN : fmax(y0, y1);
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, x, d);
+                        if (lane >= d) x += y;
                     }
+                    if (i0 + lane < n32) S.pick.count[i0 + lane] = sum + x - c;
+                    sum += __shfl_sync(0xffffffffu, x, 31);
+                }
+            __syncthreads();
+            for (int i = warp; i < n32; i += kWarps) {
+                const int j = i * 32 + lane;
+                const bool is_in = j < ncand && scores[j] >= bound;
+                const unsigned in = __ballot_sync(0xffffffffu, is_in);
+                if (is_in) {
+                    const int at = S.pick.count[i] + __popc(in & ((1u << lane) - 1u));
+                    list[at] = table[j];
+                    if (pick_out) pick_out[at] = j;
+                }
             }
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            return s;
-        });
-        // the picked pages in order: each thread takes a run of pages
-        const int per = (ncand + kNT - 1) / kNT, j0 = min(ncand, tid * per), j1 = min(ncand, j0 + per);
-        int c = 0;
-        for (int j = j0; j < j1; ++j) c += scores[j] >= bound;
-        int before = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, before, d);
-            if (lane >= d) before += x;
         }
-        __syncthreads();
-        if (lane == 31) S.pick.warp_i[0][warp] = before;
-        __syncthreads();
-        before -= c;
-        for (int k = 0; k < warp; ++k) before += S.pick.warp_i[0][k];
-        int* pick_out = picked && rank == 0 ? picked + (size_t)u * budget : nullptr;
-        for (int j = j0; j < j1; ++j)
-            if (scores[j] >= bound) {
-                list[before] = table[j];
-                if (pick_out) pick_out[before] = j;
-                ++before;
-            }
         for (int j = tid; j < recent; j += kNT) {
             list[take + j] = table[ncand + j];
             if (pick_out) pick_out[take + j] = ncand + j;
@@ -446,8 +654,6 @@ __global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, c
     const int ntiles = nlist ? ((nlist - 1) << tsh) + ((pos & (pool.ps - 1)) >> 4) + 1 : 0;
     const int stride = C * kWarps;
     const int t0 = rank * kWarps + warp;
-    CoreSimt<T, D, GP> core;
-    core.init();
     const T* K = static_cast<const T*>(pool.K);
     const T* V = static_cast<const T*>(pool.V);
     auto valid_of = [&](int t) {                           // keys of tile t up to pos
@@ -467,7 +673,7 @@ __global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, c
             for (int i = lane; i < kKeys * CH; i += 32) {
                 const int r = i / CH, c = i % CH;
                 const bool fill = r < valid;               // keys past the newest are not read: zeros
-                const size_t o = off + (fill ? (size_t)r * D + c * (16 / sizeof(T)) : 0);
+                const size_t o = off + (fill ? r * D + c * (16 / (int)sizeof(T)) : 0);
                 cp_async16(kd + tile_at<T, D>(r, c * 16), K + o, fill);
                 cp_async16(vd + tile_at<T, D>(r, c * 16), V + o, fill);
             }
@@ -477,23 +683,26 @@ __global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, c
     };
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) ask(t0 + s * stride, s);
+    Core core;
+    core.init(S.core, qrow, G);
     int stage = 0;
     for (int t = t0; t < ntiles; t += stride) {
         ask(t + (NS - 1) * stride, stage == 0 ? NS - 1 : stage - 1);
         cp_wait<NS - 1>();
         __syncwarp();
-        core.tile(ring + 2 * stage * TB, ring + 2 * stage * TB + TB, valid_of(t), S.q, S.p[warp], R.qscale, lane);
+        core.tile(ring + 2 * stage * TB, ring + 2 * stage * TB + TB, valid_of(t), S.core, R.qscale, lane, G);
         stage = stage + 1 == NS ? 0 : stage + 1;
     }
     cp_wait<0>();
     __syncwarp();
 
     // the warps' sums, then the CTAs', then the prefix's
-    float* wo = reinterpret_cast<float*>(ring);
-    static_assert(kRingBytes<T, D> >= (int)sizeof(float) * GP * D, "a warp's sums lie in its ring");
-    core.finish(wo, S.wml[warp], lane, bad);
+    constexpr int kSums = (int)sizeof(float) * kMaxPageGroups * D;
+    static_assert(kRingBytes<T, D> >= 2 * kSums, "a warp's sums and the CTA's lie in a ring");
+    core.finish(reinterpret_cast<float*>(ring), S.wml[warp], lane, G, bad);
     __syncthreads();
-    for (int i = tid; i < GP * D; i += kNT) {
+    float* sums = reinterpret_cast<float*>(raw + kSums);
+    for (int i = tid; i < G * D; i += kNT) {
         const int g = i / D;
         float m = -INFINITY, l = 0.f, o = 0.f;
 #pragma unroll
@@ -505,7 +714,7 @@ __global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, c
             l += a * S.wml[w][g].y;
             o = fmaf(a, reinterpret_cast<const float*>(raw + w * kRingBytes<T, D>)[i], o);
         }
-        S.q[i] = o;
+        sums[i] = o;
         if (i % D == 0) S.ml[g] = make_float2(m, l);
     }
     cluster_arrive();
@@ -521,8 +730,9 @@ __global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, c
         for (int c = 0; c < C; ++c) {
             const float a = ex2_approx(ld_cluster_f32(map_to_rank(&S.ml[g].x, c)) - base);
             l += a * ld_cluster_f32(map_to_rank(&S.ml[g].y, c));
-            o = fmaf(a, ld_cluster_f32(map_to_rank(&S.q[i], c)), o);
+            o = fmaf(a, ld_cluster_f32(map_to_rank(&sums[i], c)), o);
         }
+#pragma unroll 4
         for (int s = 0; s < part.splits; ++s) {
             const float2 x = part.ml[s * qrows + qr + g];
             const float a = ex2_approx(x.x - base);
@@ -536,23 +746,32 @@ __global__ void __launch_bounds__(kNT) page_attend_kernel(const PagePool pool, c
     cluster_wait();                                        // no CTA leaves while another reads its sums
 }
 
-template <typename T, int D, int GP>
+// CTAs of a unit.
+int cluster_of(long long units, int tiles, int resident)
+{
+    int c = 1;
+    while (c < 8 && units * c * 2 <= resident && tiles >= 2 * c * 2 * kWarps) c *= 2;
+    return c;
+}
+
+template <typename T, int D, class Core>
 cudaError_t go(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
 {
     const bool picks = budget > 0 && budget < r.width;
     const int wpad = picks ? (r.width + 3) & ~3 : 0;
     const int front = std::max(kWarps * kRingBytes<T, D>, 8 * wpad);
-    const size_t smem = front + sizeof(AttendSmem<T, D, GP>) + 4 * ((size_t)wpad + (picks ? budget : 0));
-    const auto kernel = page_attend_kernel<T, D, GP>;
+    const size_t smem = front + sizeof(AttendSmem<D, Core>) + 4 * ((size_t)wpad + (picks ? budget : 0));
+    const auto kernel = page_attend_kernel<T, D, Core>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int C = 1;
+    const long long units = (long long)r.rows * p.heads;
+    const int C = cluster_of(units, (picks ? budget : r.width) * (p.ps / kKeys), (smem <= 113 * 1024 ? 2 : 1) * kSMs);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)C;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)r.rows * p.heads * C));
+    cfg.gridDim = dim3((unsigned)(units * C));
     cfg.blockDim = dim3(kNT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -561,13 +780,14 @@ cudaError_t go(const PagePool& p, const PageRows& r, int budget, int recent, int
     return cudaLaunchKernelEx(&cfg, kernel, p, r, budget, recent, picked, part, front, wpad);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t by_groups(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
 {
-    if (r.G == 1) return go<T, D, 1>(p, r, budget, recent, picked, part, st);
-    if (r.G <= 4) return go<T, D, 4>(p, r, budget, recent, picked, part, st);
-    if (r.G <= 8) return go<T, D, 8>(p, r, budget, recent, picked, part, st);
-    return go<T, D, 16>(p, r, budget, recent, picked, part, st);
+    if (p.dtype) return go<__nv_bfloat16, D, CoreMma<D>>(p, r, budget, recent, picked, part, st);
+    if (r.G == 1) return go<float, D, CoreSimt<float, D, 1>>(p, r, budget, recent, picked, part, st);
+    if (r.G <= 4) return go<float, D, CoreSimt<float, D, 4>>(p, r, budget, recent, picked, part, st);
+    if (r.G <= 8) return go<float, D, CoreSimt<float, D, 8>>(p, r, budget, recent, picked, part, st);
+    return go<float, D, CoreSimt<float, D, 16>>(p, r, budget, recent, picked, part, st);
 }
 
 }  // namespace
@@ -575,11 +795,7 @@ cudaError_t by_groups(const PagePool& p, const PageRows& r, int budget, int rece
 cudaError_t launch_page_attend(const PagePool& p, const PageRows& r, int budget, int recent, int* picked,
                                const PrefixPart& part, cudaStream_t st)
 {
-    if (p.dtype)
-        return p.D == 64 ? by_groups<__nv_bfloat16, 64>(p, r, budget, recent, picked, part, st)
-                         : by_groups<__nv_bfloat16, 128>(p, r, budget, recent, picked, part, st);
-    return p.D == 64 ? by_groups<float, 64>(p, r, budget, recent, picked, part, st)
-                     : by_groups<float, 128>(p, r, budget, recent, picked, part, st);
+    return p.D == 64 ? by_groups<64>(p, r, budget, recent, picked, part, st) : by_groups<128>(p, r, budget, recent, picked, part, st);
 }
 
 }  // namespace h2o

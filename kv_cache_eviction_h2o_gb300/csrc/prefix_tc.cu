@@ -372,22 +372,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool fine = __all_sync(0xffffffffu, ok && all && *(volatile int*)&S.abort == 0);
             const size_t qr = ((size_t)blockIdx.y * R.rows * pool.heads + (size_t)(x / G) * pool.heads + h) * G + x % G;
             if (x < nx) part.ml[qr] = make_float2(m, fine && *(volatile int*)&S.bad == 0 ? l : NAN);
+            // half the channels at a time through this warp's part of the query tiles (every score is made by now), so
+            // that rows are written whole: 16-byte chunk c of row r at chunk c ^ (r % chunks)
+            constexpr int W = D / 2, CH = W / 4;
+            float4* stage = reinterpret_cast<float4*>(S.q[0]) + ((two ? s * 4 : 0) + w) * (32 * CH);
             if (fine)
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    tc_ld16_issue(tO(s) + lanes + (uint32_t)c, o);
-                    tc_ld16_wait(o);
-                    float f[16];
+                for (int d0 = 0; d0 < D; d0 += W) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        f[k] = __uint_as_float(o[k]) * a;
-                        if (join) f[k] = fmaf(b, xo[(c + k) * kT + row], f[k]);
-                    }
-                    if (x < nx)
+                    for (int c = 0; c < W; c += 16) {
+                        uint32_t o[16];
+                        tc_ld16_issue(tO(s) + lanes + (uint32_t)(d0 + c), o);
+                        tc_ld16_wait(o);
+                        float f[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            f[k] = __uint_as_float(o[k]) * a;
+                            if (join) f[k] = fmaf(b, xo[(d0 + c + k) * kT + row], f[k]);
+                        }
 #pragma unroll
                         for (int k = 0; k < 16; k += 4)
-                            *reinterpret_cast<float4*>(part.o + qr * D + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+                            stage[lane * CH + (((c + k) / 4) ^ (lane & (CH - 1)))] = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int r = lane / CH; r < 32; r += 32 / CH) {
+                        const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)qr, r);
+                        if (x - lane + r < nx)
+                            *reinterpret_cast<float4*>(part.o + to * D + d0 + (lane % CH) * 4) = stage[r * CH + ((lane % CH) ^ (r & (CH - 1)))];
+                    }
+                    __syncwarp();
                 }
         }
     }
