@@ -10,13 +10,14 @@
 // is the sum over the heads of the largest q_g . k that a key within page b's
 // bounds can have; summing the queries first makes it one product of length
 // 2 D a page whatever G is.  The page ranks are those of the exact s: scores
-// are made in fp32, whose error is at most eps = 2^-18 max_b sum |w||bound|
-// (32 fused multiply-adds a lane, 3 adds, one rounding of w: 36 roundings of
-// 2^-24, and those of the bound itself), a page more than 2 eps from the k-th largest is decided by that,
+// are made in fp32, whose error is at most eps = 24 * 2^-24 max_b sum |w||bound|
+// (two chains of 16 fused multiply-adds a lane, 4 adds, one rounding of w: 21
+// roundings; the bound's own are far below the rest), a page more than 2 eps from the k-th largest is decided by that,
 // and the few nearer ones are scored again in fp64 and ranked by that, ties
 // to the lowest page.
 #include <algorithm>
 #include <cfloat>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "paged.h"
@@ -25,10 +26,8 @@ namespace h2o {
 
 namespace {
 
-constexpr int kWarps = 4;              // warps of a CTA
-constexpr int kNT = kWarps * 32;
 constexpr int kKeys = 16;              // keys of a tile (page sizes are its multiples)
-constexpr float kEps = 3.814697e-6f;   // 2^-18
+constexpr float kEps = 1.4305115e-6f;  // 24 * 2^-24
 constexpr int kSMs = 152;
 // tiles in flight per warp
 template <typename T> constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
@@ -57,16 +56,22 @@ __device__ __forceinline__ uint32_t tile_at(int row, int byte)
 
 // -------------------------------------------------------------- picking
 
-constexpr int kHold = 16;              // scores a thread keeps in registers (kHold * kNT pages)
+constexpr int kHold = 16;              // scores a thread keeps in registers
+constexpr int kFew = 32;               // open pages that are ranked one against another
 
+template <int NW>
 struct PickSmem {
-    unsigned long long warp[2][kWarps];
+    unsigned long long warp[2][NW];
+    unsigned long long key[kFew];      // the open pages' fp64 scores, and which they are
+    int at[kFew];
+    int n_open;
     unsigned amax;                     // bits of the largest sum |w||bound| (of the whole cluster)
     int count[kMaxTableWidth / 32];    // picked pages of each 32
 };
 
 // sum over the CTA, in every thread; halves of 32 bits do not carry
-__device__ __forceinline__ unsigned long long cta_sum(PickSmem& P, unsigned lo, unsigned hi, int& phase)
+template <int NW>
+__device__ __forceinline__ unsigned long long cta_sum(PickSmem<NW>& P, unsigned lo, unsigned hi, int& phase)
 {
     lo = __reduce_add_sync(0xffffffffu, lo);
     hi = __reduce_add_sync(0xffffffffu, hi);
@@ -75,11 +80,12 @@ __device__ __forceinline__ unsigned long long cta_sum(PickSmem& P, unsigned lo, 
     __syncthreads();
     unsigned long long s = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += P.warp[phase][w];
+    for (int w = 0; w < NW; ++w) s += P.warp[phase][w];
     return s;
 }
 // (smallest a, largest b) over the CTA
-__device__ __forceinline__ uint2 cta_range(PickSmem& P, unsigned a, unsigned b, int& phase)
+template <int NW>
+__device__ __forceinline__ uint2 cta_range(PickSmem<NW>& P, unsigned a, unsigned b, int& phase)
 {
     a = __reduce_min_sync(0xffffffffu, a);
     b = __reduce_max_sync(0xffffffffu, b);
@@ -89,7 +95,7 @@ __device__ __forceinline__ uint2 cta_range(PickSmem& P, unsigned a, unsigned b, 
     a = ~0u;
     b = 0u;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < NW; ++w) {
         a = min(a, (unsigned)P.warp[phase][w]);
         b = max(b, (unsigned)(P.warp[phase][w] >> 32));
     }
@@ -109,18 +115,19 @@ __device__ __forceinline__ float ord_value(unsigned k)
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// f(key, j) for this thread's pages j = tid, tid + kNT, ..: from registers where all scores fit them
+// f(key) for this thread's pages j = tid, tid + NT, ..: from registers where all scores fit them
+template <int NT>
 struct Held {
     unsigned k[kHold];
     const float* s;
     int n;
     bool regs;
-    __device__ __forceinline__ Held(const float* s_, int n_) : s(s_), n(n_), regs(n_ <= kHold * kNT)
+    __device__ __forceinline__ Held(const float* s_, int n_) : s(s_), n(n_), regs(n_ <= kHold * NT)
     {
         if (regs)
 #pragma unroll
             for (int i = 0; i < kHold; ++i) {
-                const int j = (int)threadIdx.x + i * kNT;
+                const int j = (int)threadIdx.x + i * NT;
                 k[i] = j < n ? ord_key(s[j]) : 0u;         // (0: below every score)
             }
     }
@@ -130,7 +137,7 @@ struct Held {
 #pragma unroll
             for (int i = 0; i < kHold; ++i) f(k[i]);
         } else {
-            for (int j = threadIdx.x; j < n; j += kNT) f(ord_key(s[j]));
+            for (int j = threadIdx.x; j < n; j += NT) f(ord_key(s[j]));
         }
     }
 };
@@ -138,16 +145,17 @@ struct Held {
 // Leaves s[j] >= the returned bound exactly for the `take` best of the n
 // pages' scores s (0 < take < n).  `again(j)` is page j's score in fp64, made
 // by a whole warp.  big: room for n keys of 64 bits; s may be overwritten.
-template <class Again>
-__device__ float pick_bound(PickSmem& P, float* s, int n, int take, unsigned long long* big, Again again)
+template <int NW, class Again>
+__device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned long long* big, Again again)
 {
+    constexpr int NT = NW * 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int ph = 0;
     const float amax = __uint_as_float(P.amax);
     float above = INFINITY, below = -INFINITY;             // decided: s > above is in, s < below is out
     int in = 0;                                            // pages decided to be in
     if (amax < FLT_MAX) {                                  // (an infinity or NaN among the factors decides nothing)
-        const Held held(s, n);
+        const Held<NT> held(s, n);
         unsigned a = ~0u, b = 0u;
         held.each([&](unsigned k) { if (k) { a = min(a, k); b = max(b, k); } });
         const uint2 r = cta_range(P, a, b, ph);
@@ -181,9 +189,31 @@ __device__ float pick_bound(PickSmem& P, float* s, int n, int take, unsigned lon
         const unsigned long long c = cta_sum(P, ci, co, ph);
         in = (int)(c & 0xffffffffu);
         if ((int)(c >> 32) == take) return below;
+        const int open = (int)(c >> 32) - in;
+        if (open <= kFew) {
+            // a few: their fp64 scores, each compared with every other
+            if (tid == 0) P.n_open = 0;
+            __syncthreads();
+            for (int j = tid; j < n; j += NT)
+                if (s[j] <= above && s[j] >= below) P.at[atomicAdd(&P.n_open, 1)] = j;
+            __syncthreads();
+            for (int i = warp; i < open; i += NW) {
+                const unsigned long long k = ord_key64(again(P.at[i]));
+                if (lane == 0) P.key[i] = k;
+            }
+            __syncthreads();
+            if (tid < open) {
+                int better = 0;
+                for (int i = 0; i < open; ++i)
+                    better += P.key[i] > P.key[tid] || (P.key[i] == P.key[tid] && P.at[i] < P.at[tid]);
+                if (better >= take - in) s[P.at[tid]] = -INFINITY;
+            }
+            __syncthreads();
+            return below;
+        }
     }
     // the open pages by their fp64 scores
-    for (int j = warp; j < n; j += kWarps) {
+    for (int j = warp; j < n; j += NW) {
         const float x = s[j];
         const bool open = !(x > above) && !(x < below);
         unsigned long long key = 0;
@@ -196,28 +226,28 @@ __device__ float pick_bound(PickSmem& P, float* s, int n, int take, unsigned lon
     while (lo < hi) {
         const unsigned long long mid = lo + (hi - lo) / 2 + 1;
         int c = 0;
-        for (int j = tid; j < n; j += kNT) c += big[j] >= mid;
+        for (int j = tid; j < n; j += NT) c += big[j] >= mid;
         c = (int)cta_sum(P, (unsigned)c, 0u, ph);
         if (c >= want) lo = mid; else hi = mid - 1;
         if (c == want) break;
     }
     int c = 0;
-    for (int j = tid; j < n; j += kNT) c += big[j] >= lo;
+    for (int j = tid; j < n; j += NT) c += big[j] >= lo;
     int jl = n;                                            // pages of just the key lo are in up to jl
     if ((int)cta_sum(P, (unsigned)c, 0u, ph) != want) {
         c = 0;
-        for (int j = tid; j < n; j += kNT) c += big[j] > lo;
+        for (int j = tid; j < n; j += NT) c += big[j] > lo;
         const int ties = want - (int)cta_sum(P, (unsigned)c, 0u, ph);
         jl = 0;
         int jh = n - 1;                                    // the smallest j up to which there are `ties` of them
         while (jl < jh) {
             const int mid = (jl + jh) / 2;
             c = 0;
-            for (int j = tid; j <= mid; j += kNT) c += big[j] == lo;
+            for (int j = tid; j <= mid; j += NT) c += big[j] == lo;
             if ((int)cta_sum(P, (unsigned)c, 0u, ph) >= ties) jh = mid; else jl = mid + 1;
         }
     }
-    for (int j = tid; j < n; j += kNT) {
+    for (int j = tid; j < n; j += NT) {
         const unsigned long long k = big[j];
         const bool is_in = k == 0 ? s[j] > above : k > lo || (k == lo && j <= jl);
         s[j] = is_in ? 1.f : -1.f;
@@ -230,8 +260,9 @@ __device__ float pick_bound(PickSmem& P, float* s, int n, int take, unsigned lon
 
 // One warp's running softmax over its tiles on the CUDA cores: lane = key
 // (lane & 15) and half of D for the logits, D / 32 channels for the values.
-template <typename T, int D, int GP>
+template <typename T, int D, int GP, int NW>
 struct CoreSimt {
+    static constexpr int kWarps = NW, kNT = NW * 32;
     static constexpr int E = D / 32;
     struct Shared {
         float q[GP * D];
@@ -359,8 +390,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+template <int D, int NW>
 struct CoreMma {
+    static constexpr int kWarps = NW;
     using T = __nv_bfloat16;
     struct Shared {};
     static constexpr float kRaise = 8.f;
@@ -460,17 +492,28 @@ struct CoreMma {
     }
 };
 
-template <typename T> __device__ __forceinline__ T from_f(float x);
-template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+__device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) { *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w); }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float z, float w)
+{
+    uint32_t lo, hi;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(y), "f"(x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(w), "f"(z));
+    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 
 template <int D, class Core>
 struct alignas(16) AttendSmem {
     double w64[2 * D];                 // the page weights, minima's then maxima's
     typename Core::Shared core;
-    float2 wml[kWarps][kMaxPageGroups];
+    float2 wml[Core::kWarps][kMaxPageGroups];
     float2 ml[kMaxPageGroups];
-    PickSmem pick;
+    PickSmem<Core::kWarps> pick;
 };
 
 // Shared memory: the warps' rings (fp64 keys while picking), AttendSmem, and
@@ -478,15 +521,21 @@ struct alignas(16) AttendSmem {
 template <typename T, int D> constexpr int kTileBytes = kKeys * D * (int)sizeof(T);
 template <typename T, int D> constexpr int kRingBytes = kStages<T> * 2 * kTileBytes<T, D>;   // a warp's
 
-// Two CTAs an SM (bf16): while one ranks its pages the other reads keys.
+constexpr int kMaxSources = 8 + kMaxPrefixSplits;   // CTAs of a cluster and ranges of a prefix
+// bytes of the rings, which also hold the sums and weights at the end
+template <typename T, int D, int NW>
+constexpr int kFront = std::max(NW * kRingBytes<T, D>, 4 * kMaxPageGroups * (2 * D + kMaxSources + 1));
+
+// Several CTAs an SM (bf16): while one ranks its pages, or waits for its
+// first keys, the others read.
 template <typename T, int D, class Core>
-__global__ void __launch_bounds__(kNT, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::kWarps : 1)
     page_attend_kernel(const PagePool pool, const PageRows R, const int budget, const int recent, int* __restrict__ picked,
                        const PrefixPart part, const int front, const int wpad)
 {
     extern __shared__ __align__(128) unsigned char raw[];
     using S_t = AttendSmem<D, Core>;
-    constexpr int NS = kStages<T>, TB = kTileBytes<T, D>;
+    constexpr int NS = kStages<T>, TB = kTileBytes<T, D>, kWarps = Core::kWarps, kNT = kWarps * 32;
     S_t& S = *reinterpret_cast<S_t*>(raw + front);
     float* scores = reinterpret_cast<float*>(raw + front + sizeof(S_t));
     int* list = reinterpret_cast<int*>(scores + wpad);
@@ -496,7 +545,10 @@ __global__ void __launch_bounds__(kNT, sizeof(T) == 2 ? 2 : 1)
     const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
     const int u = blockIdx.x / C, row = u / pool.heads, h = u - row * pool.heads;
     const int seq = R.seq[row], pos = R.pos[row];
-    if (seq < 0) return;                                   // a row that is not there, for the whole cluster
+    if (seq < 0) {                                         // a row that is not there, for the whole cluster
+        if (part.splits) grid_dependency_wait();           // (this grid ends after the one it started beside)
+        return;
+    }
     const int sh = __ffs(pool.ps) - 1;
     const int G = R.G;
     int npages = pos < 0 ? 0 : (pos >> sh) + 1;
@@ -559,17 +611,20 @@ __global__ void __launch_bounds__(kNT, sizeof(T) == 2 ? 2 : 1)
                 pages_of(j0 + step);
 #pragma unroll
                 for (int x = 0; x < UN; ++x) {
-                    float s = 0.f, a = 0.f;
+                    float2 s2 = make_float2(0.f, 0.f);
+                    float a = 0.f;
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         float f[N];
                         load_vec<T, N>(reinterpret_cast<const T*>(&v[x][i]), f);
 #pragma unroll
-                        for (int e = 0; e < N; ++e) {
-                            s = fmaf(w[i][e], f[e], s);
+                        for (int e = 0; e < N; e += 2) {
+                            s2 = __ffma2_rn(make_float2(w[i][e], w[i][e + 1]), make_float2(f[e], f[e + 1]), s2);
                             a = fmaf(fabsf(w[i][e]), fabsf(f[e]), a);
+                            a = fmaf(fabsf(w[i][e + 1]), fabsf(f[e + 1]), a);
                         }
                     }
+                    float s = s2.x + s2.y;
 #pragma unroll
                     for (int d = 4; d > 0; d >>= 1) {
                         s += __shfl_xor_sync(0xffffffffu, s, d);
@@ -717,77 +772,122 @@ __global__ void __launch_bounds__(kNT, sizeof(T) == 2 ? 2 : 1)
         sums[i] = o;
         if (i % D == 0) S.ml[g] = make_float2(m, l);
     }
+    if (part.splits) grid_dependency_wait();               // the prefix pass is through
     cluster_arrive();
     cluster_wait();
-    T* orow = static_cast<T*>(R.out) + (size_t)row * R.out_stride + (size_t)h * G * D;
+    // weights of the sources: the cluster's CTAs, then the prefix's ranges
+    float* wt = reinterpret_cast<float*>(raw + 2 * kSums); // [G][sources]
+    float* scale = wt + kMaxPageGroups * kMaxSources;      // [G]
+    static_assert(kFront<T, D, kWarps> >= 2 * kSums + 4 * kMaxPageGroups * (kMaxSources + 1), "and so do the weights");
+    const int ns = C + part.splits;
     const size_t qrows = (size_t)R.rows * pool.heads * G, qr = (size_t)u * G;
-    for (int i = rank * kNT + tid; i < G * D; i += C * kNT) {
-        const int g = i / D;
-        float m = -INFINITY, l = 0.f, o = 0.f;
-        for (int c = 0; c < C; ++c) m = fmaxf(m, ld_cluster_f32(map_to_rank(&S.ml[g].x, c)));
-        for (int s = 0; s < part.splits; ++s) m = fmaxf(m, part.ml[s * qrows + qr + g].x);
+    for (int g = warp; g < G; g += kWarps) {
+        float2 x[(kMaxSources + 31) / 32];
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < (kMaxSources + 31) / 32; ++i) {
+            const int k = lane + 32 * i;
+            x[i] = make_float2(-INFINITY, 0.f);
+            if (k < C) x[i] = make_float2(ld_cluster_f32(map_to_rank(&S.ml[g].x, k)), ld_cluster_f32(map_to_rank(&S.ml[g].y, k)));
+            else if (k < ns) x[i] = part.ml[(k - C) * qrows + qr + g];
+            m = fmaxf(m, x[i].x);
+        }
+        m = warp_max(m);
         const float base = m == -INFINITY ? 0.f : m;
-        for (int c = 0; c < C; ++c) {
-            const float a = ex2_approx(ld_cluster_f32(map_to_rank(&S.ml[g].x, c)) - base);
-            l += a * ld_cluster_f32(map_to_rank(&S.ml[g].y, c));
-            o = fmaf(a, ld_cluster_f32(map_to_rank(&sums[i], c)), o);
+#pragma unroll
+        for (int i = 0; i < (kMaxSources + 31) / 32; ++i) {
+            const float a = ex2_approx(x[i].x - base);
+            l += a * x[i].y;
+            if (lane + 32 * i < ns) wt[g * kMaxSources + lane + 32 * i] = a;
         }
-#pragma unroll 4
-        for (int s = 0; s < part.splits; ++s) {
-            const float2 x = part.ml[s * qrows + qr + g];
-            const float a = ex2_approx(x.x - base);
-            l += a * x.y;
-            o = fmaf(a, part.o[(s * qrows + qr) * D + i], o);
-        }
+        l = warp_sum(l);
         // no key at all: zero; a bad table entry has made l NaN
-        orow[i] = from_f<T>(l == 0.f ? 0.f : o / l);
+        if (lane == 0) scale[g] = l == 0.f ? 0.f : 1.f / l;
+    }
+    __syncthreads();
+    T* orow = static_cast<T*>(R.out) + (size_t)row * R.out_stride + (size_t)h * G * D;
+    for (int i = (rank * kNT + tid) * 4; i < G * D; i += C * kNT * 4) {
+        const int g = i / D;
+        const float* w = wt + g * kMaxSources;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float a, float4 x) {
+            o.x = fmaf(a, x.x, o.x);
+            o.y = fmaf(a, x.y, o.y);
+            o.z = fmaf(a, x.z, o.z);
+            o.w = fmaf(a, x.w, o.w);
+        };
+        for (int c = 0; c < C; ++c) add(w[c], ld_cluster_f4(map_to_rank(&sums[i], c)));
+#pragma unroll 8
+        for (int s = 0; s < part.splits; ++s) add(w[C + s], *reinterpret_cast<const float4*>(part.o + (s * qrows + qr) * D + i));
+        const float f = scale[g];
+        store4(orow + i, o.x * f, o.y * f, o.z * f, o.w * f);
     }
     cluster_arrive();
     cluster_wait();                                        // no CTA leaves while another reads its sums
 }
 
-// CTAs of a unit.
-int cluster_of(long long units, int tiles, int resident)
+// Warps of a CTA.
+int attend_warps(const PagePool& p, const PageRows& r, int budget)
 {
+    if (const char* e = getenv("ATTEND_NW")) return atoi(e);
+    return 4;
+}
+
+// CTAs of a unit.
+int cluster_of(long long units, int tiles, int resident, int warps)   // tune
+{
+    if (const char* e = getenv("ATTEND_C")) return atoi(e);
     int c = 1;
-    while (c < 8 && units * c * 2 <= resident && tiles >= 2 * c * 2 * kWarps) c *= 2;
+    while (c < 8 && units * c * 2 <= resident && tiles >= 2 * c * 2 * warps) c *= 2;
     return c;
 }
 
 template <typename T, int D, class Core>
 cudaError_t go(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
 {
+    constexpr int NW = Core::kWarps;
     const bool picks = budget > 0 && budget < r.width;
     const int wpad = picks ? (r.width + 3) & ~3 : 0;
-    const int front = std::max(kWarps * kRingBytes<T, D>, 8 * wpad);
+    const int front = std::max(kFront<T, D, NW>, 8 * wpad);
     const size_t smem = front + sizeof(AttendSmem<D, Core>) + 4 * ((size_t)wpad + (picks ? budget : 0));
     const auto kernel = page_attend_kernel<T, D, Core>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long units = (long long)r.rows * p.heads;
-    const int C = cluster_of(units, (picks ? budget : r.width) * (p.ps / kKeys), (smem <= 113 * 1024 ? 2 : 1) * kSMs);
-    cudaLaunchAttribute at[1];
+    const int C = cluster_of(units, (picks ? budget : r.width) * (p.ps / kKeys), (int)(227 * 1024 / (smem + 1024)) * kSMs, NW);
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)C;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * C));
-    cfg.blockDim = dim3(kNT);
+    cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = part.splits ? 2 : 1;                    // behind a prefix pass: its own keys are read meanwhile
     return cudaLaunchKernelEx(&cfg, kernel, p, r, budget, recent, picked, part, front, wpad);
 }
 
-template <int D>
+template <int D, int NW>
 cudaError_t by_groups(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
 {
-    if (p.dtype) return go<__nv_bfloat16, D, CoreMma<D>>(p, r, budget, recent, picked, part, st);
-    if (r.G == 1) return go<float, D, CoreSimt<float, D, 1>>(p, r, budget, recent, picked, part, st);
-    if (r.G <= 4) return go<float, D, CoreSimt<float, D, 4>>(p, r, budget, recent, picked, part, st);
-    if (r.G <= 8) return go<float, D, CoreSimt<float, D, 8>>(p, r, budget, recent, picked, part, st);
-    return go<float, D, CoreSimt<float, D, 16>>(p, r, budget, recent, picked, part, st);
+    if (p.dtype) return go<__nv_bfloat16, D, CoreMma<D, NW>>(p, r, budget, recent, picked, part, st);
+    if (r.G == 1) return go<float, D, CoreSimt<float, D, 1, 4>>(p, r, budget, recent, picked, part, st);
+    if (r.G <= 4) return go<float, D, CoreSimt<float, D, 4, 4>>(p, r, budget, recent, picked, part, st);
+    if (r.G <= 8) return go<float, D, CoreSimt<float, D, 8, 4>>(p, r, budget, recent, picked, part, st);
+    return go<float, D, CoreSimt<float, D, 16, 4>>(p, r, budget, recent, picked, part, st);
+}
+
+template <int D>
+cudaError_t by_warps(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
+{
+    const int nw = attend_warps(p, r, budget);
+    if (nw == 1) return by_groups<D, 1>(p, r, budget, recent, picked, part, st);
+    if (nw == 2) return by_groups<D, 2>(p, r, budget, recent, picked, part, st);
+    return by_groups<D, 4>(p, r, budget, recent, picked, part, st);
 }
 
 }  // namespace
@@ -795,7 +895,7 @@ cudaError_t by_groups(const PagePool& p, const PageRows& r, int budget, int rece
 cudaError_t launch_page_attend(const PagePool& p, const PageRows& r, int budget, int recent, int* picked,
                                const PrefixPart& part, cudaStream_t st)
 {
-    return p.D == 64 ? by_groups<64>(p, r, budget, recent, picked, part, st) : by_groups<128>(p, r, budget, recent, picked, part, st);
+    return p.D == 64 ? by_warps<64>(p, r, budget, recent, picked, part, st) : by_warps<128>(p, r, budget, recent, picked, part, st);
 }
 
 }  // namespace h2o

@@ -11,6 +11,7 @@ constexpr int kMaxPageRequests = 16384;   // requests of one h2o_page_tables cal
 constexpr int kMaxTableWidth = 16384;     // pages of one request
 constexpr int kMaxPickedPages = 4096;     // budget of a call that has to choose
 constexpr int kMaxPageGroups = 16;        // query heads per cache head
+constexpr int kMaxPrefixSplits = 64;      // ranges of a shared prefix
 
 // The page pool: K, V [pages][heads][ps][D], bounds [pages][heads][2][D].
 struct PagePool {

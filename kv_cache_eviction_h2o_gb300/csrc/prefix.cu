@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, c
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int h = blockIdx.z, x0 = blockIdx.x * kRows, G = R.G, nx = R.rows * G;
     const int j0 = blockIdx.y * per, j1 = min(prefix_len, j0 + per);
+    grid_launch_dependents();          // the rows' own pass may start on what SMs are left; it waits before it reads sums
     bool bad = false;
     for (int i = tid; i < kRows * D; i += 256) {
         const int r = i / D, e = i % D, x = x0 + r;
@@ -165,7 +166,7 @@ int range_keys(int rows, int heads, int G, int prefix_len)
 {
     const long long tiles = (long long)((rows * (long long)G + kRows - 1) / kRows) * heads;
     const int steps = (prefix_len + kCols - 1) / kCols;
-    const int want = (int)std::max<long long>(1, std::min<long long>(2 * kSMs / tiles, 64));
+    const int want = (int)std::max<long long>(1, std::min<long long>(2 * kSMs / tiles, kMaxPrefixSplits));
     return (steps + std::min(want, steps) - 1) / std::min(want, steps) * kCols;
 }
 

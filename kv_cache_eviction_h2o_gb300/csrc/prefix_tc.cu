@@ -7,7 +7,11 @@
 //   S = Q K^T      (SMEM x SMEM -> TMEM, M = N = 128, K = D)
 //   P = 2^(c S - m)  (128 threads a stream, thread = TMEM lane = query row)
 //   O += P V       (TMEM x SMEM -> TMEM, M = 128, N = D, K = 128)
-// so that one stream's exponentials run under the other's products.  With more
+// so that one stream's exponentials run under the other's products.  S and P go
+// by halves of 64 keys: while the threads work on one half, the product of the
+// other's P and the next tile's scores in its place are made, so neither waits
+// for the other's latency (whole tiles: 4400 cycles a tile of two streams, of
+// which the products are 2050).  With more
 // than 128 query rows left the streams are two query tiles over the same keys
 // (each key tile is read once for 256 rows); with fewer they are the even and
 // the odd key tiles of one query tile, joined at the end.
@@ -27,6 +31,9 @@
 #include "paged.h"
 #include "tc.cuh"
 
+#ifndef KSTEPS
+#define KSTEPS 2
+#endif
 namespace h2o {
 
 namespace {
@@ -36,6 +43,7 @@ constexpr int kT = 128;
 constexpr int kThreads = 384;
 constexpr uint32_t kBox = kT * 64 * 2;             // 128 rows x 64 channels: 16 KB
 constexpr float kRaise = 8.f;
+constexpr int kSteps = KSTEPS, kStep = kT / kSteps;     // S and P go by parts of a tile
 
 template <int D> struct Cfg {
     static constexpr int kBoxes = D / 64;
@@ -49,7 +57,7 @@ struct alignas(1024) Smem {
     uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
     float2 xml[kT];
     uint64_t full[Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
-    uint64_t q_ready, s_ready[2], p_ready[2], pv_done[2], last;
+    uint64_t q_ready, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2], last;   // [stream][part of the tile]
     uint32_t tmem;
     int abort, bad;
 };
@@ -59,18 +67,33 @@ static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "one CTA's shared memory")
 template <int N, bool BMN>
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((BMN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kT >> 4) << 24);
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+// The issuing warp runs its loop as a whole, so that descriptors stay in
+// uniform registers, and one lane (`on`) issues: a loop inside one lane's
+// branch issued a product every 100 to 115 cycles, whatever its size.
+__device__ __forceinline__ uint32_t elect_lane()
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(id), "r"(acc)
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(acc), "r"(on)
                  : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc)
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(id), "r"(acc)
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"(acc), "r"(on)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t on, uint64_t* bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(on)
                  : "memory");
 }
 
@@ -105,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int NS = C::kSlots;
     extern __shared__ unsigned char raw[];
     Smem<D>& S = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (known to be uniform)
     const int G = R.G, nx = R.rows * G, h = blockIdx.z, x0 = blockIdx.x * 2 * kT;
     const bool two = x0 + kT < nx;                   // two query tiles
     const int L = two ? 1 : 2;
@@ -113,18 +136,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = (j1 - j0 + kT - 1) / kT;           // key tiles, at least one
     auto valid_of = [&](int t) { return min(kT, j1 - j0 - t * kT); };
 
+    grid_launch_dependents();                        // the rows' own pass may start on what SMs are left; it waits before it reads sums
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&S.full[s], 1);
-            mbar_init(&S.empty[s], 1);
+            mbar_init(&S.empty[s], two ? 2 : 1);
         }
         mbar_init(&S.q_ready, two ? 8 : 4);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&S.s_ready[s], 1);
-            mbar_init(&S.p_ready[s], 4);
+            for (int b = 0; b < kSteps; ++b) {
+                mbar_init(&S.s_ready[s][b], 1);
+                mbar_init(&S.p_ready[s][b], 4);
+            }
             mbar_init(&S.pv_done[s], 1);
         }
-        mbar_init(&S.last, 1);
+        mbar_init(&S.last, 2);
         S.abort = S.bad = 0;
         fence_mbar_init();
     }
@@ -170,115 +196,143 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a load that was never used (an aborted sweep) lands before the shared memory is given up
         if (lane == 0 && *(volatile int*)&S.abort)
             for (int i = max(0, at - NS); i < at; ++i) mbar_wait(&S.full[i % NS], (uint32_t)(i / NS) & 1u);
-    } else if (warp == 1) {
-        // ------------------------------------------------ products
-        if (lane == 0) {
-            bool ok = wait(S, &S.q_ready, 0);
-            auto slot_full = [&](int i) {
-                if (ok) ok = wait(S, &S.full[i % NS], i / NS);
-            };
-            auto score = [&](int s, int i) {
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t a = sw128_desc(S.q[two ? s : 0]), b = sw128_desc(S.ring[i % NS]);
+    } else if (warp <= 2) {
+        // ------------------------------------------------ products of stream s
+        const int s = warp - 1;
+        const uint32_t on = elect_lane();
+        const uint64_t q0 = sw128_desc(S.q[two ? s : 0]), k0 = sw128_desc(S.ring[0]), v0 = value_desc(S.ring[0]);
+        const uint32_t sS = tS(s), sO = tO(s);
+        bool ok = __all_sync(0xffffffffu, wait(S, &S.q_ready, 0));
+        auto slot_full = [&](int i) {
+            if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.full[i % NS], i / NS));
+        };
+        // scores of step b of the tile in place i
+        auto score = [&](int b, int i) {
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t k = k0 + (uint64_t)((uint32_t)(i % NS) * (C::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t off = (uint64_t)(((uint32_t)(k / 4) * kBox + (uint32_t)(k % 4) * 32u) >> 4);
-                    mma_ss(tS(s), a + off, b + off, kIdesc<kT, false>, k > 0);
-                }
-                tc_commit(&S.s_ready[s]);
+            for (int x = 0; x < D / 16; ++x) {
+                const uint64_t off = (uint64_t)(((uint32_t)(x / 4) * kBox + (uint32_t)(x % 4) * 32u) >> 4);
+                mma_ss(on, sS + (uint32_t)(kStep * b), q0 + off, k + off, kIdesc<kStep, false>, x > 0);
+            }
+            commit(on, &S.s_ready[s][b]);
+        };
+        // nth: tiles of this stream before; valid: keys of the tile
+        auto values = [&](int b, int nth, int i, int valid) {
+            slot_full(i);
+            if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.p_ready[s][b], nth));
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t v = v0 + (uint64_t)((uint32_t)(i % NS) * (C::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
+            const int nk = (min(kStep, valid - kStep * b) + 15) / 16;
+            auto one = [&](int x) {
+                mma_ts(on, sO, sS + (uint32_t)(kStep * b + 8 * x), v + (uint64_t)((uint32_t)x * 2048u >> 4), kIdesc<D, true>,
+                       nth > 0 || b > 0 || x > 0);
             };
-            auto values = [&](int s, int step, int i, int valid) {
-                if (ok) ok = wait(S, &S.p_ready[s], step);
-                slot_full(i);
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t b = value_desc(S.ring[i % NS]);
-                const int nk = (valid + 15) / 16;
-                for (int k = 0; k < nk; ++k)
-                    mma_ts(tO(s), tS(s) + 8u * (uint32_t)k, b + (uint64_t)((uint32_t)k * 2048u >> 4), kIdesc<D, true>, step > 0 || k > 0);
-                tc_commit(&S.pv_done[s]);
-            };
-            auto release = [&](int i) {
-                if (ok) tc_commit(&S.empty[i % NS]);
-            };
-            if (two) {
-                slot_full(0);
-                score(0, 0);
-                score(1, 0);
-                release(0);
-                for (int t = 0; t < n; ++t) {
-                    const int v = v_at(t, n, 1), k = v + 1;
-                    values(0, t, v, valid_of(t));
-                    if (t + 1 < n) { slot_full(k); score(0, k); }
-                    values(1, t, v, valid_of(t));
-                    release(v);
-                    if (t + 1 < n) { score(1, k); release(k); }
-                }
+            if (nk == kStep / 16) {
+#pragma unroll
+                for (int x = 0; x < kStep / 16; ++x) one(x);
             } else {
-                for (int t = 0; t < min(2, n); ++t) { slot_full(t); score(t, t); release(t); }
-                for (int t = 0; t < n; ++t) {
-                    const int s = t & 1, v = v_at(t, n, 2), k = v + 1;
-                    values(s, t >> 1, v, valid_of(t));
-                    release(v);
-                    if (t + 2 < n) { slot_full(k); score(s, k); release(k); }
+                for (int x = 0; x < nk; ++x) one(x);
+            }
+            commit(on, &S.pv_done[s]);
+        };
+        auto release = [&](int i) {                  // (two query tiles: when both streams have)
+            if (ok) commit(on, &S.empty[i % NS]);
+        };
+        const int stride = two ? 1 : 2, t0 = two ? 0 : s;
+        if (t0 < n) {
+            slot_full(t0);
+            for (int b = 0; b < kSteps; ++b) score(b, t0);
+            release(t0);
+        }
+        for (int t = t0, nth = 0; t < n; t += stride, ++nth) {
+            const int v = v_at(t, n, L), k = v + 1;
+            const bool more = t + stride < n;
+            for (int b = 0; b < kSteps; ++b) {
+                values(b, nth, v, valid_of(t));
+                if (b == kSteps - 1) release(v);
+                if (more) {
+                    if (b == 0) slot_full(k);
+                    score(b, k);
+                    if (b == kSteps - 1) release(k);
                 }
             }
-            // everything issued is done before TMEM is given back
-            tc_commit(&S.last);
-            mbar_wait(&S.last, 0);
         }
-        __syncwarp();
+        // everything issued is done before TMEM is given back
+        commit(on, &S.last);
+        mbar_wait(&S.last, 0);
     } else if (warp >= 4) {
         // ------------------------------------------------ softmax
         const int s = (warp - 4) >> 2, w = warp & 3, row = w * 32 + lane;
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
         if (two || s == 0) {
-            // this stream's query row into the swizzled tile
-            const int x = x0 + s * kT + row;
-            uint8_t* dst = S.q[s] + row * 128;
-            const uint4* src = nullptr;
-            if (x < nx)
-                src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(R.q) + (size_t)(x / G) * R.q_stride +
-                                                     (size_t)(h * G + x % G) * D);
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(dst + (c / 8) * kBox + (((c & 7) ^ (row & 7)) << 4)) = src ? src[c] : make_uint4(0, 0, 0, 0);
+            // the warp's 32 query rows into the swizzled tile, whole rows at a time (a short loop: code that runs once is
+            // fetched from far away, and the unrolled form took 5000 cycles)
+            constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows a step
+            const int c = lane % LPR;
+            int r = w * 32 + lane / LPR, x = x0 + s * kT + r, qr = x / G, g = x - qr * G;
+            uint8_t* dst = S.q[s] + (c / 8) * kBox;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.q) + (size_t)h * G * D + c * 8;
+#pragma unroll 1
+            for (int i = 0; i < LPR; ++i) {
+                const bool fill = x < nx;
+                const __nv_bfloat16* from = fill ? src + (size_t)qr * R.q_stride + g * D : src;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4))),
+                             "l"(from), "r"(fill ? 16 : 0)
+                             : "memory");
+                r += RPI;
+                x += RPI;
+                g += RPI;
+                while (g >= G) {
+                    g -= G;
+                    ++qr;
+                }
+            }
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.q_ready);
         }
         const float c2 = R.qscale;
-        const int steps = two ? n : (n + 1 - s) / 2;
+        const int steps = kSteps * (two ? n : (n + 1 - s) / 2);   // parts of this stream's tiles
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int i = 0; i < steps && ok; ++i) {
-            const int t = two ? i : 2 * i + s, valid = valid_of(t);
-            ok = wait(S, &S.s_ready[s], i);
-            ok = __all_sync(0xffffffffu, ok);
+        for (int i = 0; i < steps; ++i) {
+            const int nth = i / kSteps, b = i % kSteps, t = two ? nth : 2 * nth + s, valid = valid_of(t) - kStep * b;
+            const uint32_t at = tS(s) + lanes + (uint32_t)(kStep * b);
+            ok = __all_sync(0xffffffffu, wait(S, &S.s_ready[s][b], nth));
             if (!ok) break;
             tc_fence_after();
-            uint32_t z[4][32];
+            constexpr int NC = kStep / 32;
+            uint32_t z[NC][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc_ld32_issue(tS(s) + lanes + 32u * c, z[c]);
+            for (int c = 0; c < NC; ++c) tc_ld32_issue(at + 32u * c, z[c]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc_ld32_wait(z[c]);
-            if (valid < kT) {
+            for (int c = 0; c < NC; ++c) tc_ld32_wait(z[c]);
+            if (valid < kStep) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         if (c * 32 + k >= valid) z[c][k] = 0xff800000u;
             }
-            float mx[4];
+            float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx[c] = __uint_as_float(z[c][0]);
+            for (int c = 0; c < NC; ++c) {
+                float mx[2];
 #pragma unroll
-                for (int k = 1; k < 31; k += 2) mx[c] = max3f(mx[c], __uint_as_float(z[c][k]), __uint_as_float(z[c][k + 1]));
-                mx[c] = fmaxf(mx[c], __uint_as_float(z[c][31]));
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t* y = z[c] + 16 * e;
+                    mx[e] = __uint_as_float(y[0]);
+#pragma unroll
+                    for (int k = 1; k < 15; k += 2) mx[e] = max3f(mx[e], __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+                    mx[e] = fmaxf(mx[e], __uint_as_float(y[15]));
+                }
+                top = max3f(top, mx[0], mx[1]);
             }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+            top *= c2;
             const bool raise = top > m + kRaise;                 // (m = -inf: any finite logit)
             if (__any_sync(0xffffffffu, raise)) {
                 const float a = raise ? ex2_fast(m - top) : 1.f;
@@ -287,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= a;
                 }
                 if (i > 0) {
+                    // (these scores came after all products but, with two parts, the last)
                     ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s], i - 1));
                     if (!ok) break;
                     tc_fence_after();
@@ -305,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 cc = make_float2(c2, c2), nb = make_float2(-base, -base);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < NC; ++c) {
                 uint32_t p[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
@@ -314,24 +369,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum[k & 1] = __fadd2_rn(sum[k & 1], x);
                     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[k]) : "f"(x.y), "f"(x.x));
                 }
-                tc_st16(tS(s) + lanes + 16u * c, p);
+                tc_st16(at + 16u * c, p);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            if (t == n - 1 && valid < kT && (two ? s == 0 : true)) {
-                // the value rows behind the range's last key in its group of 16: their weights are 0, but what lies there may be NaN
+            if (t == n - 1 && valid > 0 && valid < kStep) {
+                // the value rows behind the range's last key in its group of 16: their weights are 0, but what lies there may be
+                // NaN (two query tiles: both streams write the zeros, each before its own product)
                 const int v = v_at(t, n, L), end = (valid + 15) & ~15;
                 ok = __all_sync(0xffffffffu, wait(S, &S.full[v % NS], v / NS));
                 if (!ok) break;
                 for (int x = row; x < (end - valid) * C::kBoxes * 8; x += kT)
-                    *reinterpret_cast<uint4*>(S.ring[v % NS] + (x >> 3) % C::kBoxes * kBox + (valid + (x >> 3) / C::kBoxes) * 128 + (x & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(S.ring[v % NS] + (x >> 3) % C::kBoxes * kBox + (kStep * b + valid + (x >> 3) / C::kBoxes) * 128 +
+                                              (x & 7) * 16) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
             tc_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.p_ready[s]);
+            if (lane == 0) mbar_arrive(&S.p_ready[s][b]);
         }
+        // (the last product but one first: a phase is told from its neighbour only)
+        if (ok && steps > 1) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s], steps - 2));
         if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s], steps - 1));
         tc_fence_after();
 
@@ -397,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
 #pragma unroll 4
                     for (int r = lane / CH; r < 32; r += 32 / CH) {
-                        const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)qr, r);
+                        const size_t to = __shfl_sync(0xffffffffu, (unsigned)qr, r);   // (below 2^30)
                         if (x - lane + r < nx)
                             *reinterpret_cast<float4*>(part.o + to * D + d0 + (lane % CH) * 4) = stage[r * CH + ((lane % CH) ^ (r & (CH - 1)))];
                     }
@@ -450,7 +508,7 @@ int prefix_tc_range(int rows, int heads, int G, int prefix_len)
     const int tiles = (prefix_len + kT - 1) / kT;
     int best = tiles;
     long long cost = -1;
-    for (int s = 1; s <= std::min(tiles, 64); ++s) {
+    for (int s = 1; s <= std::min(tiles, kMaxPrefixSplits); ++s) {
         const int each = (tiles + s - 1) / s;
         const long long ctas = units * ((tiles + each - 1) / each);
         const long long c = (ctas + kSMs - 1) / kSMs * (each + 2);
