@@ -17,7 +17,6 @@
 // to the lowest page.
 #include <algorithm>
 #include <cfloat>
-#include <cstdlib>
 
 #include "common.cuh"
 #include "paged.h"
@@ -826,19 +825,18 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
     cluster_wait();                                        // no CTA leaves while another reads its sums
 }
 
-// Warps of a CTA.
-int attend_warps(const PagePool& p, const PageRows& r, int budget)
-{
-    if (const char* e = getenv("ATTEND_NW")) return atoi(e);
-    return 4;
-}
+// Warps of a CTA: two where there are more units than CTAs fit and each has
+// few tiles, so that more units are under way (6400 units of 12 tiles: 201 us
+// with four, 153 with two; 512 of 24: 81, 80; 512 of 96: 83, 89).
+int attend_warps(long long units, int tiles) { return units > 4 * kSMs && tiles <= 32 ? 2 : 4; }
 
-// CTAs of a unit.
-int cluster_of(long long units, int tiles, int resident, int warps)   // tune
+// CTAs of a unit: up to 8 while all clusters fit the SMs at once and every
+// warp has three tiles (16 units of 96 tiles: 23 us with one, 12 with four;
+// 70 of 68: 18, 15 with four, 18 with eight).
+int cluster_of(long long units, int tiles, int resident, int warps)
 {
-    if (const char* e = getenv("ATTEND_C")) return atoi(e);
     int c = 1;
-    while (c < 8 && units * c * 2 <= resident && tiles >= 2 * c * 2 * warps) c *= 2;
+    while (c < 8 && units * c * 2 <= resident && tiles >= 3 * c * 2 * warps) c *= 2;
     return c;
 }
 
@@ -854,20 +852,27 @@ cudaError_t go(const PagePool& p, const PageRows& r, int budget, int recent, int
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long units = (long long)r.rows * p.heads;
-    const int C = cluster_of(units, (picks ? budget : r.width) * (p.ps / kKeys), (int)(227 * 1024 / (smem + 1024)) * kSMs, NW);
+    const int C = cluster_of(units, (budget > 0 ? std::min(budget, r.width) : r.width) * (p.ps / kKeys), (int)(227 * 1024 / (smem + 1024)) * kSMs, NW);
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
+    int na = 0;
+    if (C > 1) {
+        at[na].id = cudaLaunchAttributeClusterDimension;
+        at[na].val.clusterDim.x = (unsigned)C;
+        at[na].val.clusterDim.y = at[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    if (part.splits) {                                     // behind a prefix pass: its own keys are read meanwhile
+        at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * C));
     cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = part.splits ? 2 : 1;                    // behind a prefix pass: its own keys are read meanwhile
+    cfg.numAttrs = (unsigned)na;
     return cudaLaunchKernelEx(&cfg, kernel, p, r, budget, recent, picked, part, front, wpad);
 }
 
@@ -884,9 +889,8 @@ cudaError_t by_groups(const PagePool& p, const PageRows& r, int budget, int rece
 template <int D>
 cudaError_t by_warps(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
 {
-    const int nw = attend_warps(p, r, budget);
-    if (nw == 1) return by_groups<D, 1>(p, r, budget, recent, picked, part, st);
-    if (nw == 2) return by_groups<D, 2>(p, r, budget, recent, picked, part, st);
+    const int tiles = (budget > 0 ? std::min(budget, r.width) : r.width) * (p.ps / kKeys);
+    if (attend_warps((long long)r.rows * p.heads, tiles) == 2) return by_groups<D, 2>(p, r, budget, recent, picked, part, st);
     return by_groups<D, 4>(p, r, budget, recent, picked, part, st);
 }
 
