@@ -506,6 +506,20 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void add4(float4& o, float a, float4 x)
+{
+    o.x = fmaf(a, x.x, o.x);
+    o.y = fmaf(a, x.y, o.y);
+    o.z = fmaf(a, x.z, o.z);
+    o.w = fmaf(a, x.w, o.w);
+}
+
 template <int D, class Core>
 struct alignas(16) AttendSmem {
     double w64[2 * D];                 // the page weights, minima's then maxima's
@@ -562,6 +576,35 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
     if (budget > 0 && npages > budget) {
         int* pick_out = picked && rank == 0 ? picked + (size_t)u * budget : nullptr;
         if (take > 0) {                                    // (else the newest pages are all)
+            // Bounds come through the warp's ring, kScan pages a lane group and stage, each lane reading back what it asked
+            // for (registers alone kept 8 KB a warp in flight, and the ring is idle now).
+            constexpr int N = 16 / sizeof(T), NV = 2 * D / 8 / N, kScan = 4;
+            static_assert(kScan * NV * 512 <= 2 * TB, "a stage of bounds fits a stage of the ring");
+            const T* bounds = static_cast<const T*>(pool.bounds);
+            const int sub = lane & 7;                      // eight lanes a page
+            const int step = C * kWarps * 4 * kScan;
+            int j0 = (rank * kWarps + warp) * 4 * kScan;
+            int pg[NS][kScan];
+            auto ids = [&](int (&id)[kScan], int j) {
+#pragma unroll
+                for (int x = 0; x < kScan; ++x) id[x] = j + x * 4 + (lane >> 3) < ncand ? table[j + x * 4 + (lane >> 3)] : 0;
+            };
+            auto scan = [&](const int (&id)[kScan], int j, int stage) {
+                if (j < ncand)
+#pragma unroll
+                    for (int x = 0; x < kScan; ++x) {
+                        const bool ok = (unsigned)id[x] < (unsigned)pool.pages;
+                        const T* from = bounds + ((size_t)(ok ? id[x] : 0) * pool.heads + h) * 2 * D + sub * N;
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+                            cp_async16(smem_u32(ring + stage * 2 * TB + ((x * NV + i) * 32 + lane) * 16), from + i * 8 * N, true);
+                    }
+                cp_commit();
+            };
+#pragma unroll
+            for (int k = 0; k < NS; ++k) ids(pg[k], j0 + k * step);
+#pragma unroll
+            for (int k = 0; k < NS - 1; ++k) scan(pg[k], j0 + k * step, k);
             if (tid == 0) S.pick.amax = 0u;
             for (int i = tid; i < 2 * D; i += kNT) {
                 double s = 0.0;
@@ -574,48 +617,25 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             }
             __syncthreads();
             cluster_arrive();
-            constexpr int N = 16 / sizeof(T), NV = 2 * D / 8 / N;
-            constexpr int UN = sizeof(T) == 2 ? 4 : 2;         // pages a lane has in flight
-            const T* bounds = static_cast<const T*>(pool.bounds);
-            // eight lanes a page
             float w[NV][N];
-            const int sub = lane & 7;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < N; ++e) w[i][e] = (float)S.w64[(i * 8 + sub) * N + e];
             unsigned amax = 0u;
-            const int step = C * kWarps * 4 * UN;
-            int pg[UN];
-            auto pages_of = [&](int j0) {
-#pragma unroll
-                for (int x = 0; x < UN; ++x) {
-                    const int j = j0 + x * 4 + (lane >> 3);
-                    pg[x] = j < ncand ? table[j] : 0;
-                }
-            };
-            int j0 = (rank * kWarps + warp) * 4 * UN;
-            pages_of(j0);
-            cluster_wait();                                    // every CTA has set its maximum
+            cluster_wait();                                // every CTA has set its maximum
+            int stage = 0;
             for (; j0 < ncand; j0 += step) {
-                uint4 v[UN][NV];
-                bool ok[UN];
+                scan(pg[NS - 1], j0 + (NS - 1) * step, stage == 0 ? NS - 1 : stage - 1);
+                cp_wait<NS - 1>();
 #pragma unroll
-                for (int x = 0; x < UN; ++x) {
-                    ok[x] = (unsigned)pg[x] < (unsigned)pool.pages;
-                    const T* b = bounds + ((size_t)(ok[x] ? pg[x] : 0) * pool.heads + h) * 2 * D;
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) v[x][i] = *reinterpret_cast<const uint4*>(b + (i * 8 + sub) * N);
-                }
-                pages_of(j0 + step);
-#pragma unroll
-                for (int x = 0; x < UN; ++x) {
+                for (int x = 0; x < kScan; ++x) {
                     float2 s2 = make_float2(0.f, 0.f);
                     float a = 0.f;
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         float f[N];
-                        load_vec<T, N>(reinterpret_cast<const T*>(&v[x][i]), f);
+                        load_vec<T, N>(reinterpret_cast<const T*>(ring + stage * 2 * TB + ((x * NV + i) * 32 + lane) * 16), f);
 #pragma unroll
                         for (int e = 0; e < N; e += 2) {
                             s2 = __ffma2_rn(make_float2(w[i][e], w[i][e + 1]), make_float2(f[e], f[e + 1]), s2);
@@ -629,14 +649,21 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                         s += __shfl_xor_sync(0xffffffffu, s, d);
                         a += __shfl_xor_sync(0xffffffffu, a, d);
                     }
-                    if (!ok[x]) { s = NAN; a = NAN; }          // no such page: picked, and its row is NaN
+                    if ((unsigned)pg[0][x] >= (unsigned)pool.pages) { s = NAN; a = NAN; }   // no such page: picked, and its row is NaN
                     const int j = j0 + x * 4 + (lane >> 3);
                     if (j < ncand) {
                         amax = max(amax, __float_as_uint(fabsf(a)));
                         for (int c = sub; c < C; c += 8) st_cluster_f32(map_to_rank(scores + j, c), s);
                     }
                 }
+#pragma unroll
+                for (int x = 0; x < kScan; ++x)
+#pragma unroll
+                    for (int k = 0; k < NS - 1; ++k) pg[k][x] = pg[k + 1][x];
+                ids(pg[NS - 1], j0 + NS * step);
+                stage = stage + 1 == NS ? 0 : stage + 1;
             }
+            cp_wait<0>();
             amax = __reduce_max_sync(0xffffffffu, amax);
             if (lane < C) cluster_max_u32(map_to_rank(&S.pick.amax, lane), amax);
             cluster_arrive();
@@ -685,16 +712,14 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                 const int j = i * 32 + lane;
                 const bool is_in = j < ncand && scores[j] >= bound;
                 const unsigned in = __ballot_sync(0xffffffffu, is_in);
-                if (is_in) {
-                    const int at = S.pick.count[i] + __popc(in & ((1u << lane) - 1u));
-                    list[at] = table[j];
-                    if (pick_out) pick_out[at] = j;
-                }
+                if (is_in) list[S.pick.count[i] + __popc(in & ((1u << lane) - 1u))] = j;
             }
+            __syncthreads();
         }
-        for (int j = tid; j < recent; j += kNT) {
-            list[take + j] = table[ncand + j];
-            if (pick_out) pick_out[take + j] = ncand + j;
+        for (int i = tid; i < budget; i += kNT) {
+            const int j = i < take ? list[i] : ncand + i - take;
+            list[i] = table[j];
+            if (pick_out) pick_out[i] = j;
         }
         __syncthreads();
         nlist = budget;
@@ -774,52 +799,75 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
     if (part.splits) grid_dependency_wait();               // the prefix pass is through
     cluster_arrive();
     cluster_wait();
-    // weights of the sources: the cluster's CTAs, then the prefix's ranges
-    float* wt = reinterpret_cast<float*>(raw + 2 * kSums); // [G][sources]
-    float* scale = wt + kMaxPageGroups * kMaxSources;      // [G]
-    static_assert(kFront<T, D, kWarps> >= 2 * kSums + 4 * kMaxPageGroups * (kMaxSources + 1), "and so do the weights");
-    const int ns = C + part.splits;
-    const size_t qrows = (size_t)R.rows * pool.heads * G, qr = (size_t)u * G;
-    for (int g = warp; g < G; g += kWarps) {
-        float2 x[(kMaxSources + 31) / 32];
-        float m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int i = 0; i < (kMaxSources + 31) / 32; ++i) {
-            const int k = lane + 32 * i;
-            x[i] = make_float2(-INFINITY, 0.f);
-            if (k < C) x[i] = make_float2(ld_cluster_f32(map_to_rank(&S.ml[g].x, k)), ld_cluster_f32(map_to_rank(&S.ml[g].y, k)));
-            else if (k < ns) x[i] = part.ml[(k - C) * qrows + qr + g];
-            m = fmaxf(m, x[i].x);
-        }
-        m = warp_max(m);
-        const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int i = 0; i < (kMaxSources + 31) / 32; ++i) {
-            const float a = ex2_approx(x[i].x - base);
-            l += a * x[i].y;
-            if (lane + 32 * i < ns) wt[g * kMaxSources + lane + 32 * i] = a;
-        }
-        l = warp_sum(l);
-        // no key at all: zero; a bad table entry has made l NaN
-        if (lane == 0) scale[g] = l == 0.f ? 0.f : 1.f / l;
-    }
-    __syncthreads();
     T* orow = static_cast<T*>(R.out) + (size_t)row * R.out_stride + (size_t)h * G * D;
-    for (int i = (rank * kNT + tid) * 4; i < G * D; i += C * kNT * 4) {
-        const int g = i / D;
-        const float* w = wt + g * kMaxSources;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float a, float4 x) {
-            o.x = fmaf(a, x.x, o.x);
-            o.y = fmaf(a, x.y, o.y);
-            o.z = fmaf(a, x.z, o.z);
-            o.w = fmaf(a, x.w, o.w);
-        };
-        for (int c = 0; c < C; ++c) add(w[c], ld_cluster_f4(map_to_rank(&sums[i], c)));
+    if (part.splits == 0) {
+        // four channels a thread: all that is to be joined is asked for at once
+        for (int i = (rank * kNT + tid) * 4; i < G * D; i += C * kNT * 4) {
+            float2 x[8];
+            float4 v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < C) {
+                    x[c] = ld_cluster_f2(map_to_rank(&S.ml[i / D], c));
+                    v[c] = ld_cluster_f4(map_to_rank(&sums[i], c));
+                }
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < C) m = fmaxf(m, x[c].x);
+            const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < C) {
+                    const float a = ex2_approx(x[c].x - base);
+                    l = fmaf(a, x[c].y, l);
+                    add4(o, a, v[c]);
+                }
+            // no key at all: zero; a bad table entry has made l NaN
+            const float f = l == 0.f ? 0.f : 1.f / l;
+            store4(orow + i, o.x * f, o.y * f, o.z * f, o.w * f);
+        }
+    } else {
+        const size_t qrows = (size_t)R.rows * pool.heads * G, qr = (size_t)u * G;
+        // weights of the sources: the cluster's CTAs, then the prefix's ranges
+        float* wt = reinterpret_cast<float*>(raw + 2 * kSums); // [G][sources]
+        float* scale = wt + kMaxPageGroups * kMaxSources;      // [G]
+        static_assert(kFront<T, D, kWarps> >= 2 * kSums + 4 * kMaxPageGroups * (kMaxSources + 1), "and so do the weights");
+        const int ns = C + part.splits;
+        for (int g = warp; g < G; g += kWarps) {
+            float2 x[(kMaxSources + 31) / 32];
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int i = 0; i < (kMaxSources + 31) / 32; ++i) {
+                const int k = lane + 32 * i;
+                x[i] = make_float2(-INFINITY, 0.f);
+                if (k < C) x[i] = ld_cluster_f2(map_to_rank(&S.ml[g], k));
+                else if (k < ns) x[i] = part.ml[(k - C) * qrows + qr + g];
+                m = fmaxf(m, x[i].x);
+            }
+            m = warp_max(m);
+            const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int i = 0; i < (kMaxSources + 31) / 32; ++i) {
+                const float a = ex2_approx(x[i].x - base);
+                l += a * x[i].y;
+                if (lane + 32 * i < ns) wt[g * kMaxSources + lane + 32 * i] = a;
+            }
+            l = warp_sum(l);
+            if (lane == 0) scale[g] = l == 0.f ? 0.f : 1.f / l;
+        }
+        __syncthreads();
+        for (int i = (rank * kNT + tid) * 4; i < G * D; i += C * kNT * 4) {
+            const int g = i / D;
+            const float* w = wt + g * kMaxSources;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < C; ++c) add4(o, w[c], ld_cluster_f4(map_to_rank(&sums[i], c)));
 #pragma unroll 8
-        for (int s = 0; s < part.splits; ++s) add(w[C + s], *reinterpret_cast<const float4*>(part.o + (s * qrows + qr) * D + i));
-        const float f = scale[g];
-        store4(orow + i, o.x * f, o.y * f, o.z * f, o.w * f);
+            for (int s = 0; s < part.splits; ++s) add4(o, w[C + s], *reinterpret_cast<const float4*>(part.o + (s * qrows + qr) * D + i));
+            const float f = scale[g];
+            store4(orow + i, o.x * f, o.y * f, o.z * f, o.w * f);
+        }
     }
     cluster_arrive();
     cluster_wait();                                        // no CTA leaves while another reads its sums
