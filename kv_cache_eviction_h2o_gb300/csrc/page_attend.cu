@@ -10,7 +10,7 @@
 // is the sum over the heads of the largest q_g . k that a key within page b's
 // bounds can have; summing the queries first makes it one product of length
 // 2 D a page whatever G is.  The page ranks are those of the exact s: scores
-// are made in fp32, whose error is at most eps = 24 * 2^-24 max_b sum |w||bound|
+// are made in fp32, whose error is at most eps = 24 * 2^-24 sum |w| max |bound|
 // (two chains of 16 fused multiply-adds a lane, 4 adds, one rounding of w: 21
 // roundings; the bound's own are far below the rest), a page more than 2 eps from the k-th largest is decided by that,
 // and the few nearer ones are scored again in fp64 and ranked by that, ties
@@ -39,6 +39,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool f
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void cluster_max_u32(uint32_t addr, uint32_t v)
 {
     asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -55,6 +62,36 @@ __device__ __forceinline__ uint32_t tile_at(int row, int byte)
 
 // -------------------------------------------------------------- picking
 
+// the largest |x| of 16-byte vectors, NaN where one is
+template <typename T> struct AbsMax;
+template <> struct AbsMax<__nv_bfloat16> {
+    uint32_t m = 0u;
+    __device__ __forceinline__ void take(uint4 v, bool on)
+    {
+        const uint32_t mask = on ? 0x7fff7fffu : 0u;
+        const uint32_t x[4] = {v.x & mask, v.y & mask, v.z & mask, v.w & mask};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x[i]));
+    }
+    __device__ __forceinline__ float value() const
+    {
+        float a = __uint_as_float(m << 16), b = __uint_as_float(m & 0xffff0000u);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+        return a;
+    }
+};
+template <> struct AbsMax<float> {
+    float m = 0.f;
+    __device__ __forceinline__ void take(uint4 v, bool on)
+    {
+        const uint32_t mask = on ? 0x7fffffffu : 0u;
+        const uint32_t x[4] = {v.x & mask, v.y & mask, v.z & mask, v.w & mask};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(__uint_as_float(x[i])));
+    }
+    __device__ __forceinline__ float value() const { return m; }
+};
+
 constexpr int kHold = 16;              // scores a thread keeps in registers
 constexpr int kFew = 32;               // open pages that are ranked one against another
 
@@ -64,8 +101,8 @@ struct PickSmem {
     unsigned long long key[kFew];      // the open pages' fp64 scores, and which they are
     int at[kFew];
     int n_open;
-    unsigned amax;                     // bits of the largest sum |w||bound| (of the whole cluster)
-    int count[kMaxTableWidth / 32];    // picked pages of each 32
+    unsigned amax;                     // bits of sum |w| times the largest |bound| (of the whole cluster)
+    int taken[NW];                     // picked pages of each warp's range
 };
 
 // sum over the CTA, in every thread; halves of 32 bits do not carry
@@ -143,9 +180,10 @@ struct Held {
 
 // Leaves s[j] >= the returned bound exactly for the `take` best of the n
 // pages' scores s (0 < take < n).  `again(j)` is page j's score in fp64, made
-// by a whole warp.  big: room for n keys of 64 bits; s may be overwritten.
-template <int NW, class Again>
-__device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned long long* big, Again again)
+// by a whole warp.  big: room for n keys of 64 bits; s may be overwritten,
+// after `settle`, which is called once.
+template <int NW, class Settle, class Again>
+__device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned long long* big, Settle settle, Again again)
 {
     constexpr int NT = NW * 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -177,6 +215,7 @@ __device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned
                 break;
             }
         }
+        settle();
         a = ~0u;                                           // the take-th score
         held.each([&](unsigned k) { if (k >= lo) a = min(a, k); });
         const float t = ord_value(cta_range(P, a, 0u, ph).x), e2 = __fmaf_ru(2.f * kEps, amax, 1e-37f);
@@ -210,6 +249,8 @@ __device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned
             __syncthreads();
             return below;
         }
+    } else {
+        settle();
     }
     // the open pages by their fp64 scores
     for (int j = warp; j < n; j += NW) {
@@ -499,13 +540,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(w), "f"(z));
     *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr)
 {
     float2 v;
@@ -582,15 +616,17 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             static_assert(kScan * NV * 512 <= 2 * TB, "a stage of bounds fits a stage of the ring");
             const T* bounds = static_cast<const T*>(pool.bounds);
             const int sub = lane & 7;                      // eight lanes a page
-            const int step = C * kWarps * 4 * kScan;
-            int j0 = (rank * kWarps + warp) * 4 * kScan;
+            // each CTA scores a range of the pages
+            const int chunk = ((ncand + C - 1) / C + 3) & ~3, jend = min(ncand, (rank + 1) * chunk);
+            const int step = kWarps * 4 * kScan;
+            int j0 = rank * chunk + warp * 4 * kScan;
             int pg[NS][kScan];
             auto ids = [&](int (&id)[kScan], int j) {
 #pragma unroll
-                for (int x = 0; x < kScan; ++x) id[x] = j + x * 4 + (lane >> 3) < ncand ? table[j + x * 4 + (lane >> 3)] : 0;
+                for (int x = 0; x < kScan; ++x) id[x] = j + x * 4 + (lane >> 3) < jend ? table[j + x * 4 + (lane >> 3)] : 0;
             };
             auto scan = [&](const int (&id)[kScan], int j, int stage) {
-                if (j < ncand)
+                if (j < jend)
 #pragma unroll
                     for (int x = 0; x < kScan; ++x) {
                         const bool ok = (unsigned)id[x] < (unsigned)pool.pages;
@@ -622,38 +658,43 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < N; ++e) w[i][e] = (float)S.w64[(i * 8 + sub) * N + e];
-            unsigned amax = 0u;
+            float w1 = 0.f;                                // sum |w|
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < N; ++e) w1 += fabsf(w[i][e]);
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) w1 += __shfl_xor_sync(0xffffffffu, w1, d);
+            AbsMax<T> most;
             cluster_wait();                                // every CTA has set its maximum
             int stage = 0;
-            for (; j0 < ncand; j0 += step) {
+            for (; j0 < jend; j0 += step) {
                 scan(pg[NS - 1], j0 + (NS - 1) * step, stage == 0 ? NS - 1 : stage - 1);
                 cp_wait<NS - 1>();
 #pragma unroll
                 for (int x = 0; x < kScan; ++x) {
                     float2 s2 = make_float2(0.f, 0.f);
-                    float a = 0.f;
+                    const int j = j0 + x * 4 + (lane >> 3);
+                    const bool in = j < jend;
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(ring + stage * 2 * TB + ((x * NV + i) * 32 + lane) * 16);
+                        most.take(v, in);
                         float f[N];
-                        load_vec<T, N>(reinterpret_cast<const T*>(ring + stage * 2 * TB + ((x * NV + i) * 32 + lane) * 16), f);
+                        load_vec<T, N>(reinterpret_cast<const T*>(&v), f);
 #pragma unroll
-                        for (int e = 0; e < N; e += 2) {
+                        for (int e = 0; e < N; e += 2)
                             s2 = __ffma2_rn(make_float2(w[i][e], w[i][e + 1]), make_float2(f[e], f[e + 1]), s2);
-                            a = fmaf(fabsf(w[i][e]), fabsf(f[e]), a);
-                            a = fmaf(fabsf(w[i][e + 1]), fabsf(f[e + 1]), a);
-                        }
                     }
                     float s = s2.x + s2.y;
 #pragma unroll
-                    for (int d = 4; d > 0; d >>= 1) {
-                        s += __shfl_xor_sync(0xffffffffu, s, d);
-                        a += __shfl_xor_sync(0xffffffffu, a, d);
-                    }
-                    if ((unsigned)pg[0][x] >= (unsigned)pool.pages) { s = NAN; a = NAN; }   // no such page: picked, and its row is NaN
-                    const int j = j0 + x * 4 + (lane >> 3);
-                    if (j < ncand) {
-                        amax = max(amax, __float_as_uint(fabsf(a)));
-                        for (int c = sub; c < C; c += 8) st_cluster_f32(map_to_rank(scores + j, c), s);
+                    for (int d = 4; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                    if (in) {
+                        if ((unsigned)pg[0][x] >= (unsigned)pool.pages) {   // no such page: picked, and its row is NaN
+                            s = NAN;
+                            most.take(make_uint4(~0u, 0u, 0u, 0u), true);
+                        }
+                        if (sub == 0) scores[j] = s;
                     }
                 }
 #pragma unroll
@@ -664,11 +705,19 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                 stage = stage + 1 == NS ? 0 : stage + 1;
             }
             cp_wait<0>();
-            amax = __reduce_max_sync(0xffffffffu, amax);
+            const unsigned amax = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(__fmul_ru(w1, most.value()))));
             if (lane < C) cluster_max_u32(map_to_rank(&S.pick.amax, lane), amax);
             cluster_arrive();
             cluster_wait();
-            const float bound = pick_bound(S.pick, scores, ncand, take, big, [&](int j) {
+            // the other CTAs' scores, 16 bytes a lane (a store to every CTA as each score was made took four times as long)
+#pragma unroll 4
+            for (int j = tid * 4; j < ncand; j += kNT * 4) {
+                const int owner = j / chunk;
+                if (owner != rank) *reinterpret_cast<float4*>(scores + j) = ld_cluster_f4(map_to_rank(scores + j, owner));
+            }
+            __syncthreads();
+            cluster_arrive();                              // (its wait: before scores are overwritten)
+            const float bound = pick_bound(S.pick, scores, ncand, take, big, [] { cluster_wait(); }, [&](int j) {
                 const int p = table[j];
                 if ((unsigned)p >= (unsigned)pool.pages) return (double)NAN;
                 const T* b = bounds + ((size_t)p * pool.heads + h) * 2 * D;
@@ -687,32 +736,37 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                 for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
                 return s;
             });
-            // the picked pages in order: counts of each 32, their running sums, places
-            const int n32 = (ncand + 31) >> 5;
-            for (int i = warp; i < n32; i += kWarps) {
-                const int j = i * 32 + lane;
-                const unsigned in = __ballot_sync(0xffffffffu, j < ncand && scores[j] >= bound);
-                if (lane == 0) S.pick.count[i] = __popc(in);
-            }
-            __syncthreads();
-            if (warp == 0)
-                for (int i0 = 0, sum = 0; i0 < n32; i0 += 32) {
-                    const int c = i0 + lane < n32 ? S.pick.count[i0 + lane] : 0;
-                    int x = c;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int y = __shfl_up_sync(0xffffffffu, x, d);
-                        if (lane >= d) x += y;
-                    }
-                    if (i0 + lane < n32) S.pick.count[i0 + lane] = sum + x - c;
-                    sum += __shfl_sync(0xffffffffu, x, 31);
+            // the picked pages in order: each warp takes a range, each lane the marks of 32 pages at a time
+            const int n32 = (ncand + 31) >> 5, w32 = (n32 + kWarps - 1) / kWarps, g0 = min(n32, warp * w32), g1 = min(n32, g0 + w32);
+            auto marks = [&](int g) {                      // lane i: those of group g + i
+                unsigned mine = 0u;
+                for (int i = 0; i < min(32, g1 - g); ++i) {
+                    const int j = (g + i) * 32 + lane;
+                    const unsigned in = __ballot_sync(0xffffffffu, j < ncand && scores[j] >= bound);
+                    if (lane == i) mine = in;
                 }
+                return mine;
+            };
+            int count = 0;
+            const unsigned first = marks(g0);
+            for (int g = g0; g < g1; g += 32) count += __popc(g == g0 ? first : marks(g));
+            count = __reduce_add_sync(0xffffffffu, count);
+            if (lane == 0) S.pick.taken[warp] = count;
             __syncthreads();
-            for (int i = warp; i < n32; i += kWarps) {
-                const int j = i * 32 + lane;
-                const bool is_in = j < ncand && scores[j] >= bound;
-                const unsigned in = __ballot_sync(0xffffffffu, is_in);
-                if (is_in) list[S.pick.count[i] + __popc(in & ((1u << lane) - 1u))] = j;
+            int at = 0;
+            for (int k = 0; k < warp; ++k) at += S.pick.taken[k];
+            for (int g = g0; g < g1; g += 32) {
+                unsigned in = g == g0 ? first : marks(g);
+                const int c = __popc(in);
+                int x = c;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, d);
+                    if (lane >= d) x += y;
+                }
+                int to = at + x - c;
+                for (; in; in &= in - 1) list[to++] = (g + lane) * 32 + __ffs(in) - 1;
+                at += __shfl_sync(0xffffffffu, x, 31);
             }
             __syncthreads();
         }
