@@ -103,6 +103,7 @@ struct PickSmem {
     int n_open;
     unsigned amax;                     // bits of sum |w| times the largest |bound| (of the whole cluster)
     int taken[NW];                     // picked pages of each warp's range
+    unsigned mark[kMaxTableWidth / 32];   // which pages are picked
 };
 
 // sum over the CTA, in every thread; halves of 32 bits do not carry
@@ -151,30 +152,26 @@ __device__ __forceinline__ float ord_value(unsigned k)
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// f(key) for this thread's pages j = tid, tid + NT, ..: from registers where all scores fit them
+// f(key) for this thread's pages: from registers while all scores fit them (1900 pages: 2.1 us of search, 3.2 from
+// shared memory)
 template <int NT>
 struct Held {
     unsigned k[kHold];
     const float* s;
     int n;
-    bool regs;
-    __device__ __forceinline__ Held(const float* s_, int n_) : s(s_), n(n_), regs(n_ <= kHold * NT)
+    __device__ __forceinline__ Held(const float* s_, int n_) : s(s_), n(n_)
     {
-        if (regs)
 #pragma unroll
-            for (int i = 0; i < kHold; ++i) {
-                const int j = (int)threadIdx.x + i * NT;
-                k[i] = j < n ? ord_key(s[j]) : 0u;         // (0: below every score)
-            }
+        for (int i = 0; i < kHold; ++i) {
+            const int j = (int)threadIdx.x + i * NT;
+            k[i] = j < n ? ord_key(s[j]) : 0u;             // (0: below every score)
+        }
     }
     template <class F> __device__ __forceinline__ void each(F f) const
     {
-        if (regs) {
 #pragma unroll
-            for (int i = 0; i < kHold; ++i) f(k[i]);
-        } else {
-            for (int j = threadIdx.x; j < n; j += NT) f(ord_key(s[j]));
-        }
+        for (int i = 0; i < kHold; ++i) f(k[i]);
+        for (int j = threadIdx.x + kHold * NT; j < n; j += NT) f(ord_key(s[j]));
     }
 };
 
@@ -194,7 +191,7 @@ __device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned
     if (amax < FLT_MAX) {                                  // (an infinity or NaN among the factors decides nothing)
         const Held<NT> held(s, n);
         unsigned a = ~0u, b = 0u;
-        held.each([&](unsigned k) { if (k) { a = min(a, k); b = max(b, k); } });
+        held.each([&](unsigned k) { a = min(a, k ? k : ~0u); b = max(b, k); });
         const uint2 r = cta_range(P, a, b, ph);
         // count(key >= lo) >= take > count(key >= hi): three keys between them a step
         unsigned long long lo = r.x, hi = (unsigned long long)r.y + 1;
@@ -556,7 +553,7 @@ __device__ __forceinline__ void add4(float4& o, float a, float4 x)
 
 template <int D, class Core>
 struct alignas(16) AttendSmem {
-    double w64[2 * D];                 // the page weights, minima's then maxima's
+    float2 w[2 * D];                   // the page weights, minima's then maxima's, as sums hi + lo
     typename Core::Shared core;
     float2 wml[Core::kWarps][kMaxPageGroups];
     float2 ml[kMaxPageGroups];
@@ -620,36 +617,34 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             const int chunk = ((ncand + C - 1) / C + 3) & ~3, jend = min(ncand, (rank + 1) * chunk);
             const int step = kWarps * 4 * kScan;
             int j0 = rank * chunk + warp * 4 * kScan;
-            int pg[NS][kScan];
-            auto ids = [&](int (&id)[kScan], int j) {
-#pragma unroll
-                for (int x = 0; x < kScan; ++x) id[x] = j + x * 4 + (lane >> 3) < jend ? table[j + x * 4 + (lane >> 3)] : 0;
-            };
-            auto scan = [&](const int (&id)[kScan], int j, int stage) {
+            // each page's id waits in the place of its score
+            for (int j = rank * chunk + tid; j < jend; j += kNT) scores[j] = __int_as_float(table[j]);
+            __syncthreads();
+            auto scan = [&](int j, int stage) {
                 if (j < jend)
 #pragma unroll
                     for (int x = 0; x < kScan; ++x) {
-                        const bool ok = (unsigned)id[x] < (unsigned)pool.pages;
-                        const T* from = bounds + ((size_t)(ok ? id[x] : 0) * pool.heads + h) * 2 * D + sub * N;
+                        const int p = j + x * 4 + (lane >> 3), id = p < jend ? __float_as_int(scores[p]) : 0;
+                        const bool ok = (unsigned)id < (unsigned)pool.pages;
+                        const T* from = bounds + ((size_t)(ok ? id : 0) * pool.heads + h) * 2 * D + sub * N;
 #pragma unroll
                         for (int i = 0; i < NV; ++i)
                             cp_async16(smem_u32(ring + stage * 2 * TB + ((x * NV + i) * 32 + lane) * 16), from + i * 8 * N, true);
                     }
                 cp_commit();
             };
-#pragma unroll
-            for (int k = 0; k < NS; ++k) ids(pg[k], j0 + k * step);
-#pragma unroll
-            for (int k = 0; k < NS - 1; ++k) scan(pg[k], j0 + k * step, k);
+#pragma unroll 1
+            for (int k = 0; k < NS - 1; ++k) scan(j0 + k * step, k);
             if (tid == 0) S.pick.amax = 0u;
+            // (fp32 pairs hold the sums as well as fp64 would, whose pipe is so narrow that its conversions took 3 us here)
             for (int i = tid; i < 2 * D; i += kNT) {
-                double s = 0.0;
+                float2 s = make_float2(0.f, 0.f);
                 const bool lo = i < D;
                 for (int g = 0; g < G; ++g) {
                     const float x = Elem<T>::to_f(qrow[g * D + (lo ? i : i - D)]);
-                    s += (double)(lo ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x));
+                    s = pair_add(s, lo ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x));
                 }
-                S.w64[i] = s;
+                S.w[i] = s;
             }
             __syncthreads();
             cluster_arrive();
@@ -657,7 +652,7 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < N; ++e) w[i][e] = (float)S.w64[(i * 8 + sub) * N + e];
+                for (int e = 0; e < N; ++e) w[i][e] = S.w[(i * 8 + sub) * N + e].x;
             float w1 = 0.f;                                // sum |w|
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -668,8 +663,9 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             AbsMax<T> most;
             cluster_wait();                                // every CTA has set its maximum
             int stage = 0;
+#pragma unroll 1
             for (; j0 < jend; j0 += step) {
-                scan(pg[NS - 1], j0 + (NS - 1) * step, stage == 0 ? NS - 1 : stage - 1);
+                scan(j0 + (NS - 1) * step, stage == 0 ? NS - 1 : stage - 1);
                 cp_wait<NS - 1>();
 #pragma unroll
                 for (int x = 0; x < kScan; ++x) {
@@ -689,19 +685,14 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                     float s = s2.x + s2.y;
 #pragma unroll
                     for (int d = 4; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                    if (in) {
-                        if ((unsigned)pg[0][x] >= (unsigned)pool.pages) {   // no such page: picked, and its row is NaN
+                    if (in && sub == 0) {
+                        if (__float_as_uint(scores[j]) >= (unsigned)pool.pages) {   // no such page: picked, and its row is NaN
                             s = NAN;
                             most.take(make_uint4(~0u, 0u, 0u, 0u), true);
                         }
-                        if (sub == 0) scores[j] = s;
+                        scores[j] = s;
                     }
                 }
-#pragma unroll
-                for (int x = 0; x < kScan; ++x)
-#pragma unroll
-                    for (int k = 0; k < NS - 1; ++k) pg[k][x] = pg[k + 1][x];
-                ids(pg[NS - 1], j0 + NS * step);
                 stage = stage + 1 == NS ? 0 : stage + 1;
             }
             cp_wait<0>();
@@ -723,7 +714,7 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                 const T* b = bounds + ((size_t)p * pool.heads + h) * 2 * D;
                 double s = 0.0;
                 if (__uint_as_float(S.pick.amax) < FLT_MAX) {
-                    for (int e = lane; e < 2 * D; e += 32) s += S.w64[e] * (double)Elem<T>::to_f(b[e]);
+                    for (int e = lane; e < 2 * D; e += 32) s += ((double)S.w[e].x + (double)S.w[e].y) * (double)Elem<T>::to_f(b[e]);
                 } else {
                     // an infinite bound on the side that no query takes counts for nothing: the maxima themselves
                     for (int e = lane; e < D; e += 32)
@@ -738,25 +729,21 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             });
             // the picked pages in order: each warp takes a range, each lane the marks of 32 pages at a time
             const int n32 = (ncand + 31) >> 5, w32 = (n32 + kWarps - 1) / kWarps, g0 = min(n32, warp * w32), g1 = min(n32, g0 + w32);
-            auto marks = [&](int g) {                      // lane i: those of group g + i
-                unsigned mine = 0u;
-                for (int i = 0; i < min(32, g1 - g); ++i) {
-                    const int j = (g + i) * 32 + lane;
-                    const unsigned in = __ballot_sync(0xffffffffu, j < ncand && scores[j] >= bound);
-                    if (lane == i) mine = in;
-                }
-                return mine;
-            };
             int count = 0;
-            const unsigned first = marks(g0);
-            for (int g = g0; g < g1; g += 32) count += __popc(g == g0 ? first : marks(g));
-            count = __reduce_add_sync(0xffffffffu, count);
+#pragma unroll 4
+            for (int g = g0; g < g1; ++g) {
+                const int j = g * 32 + lane;
+                const unsigned in = __ballot_sync(0xffffffffu, j < ncand && scores[j] >= bound);
+                if (lane == 0) S.pick.mark[g] = in;
+                count += __popc(in);
+            }
             if (lane == 0) S.pick.taken[warp] = count;
             __syncthreads();
             int at = 0;
             for (int k = 0; k < warp; ++k) at += S.pick.taken[k];
+#pragma unroll 1
             for (int g = g0; g < g1; g += 32) {
-                unsigned in = g == g0 ? first : marks(g);
+                unsigned in = g + lane < g1 ? S.pick.mark[g + lane] : 0u;
                 const int c = __popc(in);
                 int x = c;
 #pragma unroll
@@ -814,11 +801,12 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
         }
         cp_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < NS - 1; ++s) ask(t0 + s * stride, s);
     Core core;
     core.init(S.core, qrow, G);
     int stage = 0;
+#pragma unroll 1
     for (int t = t0; t < ntiles; t += stride) {
         ask(t + (NS - 1) * stride, stage == 0 ? NS - 1 : stage - 1);
         cp_wait<NS - 1>();
