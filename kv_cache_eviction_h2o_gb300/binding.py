@@ -373,62 +373,91 @@ def h2o_prompt_scores_noalloc(Q, K, batch, heads, T, head_dim, dtype, scale, c, 
 
 
 # ------------------------------------------------------------- paged caches
+#
+# A decode step's kernels take a few microseconds, so the checks are made of
+# the cheapest comparisons there are; what is wrong is found out afterwards.
 
 _CODES = {"torch.bfloat16": H2O_BF16, "torch.float32": H2O_F32}
+_types = None          # (int32, uint8, {element type: its code}, the current device's index)
 
 
-def _tensor(x, what, dtype, shape, device):
-    """x is a contiguous tensor of `dtype` and `shape` (None: any size) on `device`."""
+def _torch_types():
+    global _types
+    if _types is None:
+        import torch
+        _types = (torch.int32, torch.uint8, {getattr(torch, k[6:]): v for k, v in _CODES.items()}, torch.cuda.current_device)
+    return _types
+
+
+def _wrong(x, what, dtype, shape, device):
+    """Raise for a tensor that is not a contiguous one of `dtype` and `shape` on `device`."""
     if not hasattr(x, "data_ptr"):
         raise TypeError("%s must be a tensor" % what)
     if x.dtype is not dtype:
         raise TypeError("%s must be of dtype %s (got %s)" % (what, dtype, x.dtype))
-    if x.device != device:
-        raise ValueError("%s must be on %s (got %s)" % (what, device, x.device))
-    if len(x.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
+    if x.get_device() != device:
+        raise ValueError("%s must be on %s (got %s)" % (what, "cuda:%d" % device if device >= 0 else "the CPU", x.device))
+    if x.shape != shape:
         raise ValueError("%s must have shape %s (got %s)" % (what, list(shape), list(x.shape)))
-    if not x.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return x.data_ptr()
+    raise ValueError("%s must be contiguous" % what)
+
+
+def _tensor(x, what, dtype, shape, device):
+    """The pointer of a contiguous tensor of `dtype` and `shape` on device `device`."""
+    try:
+        if x.dtype is dtype and x.shape == shape and x.get_device() == device and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _wrong(x, what, dtype, shape, device)
 
 
 def _head_rows(x, what, dtype, shape, device):
     """Pointer and row stride of [rows][heads][channels] whose rows may lie apart."""
-    if not hasattr(x, "data_ptr"):
+    try:
+        if x.dtype is dtype and x.shape == shape and x.get_device() == device:
+            rows, heads, d = shape
+            s = x.stride()
+            if s[2] != 1 or (heads > 1 and s[1] != d):
+                raise ValueError("%s must have contiguous heads and channels" % what)
+            return x.data_ptr(), s[0] if rows > 1 else heads * d
+    except AttributeError:
+        pass
+    _wrong(x, what, dtype, shape, device)
+
+
+def _dim(x, what, rank):
+    """x's shape, which has `rank` dimensions."""
+    shape = getattr(x, "shape", None)
+    if shape is None or not hasattr(x, "data_ptr"):
         raise TypeError("%s must be a tensor" % what)
-    if x.dtype is not dtype:
-        raise TypeError("%s must be of dtype %s (got %s)" % (what, dtype, x.dtype))
-    if x.device != device:
-        raise ValueError("%s must be on %s (got %s)" % (what, device, x.device))
-    if tuple(x.shape) != shape:
-        raise ValueError("%s must have shape %s (got %s)" % (what, list(shape), list(x.shape)))
-    width = shape[1] * shape[2]
-    s = x.stride()
-    if s[2] != 1 or (shape[1] > 1 and s[1] != shape[2]):
-        raise ValueError("%s must have contiguous heads and channels" % what)
-    return x.data_ptr(), s[0] if shape[0] > 1 else width
+    if len(shape) != rank:
+        raise ValueError("%s must have %d dimensions (got %s)" % (what, rank, list(shape)))
+    return shape
+
+
+def _on_current(x, current):
+    """The index of the GPU that x is on, which is the current device."""
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("tensors must be on the GPU (got %s)" % x.device)
+    if device != current():
+        raise ValueError("tensors are on cuda:%d, which is not the current device" % device)
+    return device
 
 
 def _pool(K, V):
-    """(device, element type, its code, pages, heads, page size, channels) of a page pool."""
-    code = _CODES.get(str(getattr(K, "dtype", None)))
+    """(device, element type, its code, K's and V's pointers, K's shape) of a page pool."""
+    types = _torch_types()
+    shape = getattr(K, "shape", None)
+    code = types[2].get(getattr(K, "dtype", None))
     if code is None:
         raise TypeError("K must be a tensor of dtype float32 or bfloat16 (got %s)" % getattr(K, "dtype", type(K)))
-    if K.dim() != 4:
-        raise ValueError("K must be [pages][kv_heads][page_size][head_dim] (got %s)" % list(K.shape))
-    device, shape = K.device, tuple(K.shape)
-    _on_current(device)
-    _tensor(K, "K", K.dtype, shape, device)
-    _tensor(V, "V", K.dtype, shape, device)
-    return (device, K.dtype, code) + shape
-
-
-def _on_current(device):
-    import torch
-    if device.type != "cuda":
-        raise ValueError("tensors must be on the GPU (got %s)" % device)
-    if device.index != torch.cuda.current_device():
-        raise ValueError("tensors are on %s, which is not the current device" % device)
+    if len(shape) != 4:
+        raise ValueError("K must be [pages][kv_heads][page_size][head_dim] (got %s)" % list(shape))
+    device = _on_current(K, types[3])
+    dt = K.dtype
+    return device, dt, code, _tensor(K, "K", dt, shape, device), _tensor(V, "V", dt, shape, device), shape
 
 
 def h2o_page_tables(len_before, n_new, free_pages, page_size, table, len_after, row_start, row_seq, row_pos, slot, status,
@@ -437,55 +466,58 @@ def h2o_page_tables(len_before, n_new, free_pages, page_size, table, len_after, 
     len_before, n_new, len_after [requests], free_pages [any], table
     [requests][width], row_start [requests + 1], row_seq, row_pos, slot
     [rows_cap], status [4]."""
-    import torch
-    i32, n, dev = torch.int32, len_before.shape[0], len_before.device
-    _on_current(dev)
-    p = [_tensor(len_before, "len_before", i32, (n,), dev), _tensor(n_new, "n_new", i32, (n,), dev),
-         _tensor(free_pages, "free_pages", i32, (None,), dev), _tensor(table, "table", i32, (n, None), dev),
-         _tensor(len_after, "len_after", i32, (n,), dev), _tensor(row_start, "row_start", i32, (n + 1,), dev)]
-    cap = slot.shape[0]
-    q = [_tensor(row_seq, "row_seq", i32, (cap,), dev), _tensor(row_pos, "row_pos", i32, (cap,), dev),
-         _tensor(slot, "slot", i32, (cap,), dev)]
-    _check(lib().h2o_page_tables(p[0], p[1], n, p[2], free_pages.shape[0], page_size, p[3], table.shape[1], p[4], p[5],
-                                 q[0], q[1], q[2], cap, _tensor(status, "status", i32, (4,), dev), _stream(stream)))
+    i32, _, _, current = _torch_types()
+    per, free, cap = _dim(len_before, "len_before", 1), _dim(free_pages, "free_pages", 1), _dim(slot, "slot", 1)
+    n, wide = per[0], _dim(table, "table", 2)
+    dev = _on_current(len_before, current)
+    rc = lib().h2o_page_tables(
+        _tensor(len_before, "len_before", i32, per, dev), _tensor(n_new, "n_new", i32, per, dev), n,
+        _tensor(free_pages, "free_pages", i32, free, dev), free[0], page_size,
+        _tensor(table, "table", i32, (n, wide[1]), dev), wide[1], _tensor(len_after, "len_after", i32, per, dev),
+        _tensor(row_start, "row_start", i32, (n + 1,), dev), _tensor(row_seq, "row_seq", i32, cap, dev),
+        _tensor(row_pos, "row_pos", i32, cap, dev), _tensor(slot, "slot", i32, cap, dev), cap[0],
+        _tensor(status, "status", i32, (4,), dev), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def h2o_page_write(k, v, slot, K, V, bounds, stream=None):
     """Key and value rows [rows][kv_heads][head_dim] into their slots; see include/h2o.h."""
-    import torch
-    dev, dt, code, pages, heads, ps, d = _pool(K, V)
-    rows = slot.shape[0]
-    kp, ks = _head_rows(k, "k", dt, (rows, heads, d), dev)
-    vp, vs = _head_rows(v, "v", dt, (rows, heads, d), dev)
-    _check(lib().h2o_page_write(kp, vp, ks, vs, _tensor(slot, "slot", torch.int32, (rows,), dev), rows, K.data_ptr(),
-                                V.data_ptr(), _tensor(bounds, "bounds", dt, (pages, heads, 2, d), dev), pages, heads, ps, d,
-                                code, _stream(stream)))
+    dev, dt, code, Kp, Vp, (pages, heads, ps, d) = _pool(K, V)
+    rows = _dim(slot, "slot", 1)
+    kp, ks = _head_rows(k, "k", dt, (rows[0], heads, d), dev)
+    vp, vs = _head_rows(v, "v", dt, (rows[0], heads, d), dev)
+    rc = lib().h2o_page_write(kp, vp, ks, vs, _tensor(slot, "slot", _types[0], rows, dev), rows[0], Kp, Vp,
+                              _tensor(bounds, "bounds", dt, (pages, heads, 2, d), dev), pages, heads, ps, d, code,
+                              _stream(stream))
+    if rc:
+        _check(rc)
 
 
-def _query_rows(q, row_seq, row_pos, table, out, pool):
-    import torch
-    dev, dt, _, _, heads, _, d = pool
-    rows, i32 = row_seq.shape[0], torch.int32
-    hq = q.shape[1] if q.dim() == 3 else 0
+def _query_rows(q, row_seq, row_pos, table, out, dev, dt, heads, d):
+    i32 = _types[0]
+    rows, wide = _dim(row_seq, "row_seq", 1), _dim(table, "table", 2)
+    hq = _dim(q, "q", 3)[1]
     if hq < 1 or hq % heads:
         raise ValueError("q must be [rows][kv_heads * groups][head_dim] (got %s for %d cache heads)" % (list(q.shape), heads))
-    qp, qs = _head_rows(q, "q", dt, (rows, hq, d), dev)
-    op, os_ = _head_rows(out, "out", dt, (rows, hq, d), dev)
-    return (qp, qs, _tensor(row_seq, "row_seq", i32, (rows,), dev), _tensor(row_pos, "row_pos", i32, (rows,), dev), rows,
-            hq // heads, _tensor(table, "table", i32, (None, None), dev), op, os_)
+    shape = (rows[0], hq, d)
+    qp, qs = _head_rows(q, "q", dt, shape, dev)
+    op, os_ = _head_rows(out, "out", dt, shape, dev)
+    return (qp, qs, _tensor(row_seq, "row_seq", i32, rows, dev), _tensor(row_pos, "row_pos", i32, rows, dev), rows[0],
+            hq // heads, _tensor(table, "table", i32, wide, dev), wide[0], wide[1], op, os_)
 
 
 def h2o_page_attend(q, row_seq, row_pos, K, V, bounds, table, budget, recent, scale, out, picked=None, stream=None):
     """Attention over the `recent` newest pages and the best-scoring others;
     see include/h2o.h."""
-    import torch
-    pool = _pool(K, V)
-    dev, dt, code, pages, heads, ps, d = pool
-    qp, qs, sp, pp, rows, groups, tp, op, os_ = _query_rows(q, row_seq, row_pos, table, out, pool)
+    dev, dt, code, Kp, Vp, (pages, heads, ps, d) = _pool(K, V)
+    qp, qs, sp, pp, rows, groups, tp, n, width, op, os_ = _query_rows(q, row_seq, row_pos, table, out, dev, dt, heads, d)
     bp = None if bounds is None else _tensor(bounds, "bounds", dt, (pages, heads, 2, d), dev)
-    kp = None if picked is None else _tensor(picked, "picked", torch.int32, (rows, heads, budget), dev)
-    _check(lib().h2o_page_attend(qp, qs, sp, pp, rows, K.data_ptr(), V.data_ptr(), bp, pages, heads, groups, ps, d, code, tp,
-                                 table.shape[0], table.shape[1], budget, recent, float(scale), op, os_, kp, _stream(stream)))
+    kp = None if picked is None else _tensor(picked, "picked", _types[0], (rows, heads, budget), dev)
+    rc = lib().h2o_page_attend(qp, qs, sp, pp, rows, Kp, Vp, bp, pages, heads, groups, ps, d, code, tp, n, width, budget,
+                               recent, scale, op, os_, kp, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def h2o_prefix_work_bytes(rows, kv_heads, groups, head_dim, prefix_len, dtype):
@@ -498,15 +530,16 @@ def h2o_prefix_work_bytes(rows, kv_heads, groups, head_dim, prefix_len, dtype):
 def h2o_prefix_attend(q, row_seq, row_pos, K, V, prefix_table, prefix_len, table, scale, out, work, stream=None):
     """Attention over a prefix that all rows share and each request's own
     pages; work: a uint8 tensor of h2o_prefix_work_bytes.  See include/h2o.h."""
-    import torch
-    pool = _pool(K, V)
-    dev, dt, code, pages, heads, ps, d = pool
-    qp, qs, sp, pp, rows, groups, tp, op, os_ = _query_rows(q, row_seq, row_pos, table, out, pool)
+    dev, dt, code, Kp, Vp, (pages, heads, ps, d) = _pool(K, V)
+    qp, qs, sp, pp, rows, groups, tp, n, width, op, os_ = _query_rows(q, row_seq, row_pos, table, out, dev, dt, heads, d)
     xp = None
     if prefix_table is not None:
-        xp = _tensor(prefix_table, "prefix_table", torch.int32, (None,), dev)
-        if prefix_table.shape[0] * ps < prefix_len:
-            raise ValueError("prefix_table lists %d pages of %d tokens, prefix_len is %d" % (prefix_table.shape[0], ps, prefix_len))
-    _check(lib().h2o_prefix_attend(qp, qs, sp, pp, rows, K.data_ptr(), V.data_ptr(), pages, heads, groups, ps, d, code, xp,
-                                   prefix_len, tp, table.shape[0], table.shape[1], float(scale), op, os_,
-                                   _tensor(work, "work", torch.uint8, (None,), dev), work.shape[0], _stream(stream)))
+        listed = _dim(prefix_table, "prefix_table", 1)
+        xp = _tensor(prefix_table, "prefix_table", _types[0], listed, dev)
+        if listed[0] * ps < prefix_len:
+            raise ValueError("prefix_table lists %d pages of %d tokens, prefix_len is %d" % (listed[0], ps, prefix_len))
+    size = _dim(work, "work", 1)
+    rc = lib().h2o_prefix_attend(qp, qs, sp, pp, rows, Kp, Vp, pages, heads, groups, ps, d, code, xp, prefix_len, tp, n,
+                                 width, scale, op, os_, _tensor(work, "work", _types[1], size, dev), size[0], _stream(stream))
+    if rc:
+        _check(rc)

@@ -939,7 +939,8 @@ cudaError_t go(const PagePool& p, const PageRows& r, int budget, int recent, int
     const int front = std::max(kFront<T, D, NW>, 8 * wpad);
     const size_t smem = front + sizeof(AttendSmem<D, Core>) + 4 * ((size_t)wpad + (picks ? budget : 0));
     const auto kernel = page_attend_kernel<T, D, Core>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemOnce once;
+    const cudaError_t e = once.allow(kernel);
     if (e != cudaSuccess) return e;
     const long long units = (long long)r.rows * p.heads;
     const int C = cluster_of(units, (budget > 0 ? std::min(budget, r.width) : r.width) * (p.ps / kKeys), (int)(227 * 1024 / (smem + 1024)) * kSMs, NW);

@@ -264,8 +264,8 @@ cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t st)
     const int grid = (int)std::min<long long>(152, std::max<long long>(1, (work + threads - 1) / threads));
     const size_t smem = 2 * sizeof(int) * ((size_t)a.n + 1);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   2 * (int)sizeof(int) * (kMaxPageRequests + 1));
+        static SmemOnce once;
+        const cudaError_t e = once.allow(page_tables_kernel);
         if (e != cudaSuccess) return e;
     }
     page_tables_kernel<<<grid, threads, smem, st>>>(a);

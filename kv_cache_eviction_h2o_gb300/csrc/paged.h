@@ -13,6 +13,26 @@ constexpr int kMaxPickedPages = 4096;     // budget of a call that has to choose
 constexpr int kMaxPageGroups = 16;        // query heads per cache head
 constexpr int kMaxPrefixSplits = 64;      // ranges of a shared prefix
 
+// Lets a kernel use all shared memory a CTA can have, once per device (a
+// kernel's own static object, so a race between threads sets the same twice).
+struct SmemOnce {
+    bool done[64] = {};
+    template <class Kernel> cudaError_t allow(Kernel* kernel)
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        if (done[dev]) return cudaSuccess;
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, kernel);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - (int)a.sharedSizeBytes);
+        if (e == cudaSuccess) done[dev] = true;
+        return e;
+    }
+};
+
 // The page pool: K, V [pages][heads][ps][D], bounds [pages][heads][2][D].
 struct PagePool {
     void* K;

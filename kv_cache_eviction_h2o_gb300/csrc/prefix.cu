@@ -188,7 +188,8 @@ cudaError_t launch_prefix(const PagePool& p, const PageRows& r, const int* prefi
     auto go = [&](auto d) {
         constexpr int D = decltype(d)::value;
         const int smem = (int)sizeof(SimtSmem<D>);
-        const cudaError_t e = cudaFuncSetAttribute(prefix_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static SmemOnce once;
+        const cudaError_t e = once.allow(prefix_simt_kernel<D>);
         if (e != cudaSuccess) return e;
         prefix_simt_kernel<D><<<grid, 256, smem, st>>>(p, r, prefix_table, prefix_len, per, part);
         return cudaGetLastError();

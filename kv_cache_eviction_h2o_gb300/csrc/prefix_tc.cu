@@ -491,7 +491,8 @@ cudaError_t go(const PagePool& p, const PageRows& r, const int* table, int prefi
     const int per = prefix_tc_range(r.rows, p.heads, r.G, prefix_len);
     const dim3 grid((unsigned)(((long long)r.rows * r.G + 2 * kT - 1) / (2 * kT)), (unsigned)part.splits, (unsigned)p.heads);
     const int smem = (int)sizeof(Smem<D>) + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOnce once;
+    const cudaError_t e = once.allow(prefix_tc_kernel<D>);
     if (e != cudaSuccess) return e;
     prefix_tc_kernel<D><<<grid, kThreads, smem, st>>>(mk, mv, p, r, table, prefix_len, per, part);
     return cudaGetLastError();

@@ -116,7 +116,7 @@ def test_binding_wants_gpu_tensors_of_fitting_shapes(L):
         L.h2o_page_write(i, i, i, K.half(), K.half(), K)
     with pytest.raises(ValueError, match="pages"):
         L.h2o_page_write(i, i, i, K[0], K[0], K)
-    cpu = torch.device("cpu")
+    cpu = -1               # get_device() of a CPU tensor
     with pytest.raises(ValueError, match="shape"):
         L._tensor(i, "slot", torch.int32, (4,), cpu)
     with pytest.raises(TypeError, match="dtype"):
