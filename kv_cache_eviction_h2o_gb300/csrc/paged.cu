@@ -129,33 +129,48 @@ __global__ void page_tables_kernel(const TablesArgs a)
     }
     // four rows a thread, written as 16 bytes where the maps lie on them
     const bool wide = (((size_t)a.row_seq | (size_t)a.row_pos | (size_t)a.slot) & 15) == 0;
-    for (int x0 = g; x0 < (a.cap + 3) / 4; x0 += stride) {
-        int seq[4], pos[4], slot[4];
-        int i = x0 * 4 < rows ? owner_of(start, a.n, x0 * 4) : 0;
+    const int last = (INT_MAX - a.ps) >> sh;
+    for (int x0 = g * 4; x0 < a.cap; x0 += stride * 4) {
+        int4 seq = make_int4(-1, -1, -1, -1), pos = seq, slot = seq;
+        if (x0 < rows) {
+            int i = owner_of(start, a.n, x0);
+            // the page of position `at` of request i; a table or free-list entry that is no page gives no slot
+            auto slot_of = [&](int at) {
+                const int owned = (a.before[i] + a.ps - 1) >> sh, pg = at >> sh;
+                const int page = pg < owned ? a.table[(size_t)i * a.width + pg] : a.free_pages[first[i] + pg - owned];
+                return page >= 0 && page <= last ? (page << sh) + (at & (a.ps - 1)) : -1;
+            };
+            const int at = a.before[i] + (x0 - start[i]);
+            if (x0 + 4 <= start[i + 1] && (at & (a.ps - 1)) <= a.ps - 4) {
+                // all in one page of one request, as most are
+                const int s = slot_of(at);
+                seq = make_int4(i, i, i, i);
+                pos = make_int4(at, at + 1, at + 2, at + 3);
+                if (s >= 0) slot = make_int4(s, s + 1, s + 2, s + 3);
+            } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int x = x0 * 4 + j;
-            seq[j] = pos[j] = slot[j] = -1;
-            if (x >= rows) continue;
-            while (start[i + 1] <= x) ++i;
-            const int b = a.before[i], at = b + (x - start[i]), owned = (b + a.ps - 1) >> sh, pg = at >> sh;
-            const int page = pg < owned ? a.table[(size_t)i * a.width + pg] : a.free_pages[first[i] + pg - owned];
-            seq[j] = i;
-            pos[j] = at;
-            // a table or free-list entry that is no page gives no slot
-            slot[j] = page >= 0 && page <= ((INT_MAX - a.ps) >> sh) ? (page << sh) + (at & (a.ps - 1)) : -1;
+                for (int j = 0; j < 4; ++j) {
+                    const int x = x0 + j;
+                    if (x >= rows) break;
+                    while (start[i + 1] <= x) ++i;
+                    const int y = a.before[i] + (x - start[i]);
+                    (&seq.x)[j] = i;
+                    (&pos.x)[j] = y;
+                    (&slot.x)[j] = slot_of(y);
+                }
+            }
         }
-        if (wide && x0 * 4 + 4 <= a.cap) {
-            reinterpret_cast<int4*>(a.row_seq)[x0] = make_int4(seq[0], seq[1], seq[2], seq[3]);
-            reinterpret_cast<int4*>(a.row_pos)[x0] = make_int4(pos[0], pos[1], pos[2], pos[3]);
-            reinterpret_cast<int4*>(a.slot)[x0] = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        if (wide && x0 + 4 <= a.cap) {
+            *reinterpret_cast<int4*>(a.row_seq + x0) = seq;
+            *reinterpret_cast<int4*>(a.row_pos + x0) = pos;
+            *reinterpret_cast<int4*>(a.slot + x0) = slot;
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (x0 * 4 + j >= a.cap) break;
-                a.row_seq[x0 * 4 + j] = seq[j];
-                a.row_pos[x0 * 4 + j] = pos[j];
-                a.slot[x0 * 4 + j] = slot[j];
+                if (x0 + j >= a.cap) break;
+                a.row_seq[x0 + j] = (&seq.x)[j];
+                a.row_pos[x0 + j] = (&pos.x)[j];
+                a.slot[x0 + j] = (&slot.x)[j];
             }
         }
     }
@@ -212,46 +227,82 @@ template <> struct Vec16<__nv_bfloat16> {
     }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256) page_write_kernel(const PagePool p, const T* __restrict__ k, const T* __restrict__ v,
-                                                         long long k_stride, long long v_stride,
-                                                         const int* __restrict__ slot, int rows)
+constexpr int kWriteThreads = 256;
+
+// A CTA takes RPT * 256 / tx rows and tx 16-byte columns of them (all heads
+// side by side): thread = column and every (256 / tx)-th row, all its loads
+// before its stores.  Then, for each row among them that ends a page, the
+// threads of a column share the page's keys.
+template <typename T, int D, int RPT>
+__global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const PagePool p, const T* __restrict__ k, const T* __restrict__ v,
+                                                                   const long long k_stride, const long long v_stride,
+                                                                   const int* __restrict__ slot, const int rows, const int tx)
 {
-    constexpr int E = 16 / sizeof(T), VPR = D / E;        // elements of a vector, vectors of a row
-    const int sh = __ffs(p.ps) - 1;
+    constexpr int E = 16 / sizeof(T), VPR = D / E;        // elements of a vector, vectors of a row's head
+    __shared__ Vec16<T> part[2][kWriteThreads];
+    const int sh = __ffs(p.ps) - 1, ty = kWriteThreads / tx;
+    const int x = threadIdx.x & (tx - 1), y = threadIdx.x / tx, col = blockIdx.y * tx + x;
+    const bool in = col < p.heads * VPR;
+    const int h = col / VPR, e = (col & (VPR - 1)) * E;
     const long long slots = (long long)p.pages * p.ps;
-    const long long total = (long long)rows * p.heads * VPR;
+    const int r0 = blockIdx.x * RPT * ty;
     T* K = static_cast<T*>(p.K);
     T* V = static_cast<T*>(p.V);
-    for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < total; x += (long long)gridDim.x * blockDim.x) {
-        const int e = (int)(x % VPR) * E;
-        const long long rh = x / VPR;
-        const int h = (int)(rh % p.heads), r = (int)(rh / p.heads);
-        const int s = slot[r];
-        if (s < 0 || s >= slots) continue;
-        const int page = s >> sh, at = s & (p.ps - 1);
-        const size_t base = ((size_t)page * p.heads + h) * p.ps * D + e;
-        Vec16<T> kv, vv;
-        kv.load(k + r * k_stride + (size_t)h * D + e);
-        vv.load(v + r * v_stride + (size_t)h * D + e);
-        kv.store(K + base + (size_t)at * D);
-        vv.store(V + base + (size_t)at * D);
-        if (at == p.ps - 1) {
-            // how many rows before this one hold the slots before it
-            int run = 0;
-            while (run < at && r - run > 0 && slot[r - run - 1] == s - run - 1) ++run;
-            Vec16<T> lo = kv, hi = kv;
-            for (int o = 1; o <= at; ++o) {
+    auto place = [&](int s) {                             // of this column in slot s
+        return (((size_t)(s >> sh) * p.heads + h) * p.ps + (s & (p.ps - 1))) * D + e;
+    };
+    Vec16<T> kv[RPT], vv[RPT];
+    int s[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = r0 + y + i * ty;
+        s[i] = r < rows ? slot[r] : -1;
+        if (s[i] >= slots || !in) s[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+        if (s[i] >= 0) {
+            const int r = r0 + y + i * ty;
+            kv[i].load(k + r * k_stride + (size_t)col * E);
+            vv[i].load(v + r * v_stride + (size_t)col * E);
+        }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+        if (s[i] >= 0) {
+            kv[i].store(K + place(s[i]));
+            vv[i].store(V + place(s[i]));
+        }
+    for (int r = r0; r < min(rows, r0 + RPT * ty); ++r) {
+        const int end = slot[r];
+        if (end < 0 || end >= slots || (end & (p.ps - 1)) != p.ps - 1) continue;   // (the same for the whole CTA)
+        Vec16<T> lo, hi;
+        if (in) {
+            const size_t page = place(end) - (size_t)(p.ps - 1) * D;
+            lo.load(k + r * k_stride + (size_t)col * E);
+            hi = lo;
+#pragma unroll 8
+            for (int o = y; o < p.ps - 1; o += ty) {
+                // the key at offset o: a row of this call, or one of before
+                const int back = r - (p.ps - 1 - o);
                 Vec16<T> w;
-                if (o <= run) w.load(k + (r - o) * k_stride + (size_t)h * D + e);
-                else w.load(K + base + (size_t)(at - o) * D);
+                w.load(back >= 0 && slot[back] == end - (p.ps - 1 - o) ? k + back * k_stride + (size_t)col * E : K + page + (size_t)o * D);
                 lo.low(w);
                 hi.high(w);
             }
-            T* b = static_cast<T*>(p.bounds) + ((size_t)page * p.heads + h) * 2 * D + e;
+            part[0][threadIdx.x] = lo;
+            part[1][threadIdx.x] = hi;
+        }
+        __syncthreads();
+        if (in && y == 0) {
+            for (int j = 1; j < ty; ++j) {
+                lo.low(part[0][j * tx + x]);
+                hi.high(part[1][j * tx + x]);
+            }
+            T* b = static_cast<T*>(p.bounds) + ((size_t)(end >> sh) * p.heads + h) * 2 * D + e;
             lo.store(b);
             hi.store(b + D);
         }
+        __syncthreads();
     }
 }
 
@@ -261,7 +312,7 @@ cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t st)
 {
     const long long work = std::max<long long>(a.n, ((long long)a.cap + 3) / 4);
     const int threads = work <= 256 ? 256 : 1024;
-    const int grid = (int)std::min<long long>(152, std::max<long long>(1, (work + threads - 1) / threads));
+    const int grid = (int)std::min<long long>(2 * 152, std::max<long long>(1, (work + threads - 1) / threads));
     const size_t smem = 2 * sizeof(int) * ((size_t)a.n + 1);
     if (smem > 48 * 1024) {
         static SmemOnce once;
@@ -275,18 +326,27 @@ cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t st)
 cudaError_t launch_page_write(const PagePool& p, const void* k, const void* v, long long k_stride, long long v_stride,
                               const int* slot, int rows, cudaStream_t st)
 {
-    const int vpr = p.D * (p.dtype ? 2 : 4) / 16;
-    const long long total = (long long)rows * p.heads * vpr;
-    const unsigned grid = (unsigned)std::min<long long>((total + 255) / 256, 1 << 20);
-    auto go = [&](auto t, auto d) {
+    const int cols = p.heads * (p.D * (p.dtype ? 2 : 4) / 16);
+    int tx = 8;
+    while (tx < 64 && tx < cols) tx *= 2;
+    const int ty = kWriteThreads / tx;
+    // four rows a thread where that still makes two CTAs an SM
+    const long long tiles = (long long)((rows + 4 * ty - 1) / (4 * ty)) * ((cols + tx - 1) / tx);
+    auto go = [&](auto t, auto d, auto rpt) {
         using T = decltype(t);
-        page_write_kernel<T, decltype(d)::value><<<grid, 256, 0, st>>>(p, static_cast<const T*>(k), static_cast<const T*>(v),
-                                                                       k_stride, v_stride, slot, rows);
+        constexpr int R = decltype(rpt)::value;
+        const dim3 grid((unsigned)((rows + R * ty - 1) / (R * ty)), (unsigned)((cols + tx - 1) / tx));
+        page_write_kernel<T, decltype(d)::value, R><<<grid, kWriteThreads, 0, st>>>(p, static_cast<const T*>(k), static_cast<const T*>(v),
+                                                                                    k_stride, v_stride, slot, rows, tx);
+    };
+    auto by_rows = [&](auto t, auto d) {
+        if (tiles >= 2 * 152) go(t, d, std::integral_constant<int, 4>());
+        else go(t, d, std::integral_constant<int, 1>());
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;
-    if (p.dtype) p.D == 64 ? go(__nv_bfloat16(), D64()) : go(__nv_bfloat16(), D128());
-    else p.D == 64 ? go(float(), D64()) : go(float(), D128());
+    if (p.dtype) p.D == 64 ? by_rows(__nv_bfloat16(), D64()) : by_rows(__nv_bfloat16(), D128());
+    else p.D == 64 ? by_rows(float(), D64()) : by_rows(float(), D128());
     return cudaGetLastError();
 }
 

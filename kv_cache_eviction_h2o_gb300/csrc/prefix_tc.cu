@@ -505,13 +505,14 @@ cudaError_t go(const PagePool& p, const PageRows& r, const int* table, int prefi
 // more for its start, its query tiles and its sums.
 int prefix_tc_range(int rows, int heads, int G, int prefix_len)
 {
-    const long long units = ((long long)rows * G + 2 * kT - 1) / (2 * kT) * heads;
+    const int units = (int)(((long long)rows * G + 2 * kT - 1) / (2 * kT) * heads);
     const int tiles = (prefix_len + kT - 1) / kT;
+    const int most = std::min({tiles, kMaxPrefixSplits, 3 * kSMs / units + 1});   // (beyond three waves nothing is gained)
     int best = tiles;
     long long cost = -1;
-    for (int s = 1; s <= std::min(tiles, kMaxPrefixSplits); ++s) {
+    for (int s = 1; s <= most; ++s) {
         const int each = (tiles + s - 1) / s;
-        const long long ctas = units * ((tiles + each - 1) / each);
+        const long long ctas = (long long)units * ((tiles + each - 1) / each);
         const long long c = (ctas + kSMs - 1) / kSMs * (each + 2);
         if (cost < 0 || c < cost) { cost = c; best = each; }
     }
