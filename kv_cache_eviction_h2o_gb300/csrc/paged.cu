@@ -47,29 +47,46 @@ __device__ __forceinline__ int owner_of(const int* start, int n, int x)
     return lo;
 }
 
-__global__ void page_tables_kernel(const TablesArgs a)
+// x[i .. i + 3], zeros from n on
+__device__ __forceinline__ int4 four_of(const int* x, int i, int n)
 {
-    extern __shared__ int sm[];
+    if (i + 4 <= n && ((size_t)x & 15) == 0) return *reinterpret_cast<const int4*>(x + i);
+    return make_int4(i < n ? x[i] : 0, i + 1 < n ? x[i + 1] : 0, i + 2 < n ? x[i + 2] : 0, i + 3 < n ? x[i + 3] : 0);
+}
+
+// A thread takes four requests at a time (i a multiple of four).
+__global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a)
+{
+    extern __shared__ __align__(16) int sm[];
+    const int n4 = (a.n + 4) & ~3;     // room for n + 1, in fours
     int* start = sm;                   // [n + 1] first row of each request
-    int* first = sm + a.n + 1;         // [n + 1] first free-list entry of each
+    int* first = sm + n4;              // [n + 1] first free-list entry of each
+    int* before = sm + 2 * n4;         // [n]
     __shared__ TableSums warp_sum[32];
     __shared__ int warp_max[32], flags;
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    const int sh = __ffs(a.ps) - 1;
-    const int per = (a.n + nt - 1) / nt, i0 = min(a.n, tid * per), i1 = min(a.n, i0 + per);
+    const int sh = __ffs(a.ps) - 1, up = a.ps - 1;
+    const int per = ((a.n + nt - 1) / nt + 3) & ~3, i0 = min(a.n, tid * per), i1 = min(a.n, i0 + per);
     if (tid == 0) flags = 0;
     __syncthreads();
 
     TableSums mine{0, 0};
     int longest = 0, bad = 0;
-    for (int i = i0; i < i1; ++i) {
-        const long long b = a.before[i], t = a.fresh[i];
-        if (b < 0 || t < 0) { bad |= kTableCount; continue; }
-        const long long want = (b + t + a.ps - 1) >> sh;
-        if (want > a.width) bad |= kTableWidth;
-        mine.rows += t;
-        mine.pages += want - ((b + a.ps - 1) >> sh);
-        longest = max(longest, (int)min(b + t, (long long)INT_MAX));
+    int4 b4 = make_int4(0, 0, 0, 0), t4 = b4;              // (the last four, which with up to 4096 requests are all)
+    for (int i = i0; i < i1; i += 4) {
+        b4 = four_of(a.before, i, a.n);
+        t4 = four_of(a.fresh, i, a.n);
+        *reinterpret_cast<int4*>(before + i) = b4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const long long b = (&b4.x)[j], t = (&t4.x)[j];
+            if (b < 0 || t < 0) { bad |= kTableCount; continue; }
+            const long long want = (b + t + up) >> sh;
+            if (want > a.width) bad |= kTableWidth;
+            mine.rows += t;
+            mine.pages += want - ((b + up) >> sh);
+            longest = max(longest, (int)min(b + t, (long long)INT_MAX));
+        }
     }
     if (bad) atomicOr(&flags, bad);
     TableSums upto = mine;
@@ -96,19 +113,32 @@ __global__ void page_tables_kernel(const TablesArgs a)
     // all or nothing: with an error no request gets rows or pages
     long long r = upto.rows - mine.rows + (warp ? warp_sum[warp - 1].rows : 0);
     long long p = upto.pages - mine.pages + (warp ? warp_sum[warp - 1].pages : 0);
-    for (int i = i0; i < i1; ++i) {
-        const int b = a.before[i], t = err ? 0 : a.fresh[i];
-        start[i] = err ? 0 : (int)r;
-        first[i] = err ? 0 : (int)p;
-        if (!err) {
-            r += t;
-            p += ((b + t + a.ps - 1) >> sh) - ((b + a.ps - 1) >> sh);
+    for (int i = i0; i < i1; i += 4) {
+        if (per > 4) {
+            b4 = four_of(a.before, i, a.n);
+            t4 = four_of(a.fresh, i, a.n);
         }
-        if (blockIdx.x == 0) {
-            a.after[i] = b + t;
-            a.row_start[i] = start[i];
-        }
+        int4 s4 = make_int4(0, 0, 0, 0), f4 = s4;
+        if (!err)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int b = (&b4.x)[j], t = (&t4.x)[j];
+                (&s4.x)[j] = (int)r;
+                (&f4.x)[j] = (int)p;
+                r += t;
+                p += ((b + t + up) >> sh) - ((b + up) >> sh);
+            }
+        *reinterpret_cast<int4*>(start + i) = s4;
+        *reinterpret_cast<int4*>(first + i) = f4;
+        if (blockIdx.x == 0)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j < a.n) {
+                    a.after[i + j] = (&b4.x)[j] + (err ? 0 : (&t4.x)[j]);
+                    a.row_start[i + j] = (&s4.x)[j];
+                }
     }
+    __syncthreads();                                       // (before start[n] goes behind the last four)
     if (tid == 0) {
         start[a.n] = rows;
         first[a.n] = pages;
@@ -125,7 +155,7 @@ __global__ void page_tables_kernel(const TablesArgs a)
     const int g = blockIdx.x * nt + tid, stride = gridDim.x * nt;
     for (int x = g; x < pages; x += stride) {
         const int i = owner_of(first, a.n, x);
-        a.table[(size_t)i * a.width + ((a.before[i] + a.ps - 1) >> sh) + (x - first[i])] = a.free_pages[x];
+        a.table[(size_t)i * a.width + ((before[i] + up) >> sh) + (x - first[i])] = a.free_pages[x];
     }
     // four rows a thread, written as 16 bytes where the maps lie on them
     const bool wide = (((size_t)a.row_seq | (size_t)a.row_pos | (size_t)a.slot) & 15) == 0;
@@ -136,12 +166,12 @@ __global__ void page_tables_kernel(const TablesArgs a)
             int i = owner_of(start, a.n, x0);
             // the page of position `at` of request i; a table or free-list entry that is no page gives no slot
             auto slot_of = [&](int at) {
-                const int owned = (a.before[i] + a.ps - 1) >> sh, pg = at >> sh;
+                const int owned = (before[i] + up) >> sh, pg = at >> sh;
                 const int page = pg < owned ? a.table[(size_t)i * a.width + pg] : a.free_pages[first[i] + pg - owned];
-                return page >= 0 && page <= last ? (page << sh) + (at & (a.ps - 1)) : -1;
+                return page >= 0 && page <= last ? (page << sh) + (at & up) : -1;
             };
-            const int at = a.before[i] + (x0 - start[i]);
-            if (x0 + 4 <= start[i + 1] && (at & (a.ps - 1)) <= a.ps - 4) {
+            const int at = before[i] + (x0 - start[i]);
+            if (x0 + 4 <= start[i + 1] && (at & up) <= a.ps - 4) {
                 // all in one page of one request, as most are
                 const int s = slot_of(at);
                 seq = make_int4(i, i, i, i);
@@ -153,7 +183,7 @@ __global__ void page_tables_kernel(const TablesArgs a)
                     const int x = x0 + j;
                     if (x >= rows) break;
                     while (start[i + 1] <= x) ++i;
-                    const int y = a.before[i] + (x - start[i]);
+                    const int y = before[i] + (x - start[i]);
                     (&seq.x)[j] = i;
                     (&pos.x)[j] = y;
                     (&slot.x)[j] = slot_of(y);
@@ -312,8 +342,8 @@ cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t st)
 {
     const long long work = std::max<long long>(a.n, ((long long)a.cap + 3) / 4);
     const int threads = work <= 256 ? 256 : 1024;
-    const int grid = (int)std::min<long long>(2 * 152, std::max<long long>(1, (work + threads - 1) / threads));
-    const size_t smem = 2 * sizeof(int) * ((size_t)a.n + 1);
+    const int grid = (int)std::min<long long>(152, std::max<long long>(1, (work + threads - 1) / threads));
+    const size_t smem = 3 * sizeof(int) * (((size_t)a.n + 4) & ~(size_t)3);
     if (smem > 48 * 1024) {
         static SmemOnce once;
         const cudaError_t e = once.allow(page_tables_kernel);
