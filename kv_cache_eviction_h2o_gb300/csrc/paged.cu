@@ -130,20 +130,12 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a)
             }
         *reinterpret_cast<int4*>(start + i) = s4;
         *reinterpret_cast<int4*>(first + i) = f4;
-        if (blockIdx.x == 0)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (i + j < a.n) {
-                    a.after[i + j] = (&b4.x)[j] + (err ? 0 : (&t4.x)[j]);
-                    a.row_start[i + j] = (&s4.x)[j];
-                }
     }
     __syncthreads();                                       // (before start[n] goes behind the last four)
     if (tid == 0) {
         start[a.n] = rows;
         first[a.n] = pages;
         if (blockIdx.x == 0) {
-            a.row_start[a.n] = rows;
             a.status[0] = rows;
             a.status[1] = pages;
             a.status[2] = err ? 0 : warp_max[0];
@@ -153,7 +145,12 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a)
     __syncthreads();
 
     const int g = blockIdx.x * nt + tid, stride = gridDim.x * nt;
-    for (int x = g; x < pages; x += stride) {
+    for (int i = g; i <= a.n; i += stride) {
+        a.row_start[i] = start[i];
+        if (i < a.n) a.after[i] = before[i] + (start[i + 1] - start[i]);
+    }
+    // (from the other end: the first CTAs have the loop above and the longer share of the one below)
+    for (int x = stride - 1 - g; x < pages; x += stride) {
         const int i = owner_of(first, a.n, x);
         a.table[(size_t)i * a.width + ((before[i] + up) >> sh) + (x - first[i])] = a.free_pages[x];
     }
