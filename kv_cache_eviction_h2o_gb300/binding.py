@@ -397,7 +397,7 @@ def _wrong(x, what, dtype, shape, device):
         raise TypeError("%s must be of dtype %s (got %s)" % (what, dtype, x.dtype))
     if x.get_device() != device:
         raise ValueError("%s must be on %s (got %s)" % (what, "cuda:%d" % device if device >= 0 else "the CPU", x.device))
-    if x.shape != shape:
+    if x.shape != shape and not (len(shape) == 1 and x.numel() == shape[0]):
         raise ValueError("%s must have shape %s (got %s)" % (what, list(shape), list(x.shape)))
     raise ValueError("%s must be contiguous" % what)
 
@@ -410,6 +410,16 @@ def _tensor(x, what, dtype, shape, device):
     except AttributeError:
         pass
     _wrong(x, what, dtype, shape, device)
+
+
+def _array(x, what, dtype, n, device):
+    """The pointer of a contiguous tensor of n elements of `dtype` on device `device`."""
+    try:
+        if x.dtype is dtype and x.numel() == n and x.get_device() == device and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _wrong(x, what, dtype, (n,), device)
 
 
 def _head_rows(x, what, dtype, shape, device):
@@ -434,6 +444,12 @@ def _dim(x, what, rank):
     if len(shape) != rank:
         raise ValueError("%s must have %d dimensions (got %s)" % (what, rank, list(shape)))
     return shape
+
+
+def _count(x, what):
+    if not hasattr(x, "data_ptr"):
+        raise TypeError("%s must be a tensor" % what)
+    return x.numel()
 
 
 def _on_current(x, current):
@@ -467,16 +483,15 @@ def h2o_page_tables(len_before, n_new, free_pages, page_size, table, len_after, 
     [requests][width], row_start [requests + 1], row_seq, row_pos, slot
     [rows_cap], status [4]."""
     i32, _, _, current = _torch_types()
-    per, free, cap = _dim(len_before, "len_before", 1), _dim(free_pages, "free_pages", 1), _dim(slot, "slot", 1)
-    n, wide = per[0], _dim(table, "table", 2)
-    dev = _on_current(len_before, current)
+    n, width = _dim(table, "table", 2)
+    dev = _on_current(table, current)
+    free, cap = _count(free_pages, "free_pages"), _count(slot, "slot")
     rc = lib().h2o_page_tables(
-        _tensor(len_before, "len_before", i32, per, dev), _tensor(n_new, "n_new", i32, per, dev), n,
-        _tensor(free_pages, "free_pages", i32, free, dev), free[0], page_size,
-        _tensor(table, "table", i32, (n, wide[1]), dev), wide[1], _tensor(len_after, "len_after", i32, per, dev),
-        _tensor(row_start, "row_start", i32, (n + 1,), dev), _tensor(row_seq, "row_seq", i32, cap, dev),
-        _tensor(row_pos, "row_pos", i32, cap, dev), _tensor(slot, "slot", i32, cap, dev), cap[0],
-        _tensor(status, "status", i32, (4,), dev), _stream(stream))
+        _array(len_before, "len_before", i32, n, dev), _array(n_new, "n_new", i32, n, dev), n,
+        _array(free_pages, "free_pages", i32, free, dev), free, page_size, _array(table, "table", i32, n * width, dev), width,
+        _array(len_after, "len_after", i32, n, dev), _array(row_start, "row_start", i32, n + 1, dev),
+        _array(row_seq, "row_seq", i32, cap, dev), _array(row_pos, "row_pos", i32, cap, dev), _array(slot, "slot", i32, cap, dev),
+        cap, _array(status, "status", i32, 4, dev), _stream(stream))
     if rc:
         _check(rc)
 
@@ -484,10 +499,11 @@ def h2o_page_tables(len_before, n_new, free_pages, page_size, table, len_after, 
 def h2o_page_write(k, v, slot, K, V, bounds, stream=None):
     """Key and value rows [rows][kv_heads][head_dim] into their slots; see include/h2o.h."""
     dev, dt, code, Kp, Vp, (pages, heads, ps, d) = _pool(K, V)
-    rows = _dim(slot, "slot", 1)
-    kp, ks = _head_rows(k, "k", dt, (rows[0], heads, d), dev)
-    vp, vs = _head_rows(v, "v", dt, (rows[0], heads, d), dev)
-    rc = lib().h2o_page_write(kp, vp, ks, vs, _tensor(slot, "slot", _types[0], rows, dev), rows[0], Kp, Vp,
+    rows = _count(slot, "slot")
+    shape = (rows, heads, d)
+    kp, ks = _head_rows(k, "k", dt, shape, dev)
+    vp, vs = _head_rows(v, "v", dt, shape, dev)
+    rc = lib().h2o_page_write(kp, vp, ks, vs, _array(slot, "slot", _types[0], rows, dev), rows, Kp, Vp,
                               _tensor(bounds, "bounds", dt, (pages, heads, 2, d), dev), pages, heads, ps, d, code,
                               _stream(stream))
     if rc:
@@ -496,15 +512,15 @@ def h2o_page_write(k, v, slot, K, V, bounds, stream=None):
 
 def _query_rows(q, row_seq, row_pos, table, out, dev, dt, heads, d):
     i32 = _types[0]
-    rows, wide = _dim(row_seq, "row_seq", 1), _dim(table, "table", 2)
-    hq = _dim(q, "q", 3)[1]
+    n, width = _dim(table, "table", 2)
+    rows, hq, _ = _dim(q, "q", 3)
     if hq < 1 or hq % heads:
         raise ValueError("q must be [rows][kv_heads * groups][head_dim] (got %s for %d cache heads)" % (list(q.shape), heads))
-    shape = (rows[0], hq, d)
+    shape = (rows, hq, d)
     qp, qs = _head_rows(q, "q", dt, shape, dev)
     op, os_ = _head_rows(out, "out", dt, shape, dev)
-    return (qp, qs, _tensor(row_seq, "row_seq", i32, rows, dev), _tensor(row_pos, "row_pos", i32, rows, dev), rows[0],
-            hq // heads, _tensor(table, "table", i32, wide, dev), wide[0], wide[1], op, os_)
+    return (qp, qs, _array(row_seq, "row_seq", i32, rows, dev), _array(row_pos, "row_pos", i32, rows, dev), rows,
+            hq // heads, _array(table, "table", i32, n * width, dev), n, width, op, os_)
 
 
 def h2o_page_attend(q, row_seq, row_pos, K, V, bounds, table, budget, recent, scale, out, picked=None, stream=None):
@@ -534,12 +550,12 @@ def h2o_prefix_attend(q, row_seq, row_pos, K, V, prefix_table, prefix_len, table
     qp, qs, sp, pp, rows, groups, tp, n, width, op, os_ = _query_rows(q, row_seq, row_pos, table, out, dev, dt, heads, d)
     xp = None
     if prefix_table is not None:
-        listed = _dim(prefix_table, "prefix_table", 1)
-        xp = _tensor(prefix_table, "prefix_table", _types[0], listed, dev)
-        if listed[0] * ps < prefix_len:
-            raise ValueError("prefix_table lists %d pages of %d tokens, prefix_len is %d" % (listed[0], ps, prefix_len))
-    size = _dim(work, "work", 1)
+        listed = _count(prefix_table, "prefix_table")
+        xp = _array(prefix_table, "prefix_table", _types[0], listed, dev)
+        if listed * ps < prefix_len:
+            raise ValueError("prefix_table lists %d pages of %d tokens, prefix_len is %d" % (listed, ps, prefix_len))
+    size = _count(work, "work")
     rc = lib().h2o_prefix_attend(qp, qs, sp, pp, rows, Kp, Vp, pages, heads, groups, ps, d, code, xp, prefix_len, tp, n,
-                                 width, scale, op, os_, _tensor(work, "work", _types[1], size, dev), size[0], _stream(stream))
+                                 width, scale, op, os_, _array(work, "work", _types[1], size, dev), size, _stream(stream))
     if rc:
         _check(rc)

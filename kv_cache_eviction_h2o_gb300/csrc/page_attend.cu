@@ -170,7 +170,10 @@ struct Held {
     template <class F> __device__ __forceinline__ void each(F f) const
     {
 #pragma unroll
-        for (int i = 0; i < kHold; ++i) f(k[i]);
+        for (int i = 0; i < kHold; ++i) {
+            if (i * NT >= n) break;
+            f(k[i]);
+        }
         for (int j = threadIdx.x + kHold * NT; j < n; j += NT) f(ord_key(s[j]));
     }
 };

@@ -26,26 +26,37 @@ struct SimtSmem {
     float p[kRows][kCols + 4];
 };
 
-// prefix positions [j0, j1) of one cache head into S.kv, zeros past j1
+// prefix positions [j0, j0 + 64) of one cache head, zeros from j1 on: asked for
+// into registers, and put into S.kv when that is free
 template <int D>
-__device__ __forceinline__ void load_rows(float (*dst)[D + 4], const float* src, const PagePool& pool, const int* table, int h,
-                                          int j0, int j1, bool& bad)
-{
-    constexpr int N = 4, VPR = D / N;
-    const int sh = __ffs(pool.ps) - 1;
-    for (int i = threadIdx.x; i < kCols * VPR; i += 256) {
-        const int r = i / VPR, e = (i % VPR) * N, j = j0 + r;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < j1) {
-            const int pg = table[j >> sh];
-            if ((unsigned)pg < (unsigned)pool.pages)
-                x = *reinterpret_cast<const float4*>(src + (((size_t)pg * pool.heads + h) * pool.ps + (j & (pool.ps - 1))) * D + e);
-            else
-                bad = true;
+struct Rows64 {
+    static constexpr int VPR = D / 4, N = kCols * VPR / 256;
+    float4 v[N];
+    __device__ __forceinline__ void ask(const float* src, const PagePool& pool, const int* table, int h, int j0, int j1, bool& bad)
+    {
+        const int sh = __ffs(pool.ps) - 1;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = threadIdx.x + i * 256, j = j0 + k / VPR, e = (k % VPR) * 4;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < j1) {
+                const int pg = table[j >> sh];
+                if ((unsigned)pg < (unsigned)pool.pages)
+                    v[i] = *reinterpret_cast<const float4*>(src + (((size_t)pg * pool.heads + h) * pool.ps + (j & (pool.ps - 1))) * D + e);
+                else
+                    bad = true;
+            }
         }
-        *reinterpret_cast<float4*>(&dst[r][e]) = x;
     }
-}
+    __device__ __forceinline__ void put(float (*dst)[D + 4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = threadIdx.x + i * 256;
+            *reinterpret_cast<float4*>(&dst[k / VPR][(k % VPR) * 4]) = v[i];
+        }
+    }
+};
 
 // grid: (query tile, split, cache head)
 template <int D>
@@ -59,9 +70,15 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, c
     const int j0 = blockIdx.y * per, j1 = min(prefix_len, j0 + per);
     grid_launch_dependents();          // the rows' own pass may start on what SMs are left; it waits before it reads sums
     bool bad = false;
-    for (int i = tid; i < kRows * D; i += 256) {
-        const int r = i / D, e = i % D, x = x0 + r;
-        S.q[r][e] = x < nx ? static_cast<const float*>(R.q)[(size_t)(x / G) * R.q_stride + (size_t)(h * G + x % G) * D + e] : 0.f;
+    const float* K = static_cast<const float*>(pool.K);
+    const float* V = static_cast<const float*>(pool.V);
+    Rows64<D> next;                    // keys while values are in use, and the other way round
+    next.ask(K, pool, table, h, j0, j1, bad);
+    for (int i = tid; i < kRows * D / 4; i += 256) {
+        const int r = i / (D / 4), e = i % (D / 4) * 4, x = x0 + r;
+        *reinterpret_cast<float4*>(&S.q[r][e]) =
+            x < nx ? *reinterpret_cast<const float4*>(static_cast<const float*>(R.q) + (size_t)(x / G) * R.q_stride + (size_t)(h * G + x % G) * D + e)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     constexpr int NJ = D / 64;
     float m[4], l[4], o[4][NJ][4];
@@ -76,7 +93,8 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, c
     }
     for (int j = j0; j < j1; j += kCols) {
         __syncthreads();
-        load_rows<D>(S.kv, static_cast<const float*>(pool.K), pool, table, h, j, j1, bad);
+        next.put(S.kv);
+        next.ask(V, pool, table, h, j, j1, bad);
         __syncthreads();
         float z[4][4] = {};
 #pragma unroll 4
@@ -122,7 +140,8 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, c
                 for (int k = 0; k < 4; ++k) o[i][n][k] *= a;
         }
         __syncthreads();
-        load_rows<D>(S.kv, static_cast<const float*>(pool.V), pool, table, h, j, j1, bad);
+        next.put(S.kv);
+        if (j + kCols < j1) next.ask(K, pool, table, h, j + kCols, j1, bad);
         __syncthreads();
 #pragma unroll 2
         for (int c = 0; c < kCols; c += 4) {
