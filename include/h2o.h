@@ -462,12 +462,11 @@ int h2o_selftest_wait_timeout(h2o_handle h);
  *             (slot is also -1 where a table or free-list entry is no page
  *             number);
  *   status    [4]: {rows, pages taken, longest len_after, error bits}.
- * All arrays are device int32; none of the outputs overlaps an input.
- * free_pages is only read: the caller drops
- * the first status[1] of it.  All or nothing: with an error bit (1: a
- * negative count, 2: more than rows_cap rows, 4: more than n_free pages,
- * 8: a request longer than table_width pages) no page is taken, len_after is
- * len_before and there are no rows.  1 <= requests <= 16384.
+ * All arrays are device int32; no output overlaps an input.  free_pages is
+ * only read: the caller drops the first status[1] of it.  All or nothing: with
+ * an error bit (1: a negative count, 2: more than rows_cap rows, 4: more than
+ * n_free pages, 8: a request longer than table_width pages) no page is taken,
+ * len_after is len_before and there are no rows.  1 <= requests <= 16384, rows_cap <= 2^30.
  */
 int h2o_page_tables(const int* len_before, const int* n_new, int requests, const int* free_pages, int n_free,
                     int page_size, int* table, int table_width, int* len_after, int* row_start, int* row_seq,

@@ -89,7 +89,8 @@ int h2o_page_tables(const int* len_before, const int* n_new, int requests, const
 {
     if (requests < 1 || requests > kMaxPageRequests)
         return set_last_error(H2O_ERR_ARG, "requests must be in [1, %d] (got %d)", kMaxPageRequests, requests);
-    if (n_free < 0 || rows_cap < 0) return set_last_error(H2O_ERR_ARG, "n_free and rows_cap must be >= 0");
+    if (n_free < 0 || rows_cap < 0 || rows_cap > 1 << 30)
+        return set_last_error(H2O_ERR_ARG, "n_free must be >= 0 and rows_cap in [0, 2^30]");
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
         return set_last_error(H2O_ERR_ARG, "page_size must be 16, 32, 64 or 128 (got %d)", page_size);
     if (table_width < 1 || table_width > kMaxTableWidth)

@@ -365,11 +365,11 @@ cudaError_t launch_page_write(const PagePool& p, const void* k, const void* v, l
     while (tx < 64 && tx < cols) tx *= 2;
     const int ty = kWriteThreads / tx;
     // four rows a thread where that still makes two CTAs an SM
-    const long long tiles = (long long)((rows + 4 * ty - 1) / (4 * ty)) * ((cols + tx - 1) / tx);
+    const long long tiles = ((rows + 4LL * ty - 1) / (4 * ty)) * ((cols + tx - 1) / tx);
     auto go = [&](auto t, auto d, auto rpt) {
         using T = decltype(t);
         constexpr int R = decltype(rpt)::value;
-        const dim3 grid((unsigned)((rows + R * ty - 1) / (R * ty)), (unsigned)((cols + tx - 1) / tx));
+        const dim3 grid((unsigned)((rows + (long long)R * ty - 1) / (R * ty)), (unsigned)((cols + tx - 1) / tx));
         page_write_kernel<T, decltype(d)::value, R><<<grid, kWriteThreads, 0, st>>>(p, static_cast<const T*>(k), static_cast<const T*>(v),
                                                                                     k_stride, v_stride, slot, rows, tx);
     };

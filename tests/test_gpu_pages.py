@@ -166,6 +166,21 @@ def test_sparse_long_request_picks_exactly():
     _check(out, want, "long")
 
 
+@pytest.mark.parametrize("dtype,d,groups,pages", [(BF16, 64, 2, 16384), (F32, 128, 16, 16384), (BF16, 128, 16, 9000), (F32, 64, 1, 4097)])
+def test_sparse_at_the_widest_table(dtype, d, groups, pages):
+    # a table may list a page more than once: scores tie over and over, and the lowest entries win
+    c = Cache([40 * 16], 1, d, 16, dtype, seed=d)
+    table = np.tile(c.table, (1, -(-pages // 40)))[:, :pages]
+    c.table = np.concatenate([table, np.full((1, 16384 - pages), -1, np.int32)], 1)
+    q = _queries(2, groups, d, dtype, 4)
+    for budget, recent in ((4096, 7), (100, 1)):
+        seq, pos = [0, 0], [16 * pages - 1, 16 * (pages // 2) + 3]
+        want, picked = _sparse_ref(c, q, seq, pos, budget, recent, d ** -0.5)
+        out, got = _sparse(c, q.cuda(), seq, pos, budget, recent, d ** -0.5)
+        np.testing.assert_array_equal(got.cpu().numpy(), picked, err_msg="budget %d" % budget)
+        _check(out, want, "budget %d" % budget)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("kind", ["same", "pairs", "zero", "last bit"])
 def test_sparse_ties_go_to_the_lowest_page(dtype, kind):

@@ -33,7 +33,7 @@ PREFIX = dict(q=FAKE, qs=1024, seq=FAKE, pos=FAKE, rows=3, K=FAKE, V=FAKE, pages
 
 
 @pytest.mark.parametrize("change,frag", [
-    (dict(n=0), "requests"), (dict(n=16385), "requests"), (dict(n_free=-1), "n_free"), (dict(cap=-1), "rows_cap"),
+    (dict(n=0), "requests"), (dict(n=16385), "requests"), (dict(n_free=-1), "n_free"), (dict(cap=-1), "rows_cap"), (dict(cap=(1 << 30) + 1), "rows_cap"),
     (dict(ps=48), "page_size"), (dict(width=0), "table_width"), (dict(width=16385), "table_width"), (dict(before=None), "non-NULL"),
     (dict(free=None), "non-NULL"), (dict(slot=None), "non-NULL"), (dict(status=None), "non-NULL"), (dict(seq=FAKE + 2), "aligned"),
 ])
