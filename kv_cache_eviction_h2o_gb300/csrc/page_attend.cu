@@ -532,13 +532,30 @@ struct CoreMma {
     }
 };
 
-__device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) { *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w); }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float z, float w)
+// two or four floats
+template <int N> __device__ __forceinline__ void load_f(const float* p, float* x)
 {
-    uint32_t lo, hi;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(y), "f"(x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(w), "f"(z));
-    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+    if constexpr (N == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(p);
+        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+    } else {
+        const float2 w = *reinterpret_cast<const float2*>(p);
+        x[0] = w.x; x[1] = w.y;
+    }
+}
+template <int N> __device__ __forceinline__ void store_f(float* p, const float* x)
+{
+    if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+}
+template <int N> __device__ __forceinline__ void store_out(float* p, const float* x) { store_f<N>(p, x); }
+template <int N> __device__ __forceinline__ void store_out(__nv_bfloat16* p, const float* x)
+{
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr)
 {
@@ -546,12 +563,15 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr)
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void add4(float4& o, float a, float4 x)
+template <int N> __device__ __forceinline__ void ld_cluster_f(uint32_t addr, float* x)
 {
-    o.x = fmaf(a, x.x, o.x);
-    o.y = fmaf(a, x.y, o.y);
-    o.z = fmaf(a, x.z, o.z);
-    o.w = fmaf(a, x.w, o.w);
+    if constexpr (N == 4) {
+        const float4 w = ld_cluster_f4(addr);
+        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+    } else {
+        const float2 w = ld_cluster_f2(addr);
+        x[0] = w.x; x[1] = w.y;
+    }
 }
 
 template <int D, class Core>
@@ -569,9 +589,6 @@ template <typename T, int D> constexpr int kTileBytes = kKeys * D * (int)sizeof(
 template <typename T, int D> constexpr int kRingBytes = kStages<T> * 2 * kTileBytes<T, D>;   // a warp's
 
 constexpr int kMaxSources = 8 + kMaxPrefixSplits;   // CTAs of a cluster and ranges of a prefix
-// bytes of the rings, which also hold the sums and weights at the end
-template <typename T, int D, int NW>
-constexpr int kFront = std::max(NW * kRingBytes<T, D>, 4 * kMaxPageGroups * (2 * D + kMaxSources + 1));
 
 // Several CTAs an SM (bf16): while one ranks its pages, or waits for its
 // first keys, the others read.
@@ -826,93 +843,81 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
     core.finish(reinterpret_cast<float*>(ring), S.wml[warp], lane, G, bad);
     __syncthreads();
     float* sums = reinterpret_cast<float*>(raw + kSums);
-    for (int i = tid; i < G * D; i += kNT) {
-        const int g = i / D;
-        float m = -INFINITY, l = 0.f, o = 0.f;
+    constexpr int V4 = D / 32;                             // a lane's channels of a head
+    for (int g = warp; g < G; g += kWarps) {
+        float m = -INFINITY, l = 0.f, o[V4] = {};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) m = fmaxf(m, S.wml[w][g].x);
         const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float a = ex2_approx(S.wml[w][g].x - base);
-            l += a * S.wml[w][g].y;
-            o = fmaf(a, reinterpret_cast<const float*>(raw + w * kRingBytes<T, D>)[i], o);
+            l = fmaf(a, S.wml[w][g].y, l);
+            float x[V4];
+            load_f<V4>(reinterpret_cast<const float*>(raw + w * kRingBytes<T, D>) + g * D + lane * V4, x);
+#pragma unroll
+            for (int e = 0; e < V4; ++e) o[e] = fmaf(a, x[e], o[e]);
         }
-        sums[i] = o;
-        if (i % D == 0) S.ml[g] = make_float2(m, l);
+        store_f<V4>(sums + g * D + lane * V4, o);
+        if (lane == 0) S.ml[g] = make_float2(m, l);
     }
     if (part.splits) grid_dependency_wait();               // the prefix pass is through
     cluster_arrive();
     cluster_wait();
+    // A warp joins a head's sums of all sources, the cluster's CTAs and the prefix's ranges: eight sources' values are
+    // asked for at a time, the first beside the sources' maxima.
     T* orow = static_cast<T*>(R.out) + (size_t)row * R.out_stride + (size_t)h * G * D;
-    if (part.splits == 0) {
-        // four channels a thread: all that is to be joined is asked for at once
-        for (int i = (rank * kNT + tid) * 4; i < G * D; i += C * kNT * 4) {
-            float2 x[8];
-            float4 v[8];
+    const int ns = C + part.splits;
+    const size_t qrows = (size_t)R.rows * pool.heads * G, qr = (size_t)u * G;
+#pragma unroll 1
+    for (int g = rank * kWarps + warp; g < G; g += C * kWarps) {
+        constexpr int NX = (kMaxSources + 31) / 32, kAtOnce = 8;
+        float v[kAtOnce][V4];
+        auto ask = [&](int s0) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < C) {
-                    x[c] = ld_cluster_f2(map_to_rank(&S.ml[i / D], c));
-                    v[c] = ld_cluster_f4(map_to_rank(&sums[i], c));
-                }
-            float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < C) m = fmaxf(m, x[c].x);
-            const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < C) {
-                    const float a = ex2_approx(x[c].x - base);
-                    l = fmaf(a, x[c].y, l);
-                    add4(o, a, v[c]);
-                }
-            // no key at all: zero; a bad table entry has made l NaN
-            const float f = l == 0.f ? 0.f : 1.f / l;
-            store4(orow + i, o.x * f, o.y * f, o.z * f, o.w * f);
-        }
-    } else {
-        const size_t qrows = (size_t)R.rows * pool.heads * G, qr = (size_t)u * G;
-        // weights of the sources: the cluster's CTAs, then the prefix's ranges
-        float* wt = reinterpret_cast<float*>(raw + 2 * kSums); // [G][sources]
-        float* scale = wt + kMaxPageGroups * kMaxSources;      // [G]
-        static_assert(kFront<T, D, kWarps> >= 2 * kSums + 4 * kMaxPageGroups * (kMaxSources + 1), "and so do the weights");
-        const int ns = C + part.splits;
-        for (int g = warp; g < G; g += kWarps) {
-            float2 x[(kMaxSources + 31) / 32];
-            float m = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int i = 0; i < (kMaxSources + 31) / 32; ++i) {
-                const int k = lane + 32 * i;
-                x[i] = make_float2(-INFINITY, 0.f);
-                if (k < C) x[i] = ld_cluster_f2(map_to_rank(&S.ml[g], k));
-                else if (k < ns) x[i] = part.ml[(k - C) * qrows + qr + g];
-                m = fmaxf(m, x[i].x);
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int s = s0 + k;
+                if (s < C) ld_cluster_f<V4>(map_to_rank(sums + g * D + lane * V4, s), v[k]);
+                else if (s < ns) load_f<V4>(part.o + ((s - C) * qrows + qr + g) * D + lane * V4, v[k]);
             }
-            m = warp_max(m);
-            const float base = m == -INFINITY ? 0.f : m;
+        };
+        ask(0);
+        float2 x[NX];
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int i = 0; i < (kMaxSources + 31) / 32; ++i) {
-                const float a = ex2_approx(x[i].x - base);
-                l += a * x[i].y;
-                if (lane + 32 * i < ns) wt[g * kMaxSources + lane + 32 * i] = a;
+        for (int i = 0; i < NX; ++i) {
+            const int k = lane + 32 * i;
+            x[i] = make_float2(-INFINITY, 0.f);
+            if (k < C) x[i] = ld_cluster_f2(map_to_rank(&S.ml[g], k));
+            else if (k < ns) x[i] = part.ml[(k - C) * qrows + qr + g];
+            m = fmaxf(m, x[i].x);
+        }
+        m = warp_max(m);
+        const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            x[i].x = ex2_approx(x[i].x - base);            // the source's weight
+            l = fmaf(x[i].x, x[i].y, l);
+        }
+        l = warp_sum(l);
+        float o[V4] = {};
+#pragma unroll 1
+        for (int s0 = 0; s0 < ns; s0 += kAtOnce) {
+            const float mine = s0 < 32 ? x[0].x : s0 < 64 ? x[1].x : x[NX - 1].x;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const float a = __shfl_sync(0xffffffffu, mine, (s0 + k) & 31);
+                if (s0 + k < ns)
+#pragma unroll
+                    for (int e = 0; e < V4; ++e) o[e] = fmaf(a, v[k][e], o[e]);
             }
-            l = warp_sum(l);
-            if (lane == 0) scale[g] = l == 0.f ? 0.f : 1.f / l;
+            if (s0 + kAtOnce < ns) ask(s0 + kAtOnce);
         }
-        __syncthreads();
-        for (int i = (rank * kNT + tid) * 4; i < G * D; i += C * kNT * 4) {
-            const int g = i / D;
-            const float* w = wt + g * kMaxSources;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < C; ++c) add4(o, w[c], ld_cluster_f4(map_to_rank(&sums[i], c)));
-#pragma unroll 8
-            for (int s = 0; s < part.splits; ++s) add4(o, w[C + s], *reinterpret_cast<const float4*>(part.o + (s * qrows + qr) * D + i));
-            const float f = scale[g];
-            store4(orow + i, o.x * f, o.y * f, o.z * f, o.w * f);
-        }
+        // no key at all: zero; a bad table entry has made l NaN
+        const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < V4; ++e) o[e] *= f;
+        store_out<V4>(orow + g * D + lane * V4, o);
     }
     cluster_arrive();
     cluster_wait();                                        // no CTA leaves while another reads its sums
@@ -939,7 +944,7 @@ cudaError_t go(const PagePool& p, const PageRows& r, int budget, int recent, int
     constexpr int NW = Core::kWarps;
     const bool picks = budget > 0 && budget < r.width;
     const int wpad = picks ? (r.width + 3) & ~3 : 0;
-    const int front = std::max(kFront<T, D, NW>, 8 * wpad);
+    const int front = std::max(NW * kRingBytes<T, D>, 8 * wpad);
     const size_t smem = front + sizeof(AttendSmem<D, Core>) + 4 * ((size_t)wpad + (picks ? budget : 0));
     const auto kernel = page_attend_kernel<T, D, Core>;
     static SmemOnce once;

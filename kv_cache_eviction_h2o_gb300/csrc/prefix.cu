@@ -60,7 +60,7 @@ struct Rows64 {
 
 // grid: (query tile, split, cache head)
 template <int D>
-__global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, const PageRows R, const int* __restrict__ table,
+__global__ void __launch_bounds__(256, 2) prefix_simt_kernel(const PagePool pool, const PageRows R, const int* __restrict__ table,
                                                           const int prefix_len, const int per, const PrefixPart part)
 {
     extern __shared__ __align__(16) unsigned char raw[];
@@ -180,13 +180,22 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const PagePool pool, c
     }
 }
 
-// keys of each range: a multiple of 64
+// Keys of each range, a multiple of 64: the number of ranges that makes the
+// shortest sequence of waves (two CTAs an SM), a CTA costing its steps and
+// about one more for its start and its sums.
 int range_keys(int rows, int heads, int G, int prefix_len)
 {
-    const long long tiles = (long long)((rows * (long long)G + kRows - 1) / kRows) * heads;
-    const int steps = (prefix_len + kCols - 1) / kCols;
-    const int want = (int)std::max<long long>(1, std::min<long long>(2 * kSMs / tiles, kMaxPrefixSplits));
-    return (steps + std::min(want, steps) - 1) / std::min(want, steps) * kCols;
+    const long long tiles = ((long long)rows * G + kRows - 1) / kRows * heads;
+    const int steps = (prefix_len + kCols - 1) / kCols, resident = 2 * kSMs;
+    const int most = (int)std::min<long long>(std::min(steps, kMaxPrefixSplits), 3 * resident / tiles + 1);
+    int best = steps;
+    long long cost = -1;
+    for (int s = 1; s <= most; ++s) {
+        const int each = (steps + s - 1) / s;
+        const long long ctas = tiles * ((steps + each - 1) / each), c = (ctas + resident - 1) / resident * (each + 1);
+        if (cost < 0 || c < cost) { cost = c; best = each; }
+    }
+    return best * kCols;
 }
 
 }  // namespace

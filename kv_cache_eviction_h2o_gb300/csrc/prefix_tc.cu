@@ -500,20 +500,24 @@ cudaError_t go(const PagePool& p, const PageRows& r, const int* table, int prefi
 
 }  // namespace
 
-// Keys of each CTA's range, a multiple of 128: the number of ranges that makes
-// the shortest sequence of waves, a CTA costing its key tiles and about two
-// more for its start, its query tiles and its sums.
+// Keys of each CTA's range, a multiple of 128: the number of ranges for the
+// shortest time.  In key tiles (1.6 us), a CTA costs those of its range and
+// about two for its start, its query tiles and its sums; the rows' own pass
+// about three when it finds no SMs left beside this one (8 requests of 8 heads
+// behind 2048 tokens: 16.0 us with 16 ranges, 13.2 with 8); and joining the
+// ranges 0.4 for every eight of them and four heads.
 int prefix_tc_range(int rows, int heads, int G, int prefix_len)
 {
     const int units = (int)(((long long)rows * G + 2 * kT - 1) / (2 * kT) * heads);
     const int tiles = (prefix_len + kT - 1) / kT;
     const int most = std::min({tiles, kMaxPrefixSplits, 3 * kSMs / units + 1});   // (beyond three waves nothing is gained)
+    const int own = (int)std::min<long long>((long long)rows * heads, kSMs);   // (two CTAs an SM, two a unit where there are few)
     int best = tiles;
     long long cost = -1;
     for (int s = 1; s <= most; ++s) {
-        const int each = (tiles + s - 1) / s;
-        const long long ctas = (long long)units * ((tiles + each - 1) / each);
-        const long long c = (ctas + kSMs - 1) / kSMs * (each + 2);
+        const int each = (tiles + s - 1) / s, n = (tiles + each - 1) / each;
+        const long long ctas = (long long)units * n;
+        const long long c = 10 * ((ctas + kSMs - 1) / kSMs * (each + 2) + (ctas + own > kSMs ? 3 : 0)) + 4 * ((n + 7) / 8) * ((G + 3) / 4);
         if (cost < 0 || c < cost) { cost = c; best = each; }
     }
     return best * kT;
