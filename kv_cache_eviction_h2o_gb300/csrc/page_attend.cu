@@ -588,7 +588,8 @@ struct alignas(16) AttendSmem {
 template <typename T, int D> constexpr int kTileBytes = kKeys * D * (int)sizeof(T);
 template <typename T, int D> constexpr int kRingBytes = kStages<T> * 2 * kTileBytes<T, D>;   // a warp's
 
-constexpr int kMaxSources = 8 + kMaxPrefixSplits;   // CTAs of a cluster and ranges of a prefix
+constexpr int kMaxCluster = 16;
+constexpr int kMaxSources = kMaxCluster + kMaxPrefixSplits;   // CTAs of a cluster and ranges of a prefix
 
 // Several CTAs an SM (bf16): while one ranks its pages, or waits for its
 // first keys, the others read.
@@ -925,16 +926,31 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
 
 // Warps of a CTA: two where there are more units than CTAs fit and each has
 // few tiles, so that more units are under way (6400 units of 12 tiles: 201 us
-// with four, 153 with two; 512 of 24: 81, 80; 512 of 96: 83, 89).
-int attend_warps(long long units, int tiles) { return units > 4 * kSMs && tiles <= 32 ? 2 : 4; }
+// with four, 153 with two; 512 of 24: 81, 80; 512 of 96: 83, 89), and in fp32,
+// whose ring of four leaves an SM one CTA (832 units of 3 tiles and a prefix:
+// 40 us, 23 with two), unless the units are few.
+int attend_warps(long long units, int tiles, int dtype)
+{
+    if (dtype) return units > 4 * kSMs && tiles <= 32 ? 2 : 4;
+    return units > kSMs / 8 ? 2 : 4;
+}
 
-// CTAs of a unit: up to 8 while all clusters fit the SMs at once and every
-// warp has three tiles (16 units of 96 tiles: 23 us with one, 12 with four;
-// 70 of 68: 18, 15 with four, 18 with eight).
-int cluster_of(long long units, int tiles, int resident, int warps)
+// Clusters of c CTAs that the GPU holds at once, about: what is left over of
+// each group of SMs makes larger ones fit worse (at two CTAs an SM 152, 74, 36
+// and 14 of 2, 4, 8 and 16; at one 76, 36, 15 and 7).
+int clusters_that_fit(int c, int per_sm)
+{
+    return c == 1 ? 152 * per_sm : c == 2 ? 76 * per_sm : c == 4 ? 36 * per_sm : c == 8 ? (per_sm == 1 ? 15 : 17 * per_sm) : 7 * per_sm;
+}
+
+// CTAs of a unit: as many, up to 16, as leave all clusters at once on the GPU
+// and every warp three tiles (16 units of 96 tiles: 23 us with one, 12 with
+// four; 70 of 68: 18, 15 with four, 18 with eight; 8 of 256: 19 with eight, 18
+// with sixteen; 16 of 256: 21 with eight, 32 with sixteen, which take turns).
+int cluster_of(long long units, int tiles, int per_sm, int warps)
 {
     int c = 1;
-    while (c < 8 && units * c * 2 <= resident && tiles >= 3 * c * 2 * warps) c *= 2;
+    while (c < kMaxCluster && units <= clusters_that_fit(2 * c, per_sm) && tiles >= 3 * c * 2 * warps) c *= 2;
     return c;
 }
 
@@ -948,10 +964,10 @@ cudaError_t go(const PagePool& p, const PageRows& r, int budget, int recent, int
     const size_t smem = front + sizeof(AttendSmem<D, Core>) + 4 * ((size_t)wpad + (picks ? budget : 0));
     const auto kernel = page_attend_kernel<T, D, Core>;
     static SmemOnce once;
-    const cudaError_t e = once.allow(kernel);
+    const cudaError_t e = once.allow(kernel, true);
     if (e != cudaSuccess) return e;
     const long long units = (long long)r.rows * p.heads;
-    const int C = cluster_of(units, (budget > 0 ? std::min(budget, r.width) : r.width) * (p.ps / kKeys), (int)(227 * 1024 / (smem + 1024)) * kSMs, NW);
+    const int C = cluster_of(units, (budget > 0 ? std::min(budget, r.width) : r.width) * (p.ps / kKeys), (int)(227 * 1024 / (smem + 1024)), NW);
     cudaLaunchAttribute at[2];
     int na = 0;
     if (C > 1) {
@@ -979,17 +995,17 @@ template <int D, int NW>
 cudaError_t by_groups(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
 {
     if (p.dtype) return go<__nv_bfloat16, D, CoreMma<D, NW>>(p, r, budget, recent, picked, part, st);
-    if (r.G == 1) return go<float, D, CoreSimt<float, D, 1, 4>>(p, r, budget, recent, picked, part, st);
-    if (r.G <= 4) return go<float, D, CoreSimt<float, D, 4, 4>>(p, r, budget, recent, picked, part, st);
-    if (r.G <= 8) return go<float, D, CoreSimt<float, D, 8, 4>>(p, r, budget, recent, picked, part, st);
-    return go<float, D, CoreSimt<float, D, 16, 4>>(p, r, budget, recent, picked, part, st);
+    if (r.G == 1) return go<float, D, CoreSimt<float, D, 1, NW>>(p, r, budget, recent, picked, part, st);
+    if (r.G <= 4) return go<float, D, CoreSimt<float, D, 4, NW>>(p, r, budget, recent, picked, part, st);
+    if (r.G <= 8) return go<float, D, CoreSimt<float, D, 8, NW>>(p, r, budget, recent, picked, part, st);
+    return go<float, D, CoreSimt<float, D, 16, NW>>(p, r, budget, recent, picked, part, st);
 }
 
 template <int D>
 cudaError_t by_warps(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
 {
     const int tiles = (budget > 0 ? std::min(budget, r.width) : r.width) * (p.ps / kKeys);
-    if (attend_warps((long long)r.rows * p.heads, tiles) == 2) return by_groups<D, 2>(p, r, budget, recent, picked, part, st);
+    if (attend_warps((long long)r.rows * p.heads, tiles, p.dtype) == 2) return by_groups<D, 2>(p, r, budget, recent, picked, part, st);
     return by_groups<D, 4>(p, r, budget, recent, picked, part, st);
 }
 

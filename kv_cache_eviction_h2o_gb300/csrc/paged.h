@@ -17,7 +17,7 @@ constexpr int kMaxPrefixSplits = 64;      // ranges of a shared prefix
 // kernel's own static object, so a race between threads sets the same twice).
 struct SmemOnce {
     bool done[64] = {};
-    template <class Kernel> cudaError_t allow(Kernel* kernel)
+    template <class Kernel> cudaError_t allow(Kernel* kernel, bool large_clusters = false)
     {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
@@ -28,6 +28,7 @@ struct SmemOnce {
         e = cudaFuncGetAttributes(&a, kernel);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - (int)a.sharedSizeBytes);
+        if (e == cudaSuccess && large_clusters) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess) done[dev] = true;
         return e;
     }

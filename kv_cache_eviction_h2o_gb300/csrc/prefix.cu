@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(256, 2) prefix_simt_kernel(const PagePool pool
     const int h = blockIdx.z, x0 = blockIdx.x * kRows, G = R.G, nx = R.rows * G;
     const int j0 = blockIdx.y * per, j1 = min(prefix_len, j0 + per);
     grid_launch_dependents();          // the rows' own pass may start on what SMs are left; it waits before it reads sums
+    const bool live = x0 + ty * 4 < nx;    // (of the last tile, warps without rows only help loading)
     bool bad = false;
     const float* K = static_cast<const float*>(pool.K);
     const float* V = static_cast<const float*>(pool.V);
@@ -97,24 +98,25 @@ __global__ void __launch_bounds__(256, 2) prefix_simt_kernel(const PagePool pool
         next.ask(V, pool, table, h, j, j1, bad);
         __syncthreads();
         float z[4][4] = {};
+        if (live)
 #pragma unroll 4
-        for (int d = 0; d < D; d += 4) {
-            float4 a[4], b[4];
+            for (int d = 0; d < D; d += 4) {
+                float4 a[4], b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = *reinterpret_cast<const float4*>(&S.q[ty * 4 + i][d]);
-                b[i] = *reinterpret_cast<const float4*>(&S.kv[tx + 16 * i][d]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    z[i][k] = fmaf(a[i].x, b[k].x, z[i][k]);
-                    z[i][k] = fmaf(a[i].y, b[k].y, z[i][k]);
-                    z[i][k] = fmaf(a[i].z, b[k].z, z[i][k]);
-                    z[i][k] = fmaf(a[i].w, b[k].w, z[i][k]);
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = *reinterpret_cast<const float4*>(&S.q[ty * 4 + i][d]);
+                    b[i] = *reinterpret_cast<const float4*>(&S.kv[tx + 16 * i][d]);
                 }
-        }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        z[i][k] = fmaf(a[i].x, b[k].x, z[i][k]);
+                        z[i][k] = fmaf(a[i].y, b[k].y, z[i][k]);
+                        z[i][k] = fmaf(a[i].z, b[k].z, z[i][k]);
+                        z[i][k] = fmaf(a[i].w, b[k].w, z[i][k]);
+                    }
+            }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float t = -INFINITY;
@@ -143,26 +145,27 @@ __global__ void __launch_bounds__(256, 2) prefix_simt_kernel(const PagePool pool
         next.put(S.kv);
         if (j + kCols < j1) next.ask(K, pool, table, h, j + kCols, j1, bad);
         __syncthreads();
+        if (live)
 #pragma unroll 2
-        for (int c = 0; c < kCols; c += 4) {
-            float4 p[4];
+            for (int c = 0; c < kCols; c += 4) {
+                float4 p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&S.p[ty * 4 + i][c]);
+                for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&S.p[ty * 4 + i][c]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int n = 0; n < NJ; ++n) {
-                    const float4 v = *reinterpret_cast<const float4*>(&S.kv[c + k][n * 64 + tx * 4]);
+                    for (int n = 0; n < NJ; ++n) {
+                        const float4 v = *reinterpret_cast<const float4*>(&S.kv[c + k][n * 64 + tx * 4]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float w = k == 0 ? p[i].x : k == 1 ? p[i].y : k == 2 ? p[i].z : p[i].w;
-                        o[i][n][0] = fmaf(w, v.x, o[i][n][0]);
-                        o[i][n][1] = fmaf(w, v.y, o[i][n][1]);
-                        o[i][n][2] = fmaf(w, v.z, o[i][n][2]);
-                        o[i][n][3] = fmaf(w, v.w, o[i][n][3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const float w = k == 0 ? p[i].x : k == 1 ? p[i].y : k == 2 ? p[i].z : p[i].w;
+                            o[i][n][0] = fmaf(w, v.x, o[i][n][0]);
+                            o[i][n][1] = fmaf(w, v.y, o[i][n][1]);
+                            o[i][n][2] = fmaf(w, v.z, o[i][n][2]);
+                            o[i][n][3] = fmaf(w, v.w, o[i][n][3]);
+                        }
                     }
-                }
-        }
+            }
     }
     // a page that is not there: every row of this range is NaN
     if (__syncthreads_or(bad)) l[0] = l[1] = l[2] = l[3] = NAN;
