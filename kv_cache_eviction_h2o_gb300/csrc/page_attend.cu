@@ -410,11 +410,11 @@ struct CoreSimt {
 
 // The same on the tensor cores (bf16): the G queries are the rows of 16-row
 // products, S = Q K^T with 16 keys and O += P V with P from S's registers.
-// 32 products of 16 x 8 x 16 a tile, a small part of the time its 4 KB of
+// 48 products of 16 x 8 x 16 a tile, a small part of the time its 4 KB of
 // keys and 4 KB of values (head_dim 128) take to arrive; tcgen05's 128 rows
-// would be seven eighths padding here.  P is rounded to bf16 (2^-9 relative a
-// weight, as the output is); l sums the unrounded weights.  The maximum is
-// raised only when a logit passes it by 2^8.
+// would be seven eighths padding here.  There is time for P in two bf16 parts
+// (2^-17 relative a weight, far below the output's own rounding).  The maximum
+// is raised only when a logit passes it by 2^8.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -478,10 +478,10 @@ struct CoreMma {
                 for (int e = 0; e < 4; ++e)
                     if (i * 8 + c + (e & 1) >= valid) z[i][e] = -INFINITY;
         }
-        uint32_t p[4];
+        uint32_t p[4], r[4];                               // the weights in bf16, and what that leaves of them
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            p[x] = p[x + 2] = 0u;
+            p[x] = p[x + 2] = r[x] = r[x + 2] = 0u;
             if (x == 1 && G <= 8) break;                   // rows of padding
             float t = fmaxf(fmaxf(z[0][2 * x], z[0][2 * x + 1]), fmaxf(z[1][2 * x], z[1][2 * x + 1]));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
@@ -502,8 +502,14 @@ struct CoreMma {
 #pragma unroll
             for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaf(z[i >> 1][2 * x + (i & 1)], qscale, -base));
             l[x] += (e[0] + e[1]) + (e[2] + e[3]);
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[x]) : "f"(e[1]), "f"(e[0]));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[x + 2]) : "f"(e[3]), "f"(e[2]));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t& hi = p[x + 2 * i];
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(e[2 * i + 1]), "f"(e[2 * i]));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                    : "=r"(r[x + 2 * i])
+                    : "f"(e[2 * i + 1] - __uint_as_float(hi & 0xffff0000u)), "f"(e[2 * i] - __uint_as_float(hi << 16)));
+            }
         }
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -511,6 +517,8 @@ struct CoreMma {
             ldsm4_t(b, va + (uint32_t)(((k * 2 + (mat >> 1)) ^ r8) << 4));
             mma16816(o[2 * k], p, b[0], b[1]);
             mma16816(o[2 * k + 1], p, b[2], b[3]);
+            mma16816(o[2 * k], r, b[0], b[1]);
+            mma16816(o[2 * k + 1], r, b[2], b[3]);
         }
         __syncwarp();
     }
