@@ -4,36 +4,42 @@
 // Query rows of one cache head (row r's G query heads are rows r G .. r G + G - 1)
 // go in tiles of 128, keys in tiles of 128, and a CTA sweeps a range of the
 // prefix with two score streams:
-//   S = Q K^T      (SMEM x SMEM -> TMEM, M = N = 128, K = D)
+//   S = Q K^T        (SMEM x SMEM -> TMEM, M = 128, K = D)
 //   P = 2^(c S - m)  (128 threads a stream, thread = TMEM lane = query row)
-//   O += P V       (TMEM x SMEM -> TMEM, M = 128, N = D, K = 128)
-// so that one stream's exponentials run under the other's products.  S and P go
-// by halves of 64 keys: while the threads work on one half, the product of the
-// other's P and the next tile's scores in its place are made, so neither waits
-// for the other's latency (whole tiles: 4400 cycles a tile of two streams, of
-// which the products are 2050).  With more
+//   O += P V         (TMEM x SMEM -> TMEM, M = 128, N = D)
+// so that one stream's exponentials run under the other's products.  With more
 // than 128 query rows left the streams are two query tiles over the same keys
 // (each key tile is read once for 256 rows); with fewer they are the even and
-// the odd key tiles of one query tile, joined at the end.
+// the odd key tiles of one query tile, joined at the end.  S and P go by halves
+// of 64 keys: while the threads work on one half, the product of the other's P
+// and the next tile's scores in its place are made, so neither waits for the
+// other's latency.
 //
 // One CTA per SM: TMEM holds S and O of both streams (P overwrites S: the
 // tensor pipe works in the order of issue, and S of the next tile is issued
 // after the product that reads P).  Warp 0 loads key and value tiles with TMA
-// (a box per page and 64 channels, so pages lie anywhere), lane 0 of warp 1
-// issues the products, warps 4..7 and 8..11 are the streams.  A row's maximum
-// m is raised, and O scaled, only when a logit passes it by more than 2^8: the
-// weights are relative to m in any case, and l stays in fp32.  P is rounded
-// to bf16 for the product (2^-9 relative a weight, as the output is), the sums
-// l are of the unrounded weights.  Waits are bounded; one that runs out leaves
-// NaN sums.
+// (a box per page and 64 channels, so pages lie anywhere), warps 1 and 2 issue
+// their stream's products, warps 4..7 and 8..11 are the streams' threads.  A
+// row's maximum m is raised, and O scaled, only when a logit passes it by more
+// than 2^8: the weights are relative to m in any case, and l stays in fp32.  P
+// is rounded to bf16 for the product (2^-9 relative a weight, as the output is;
+// a second product of what that leaves took 13 us of 55 more), the sums l are
+// of the unrounded weights.  Waits are bounded; one that runs out leaves NaN
+// sums.
+//
+// Measured, 64 requests of 8 x 8 heads behind 32768 tokens (68.7 GFLOP): 55 us,
+// 1.24 PFLOP/s, 0.64 of the bf16 peak measured with a library product.  A tile
+// of both streams takes 3200 cycles, of which its products are 2050.  What
+// bounds it is shared memory: the products of Q K^T read both operands from it,
+// those of P V one, and the loads write into it, which makes 2300 cycles of its
+// 128 bytes a cycle; without the loads the products alone run at 73 cycles
+// each, of 64.  About 7 us are the CTA's start (code that runs once, the first
+// loads) and the writing of its sums.
 #include <algorithm>
 
 #include "paged.h"
 #include "tc.cuh"
 
-#ifndef KSTEPS
-#define KSTEPS 2
-#endif
 namespace h2o {
 
 namespace {
@@ -43,7 +49,7 @@ constexpr int kT = 128;
 constexpr int kThreads = 384;
 constexpr uint32_t kBox = kT * 64 * 2;             // 128 rows x 64 channels: 16 KB
 constexpr float kRaise = 8.f;
-constexpr int kSteps = KSTEPS, kStep = kT / kSteps;     // S and P go by parts of a tile
+constexpr int kSteps = 2, kStep = kT / kSteps;     // S and P go by parts of a tile
 
 template <int D> struct Cfg {
     static constexpr int kBoxes = D / 64;
@@ -69,7 +75,8 @@ constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((BMN ? 1u : 0u
 
 // The issuing warp runs its loop as a whole, so that descriptors stay in
 // uniform registers, and one lane (`on`) issues: a loop inside one lane's
-// branch issued a product every 100 to 115 cycles, whatever its size.
+// branch issued a product every 100 to 115 cycles, whatever its size, and one
+// warp for both streams left 4000 cycles a tile.
 __device__ __forceinline__ uint32_t elect_lane()
 {
     uint32_t r;
@@ -173,18 +180,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         auto load = [&](const CUtensorMap* map, int t) {
             if (!ok) return;
-            const int s = at % NS;
+            const int s = at % NS, pages = (valid_of(t) + ps - 1) / ps, i = lane / C::kBoxes, b = lane % C::kBoxes;
+            const bool mine = i < pages;             // this lane's box
+            int pg = mine ? table[(j0 + t * kT) / ps + i] : 0;
+            if ((unsigned)pg >= (unsigned)pool.pages) { pg = 0; *(volatile int*)&S.bad = 1; }
             if (at >= NS) ok = __all_sync(0xffffffffu, wait(S, &S.empty[s], at / NS - 1));
             if (!ok) return;
-            const int pages = (valid_of(t) + ps - 1) / ps;
             if (lane == 0) mbar_arrive_expect_tx(&S.full[s], (uint32_t)pages * page_bytes * C::kBoxes);
             __syncwarp();
-            if (lane < pages * C::kBoxes) {
-                const int i = lane / C::kBoxes, b = lane % C::kBoxes;
-                int pg = table[(j0 + t * kT) / ps + i];
-                if ((unsigned)pg >= (unsigned)pool.pages) { pg = 0; *(volatile int*)&S.bad = 1; }
-                tma_load_2d(S.ring[s] + b * kBox + i * page_bytes, map, b * 64, (pg * pool.heads + h) * ps, &S.full[s]);
-            }
+            if (mine) tma_load_2d(S.ring[s] + b * kBox + i * page_bytes, map, b * 64, (pg * pool.heads + h) * ps, &S.full[s]);
             __syncwarp();
             ++at;
         };
@@ -193,9 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             load(&mapV, t);
             if (t + L < n) load(&mapK, t + L);
         }
-        // a load that was never used (an aborted sweep) lands before the shared memory is given up
-        if (lane == 0 && *(volatile int*)&S.abort)
-            for (int i = max(0, at - NS); i < at; ++i) mbar_wait(&S.full[i % NS], (uint32_t)(i / NS) & 1u);
+        // every load has landed before the shared memory is given up, those of an abandoned sweep too
+        for (int i = max(0, at - NS); i < at; ++i) mbar_wait(&S.full[i % NS], (uint32_t)(i / NS) & 1u);
     } else if (warp <= 2) {
         // ------------------------------------------------ products of stream s
         const int s = warp - 1;
