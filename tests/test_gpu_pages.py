@@ -321,7 +321,7 @@ def test_prefix(dtype, heads, groups, d, ps):
 
 @pytest.mark.parametrize("dtype,rows,heads,groups,d,plen", [
     (BF16, 1, 1, 1, 128, 4099), (BF16, 129, 1, 1, 128, 700), (BF16, 40, 2, 8, 128, 2500), (BF16, 67, 1, 8, 64, 1111),
-    (BF16, 300, 3, 1, 64, 257), (BF16, 33, 1, 16, 128, 129), (F32, 70, 2, 4, 64, 600), (F32, 65, 1, 1, 128, 333),
+    (BF16, 300, 3, 1, 64, 257), (BF16, 33, 1, 16, 128, 129), (BF16, 1000, 1, 16, 64, 300), (F32, 70, 2, 4, 64, 600), (F32, 65, 1, 1, 128, 333),
 ])
 def test_prefix_many_rows(dtype, rows, heads, groups, d, plen):
     g = np.random.default_rng(rows)
@@ -567,6 +567,63 @@ def test_strided_rows_and_another_stream():
     side.synchronize()
     _check(hold[:, 8:], _prefix_ref(c, q, seq, pos, c.table[2], 490, 0.1), "prefix")
     assert (hold[:, :8] == 3).all()
+
+
+def test_outputs_in_the_place_of_queries():
+    c = Cache([300, 200, 500], 2, 128, 32, BF16, seed=3)
+    seq, pos = [0, 1, 1, 0], [299, 150, 199, 17]
+    q = _queries(4, 8, 128, BF16, 2)
+    a, b = q.cuda(), q.cuda()
+    _sparse(c, a, seq, pos, 4, 1, 0.1, out=a)
+    _prefix(c, b, seq, pos, c.table[2], 490, 0.1, out=b)
+    assert torch.equal(a, _sparse(c, q.cuda(), seq, pos, 4, 1, 0.1)[0])
+    assert torch.equal(b, _prefix(c, q.cuda(), seq, pos, c.table[2], 490, 0.1))
+
+
+def test_calls_on_two_streams_at_once():
+    c = Cache([3000, 2000, 5000], 2, 128, 32, BF16, seed=6)
+    K, V, B, table = c.K.cuda(), c.V.cuda(), c.bounds().cuda(), _i32(c.table)
+    seq, pos = _i32([0, 1, 1, 0] * 8), _i32([2999, 1500, 1999, 170] * 8)
+    q = _queries(32, 8, 128, BF16, 2).cuda()
+    n = L.h2o_prefix_work_bytes(32, 2, 4, 128, 4900, L.H2O_BF16)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    bufs = [(torch.empty_like(q), torch.empty_like(q), torch.empty(n, dtype=torch.uint8, device="cuda")) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (a, b, w) in zip(streams, bufs):
+            L.h2o_page_attend(q, seq, pos, K, V, B, table, 9, 2, 0.1, a, None, st)
+            L.h2o_prefix_attend(q, seq, pos, K, V, table[2], 4900, table, 0.1, b, w, st)
+    torch.cuda.synchronize()
+    assert torch.equal(bufs[0][0], bufs[1][0]) and torch.equal(bufs[0][1], bufs[1][1])
+    want = _sparse_ref(c, q[:4].cpu(), [0, 1, 1, 0], [2999, 1500, 1999, 170], 9, 2, 0.1)[0]
+    _check(bufs[0][0][:4], want, "sparse")
+    _check(bufs[0][1][:4], _prefix_ref(c, q[:4].cpu(), [0, 1, 1, 0], [2999, 1500, 1999, 170], c.table[2], 4900, 0.1), "prefix")
+
+
+@pytest.mark.parametrize("dtype,pages", [(BF16, 40000), (F32, 36000)])
+def test_offsets_beyond_32_bits(dtype, pages):
+    """The pool holds more than 2^31 elements, the request its last pages: the
+    bits are those of a small pool with the same pages."""
+    heads, ps, d, n = 8, 64, 128, 11
+    assert pages * heads * ps * d > 2 ** 31
+    K, V = (torch.empty(pages, heads, ps, d, dtype=dtype, device="cuda") for _ in range(2))
+    B = torch.empty(pages, heads, 2, d, dtype=dtype, device="cuda")
+    k, v, q = (_queries(n * ps, h, d, dtype, i).cuda() for i, h in enumerate((heads, heads, 16)))
+    stream = torch.cuda.current_stream()
+    got = []
+    for first, (pk, pv, pb) in ((pages - n, (K, V, B)), (0, tuple(torch.empty(n, *x.shape[1:], dtype=dtype, device="cuda") for x in (K, V, B)))):
+        slot = torch.arange(first * ps, (first + n) * ps, dtype=torch.int32, device="cuda")
+        L.h2o_page_write(k, v, slot, pk, pv, pb, stream)
+        table = torch.arange(first, first + n, dtype=torch.int32, device="cuda")[None]
+        seq, pos = _i32([0] * 5), _i32([n * ps - 1, 400, 64, 63, 0])
+        a, b = torch.empty_like(q[:5]), torch.empty_like(q[:5])
+        picked = torch.empty(5, heads, 3, dtype=torch.int32, device="cuda")
+        L.h2o_page_attend(q[:5], seq, pos, pk, pv, pb, table, 3, 1, 0.1, a, picked, stream)
+        w = torch.empty(L.h2o_prefix_work_bytes(5, heads, 2, d, 600, L._CODES[str(dtype)]), dtype=torch.uint8, device="cuda")
+        L.h2o_prefix_attend(q[:5], seq, pos, pk, pv, table[0], 600, table, 0.1, b, w, stream)
+        got.append((pk[first:first + n].clone(), pb[first:first + n].clone(), a, picked, b))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
 
 
 def test_captured_steps_read_what_their_buffers_hold_then():
