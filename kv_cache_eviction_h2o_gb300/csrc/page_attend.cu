@@ -191,7 +191,7 @@ __device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned
     const float amax = __uint_as_float(P.amax);
     float above = INFINITY, below = -INFINITY;             // decided: s > above is in, s < below is out
     int in = 0;                                            // pages decided to be in
-    if (amax < FLT_MAX) {                                  // (an infinity or NaN among the factors decides nothing)
+    if (amax < FLT_MAX / 2) {                              // (an infinity or NaN among the factors, or a sum, decides nothing)
         const Held<NT> held(s, n);
         unsigned a = ~0u, b = 0u;
         held.each([&](unsigned k) { a = min(a, k ? k : ~0u); b = max(b, k); });
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                 if ((unsigned)p >= (unsigned)pool.pages) return (double)NAN;
                 const T* b = bounds + ((size_t)p * pool.heads + h) * 2 * D;
                 double s = 0.0;
-                if (__uint_as_float(S.pick.amax) < FLT_MAX) {
+                if (__uint_as_float(S.pick.amax) < FLT_MAX) {      // (finite factors; fp64 holds their sum)
                     for (int e = lane; e < 2 * D; e += 32) s += ((double)S.w[e].x + (double)S.w[e].y) * (double)Elem<T>::to_f(b[e]);
                 } else {
                     // an infinite bound on the side that no query takes counts for nothing: the maxima themselves

@@ -235,6 +235,18 @@ def test_sparse_infinite_and_nan_keys(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kscale", [3e35, 8e35, 3e36])      # sums of |w||bound| below, about and above fp32's largest
+def test_sparse_scores_near_the_end_of_fp32(dtype, kscale):
+    ps, n = 16, 60
+    c = Cache([n * ps], 2, 64, ps, dtype, seed=21, kscale=kscale)
+    q = _queries(1, 2, 64, dtype, 22)
+    want, picked = _sparse_ref(c, q, [0], [n * ps - 1], 9, 2, 1 / (8 * kscale))
+    out, got = _sparse(c, q.cuda(), [0], [n * ps - 1], 9, 2, 1 / (8 * kscale))
+    np.testing.assert_array_equal(got.cpu().numpy(), picked)
+    _check(out, want, "large scores")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_sparse_large_logits(dtype):
     # one key takes all the weight, whatever the scale of the logits
     c = Cache([500], 2, 64, 16, dtype, seed=8, kscale=40.0)
