@@ -462,11 +462,12 @@ int h2o_selftest_wait_timeout(h2o_handle h);
  *             (slot is also -1 where a table or free-list entry is no page
  *             number);
  *   status    [4]: {rows, pages taken, longest len_after, error bits}.
- * All arrays are device int32; no output overlaps an input.  free_pages is
- * only read: the caller drops the first status[1] of it.  All or nothing: with
- * an error bit (1: a negative count, 2: more than rows_cap rows, 4: more than
- * n_free pages, 8: a request longer than table_width pages) no page is taken,
- * len_after is len_before and there are no rows.  1 <= requests <= 16384, rows_cap <= 2^30.
+ * All arrays are device int32; an output that overlaps an input is refused
+ * (so len_after is not len_before).  free_pages is only read: the caller
+ * drops the first status[1] of it.  All or nothing: with an error bit (1: a
+ * negative count, 2: more than rows_cap rows, 4: more than n_free pages, 8: a
+ * request longer than table_width pages) no page is taken, len_after is
+ * len_before and there are no rows.  1 <= requests <= 16384, rows_cap <= 2^30.
  */
 int h2o_page_tables(const int* len_before, const int* n_new, int requests, const int* free_pages, int n_free,
                     int page_size, int* table, int table_width, int* len_after, int* row_start, int* row_seq,
@@ -494,8 +495,8 @@ int h2o_page_write(const void* k, const void* v, long long k_stride, long long v
  * others of the largest
  *   s_b = sum_g sum_e max(q_ge bounds_b0e, q_ge bounds_b1e),
  * the sum over the head's `groups` query heads of the largest dot product
- * that keys within page b's bounds allow (by the exact value of s_b, ties to
- * the lower page; a NaN ranks first).  Only full pages older than the row's
+ * that keys within page b's bounds allow (by s_b in fp64 where fp32 does not
+ * settle the order, ties to the lower page; a NaN ranks first).  Only full pages older than the row's
  * own are ranked.  out = softmax(scale q.K) V over the tokens of those pages.
  *   q, out [rows][kv_heads * groups][head_dim] of dtype (sums in fp32; bf16
  *   weights and outputs are rounded once), query head h * groups + g to cache

@@ -101,6 +101,16 @@ int h2o_page_tables(const int* len_before, const int* n_new, int requests, const
     const void* all[] = {len_before, n_new, free_pages, table, len_after, row_start, row_seq, row_pos, slot, status};
     for (const void* p : all)
         if (!aligned4(p)) return set_last_error(H2O_ERR_ARG, "h2o_page_tables arrays must be 4-byte aligned");
+    // (CTAs read the inputs while others write: lengths updated in place would be taken for both)
+    struct Range { const int* p; long long n; };
+    const Range in[] = {{len_before, requests}, {n_new, requests}, {free_pages, n_free}};
+    const Range out[] = {{table, (long long)requests * table_width}, {len_after, requests}, {row_start, requests + 1LL},
+                         {row_seq, rows_cap}, {row_pos, rows_cap}, {slot, rows_cap}, {status, 4}};
+    for (const Range& x : in)
+        for (const Range& y : out)
+            if (x.n && y.n && reinterpret_cast<uintptr_t>(x.p) < reinterpret_cast<uintptr_t>(y.p) + y.n * sizeof(int) &&
+                reinterpret_cast<uintptr_t>(y.p) < reinterpret_cast<uintptr_t>(x.p) + x.n * sizeof(int))
+                return set_last_error(H2O_ERR_ARG, "an output of h2o_page_tables overlaps an input");
     if (inject_launch()) return set_last_error(H2O_ERR_CUDA, "kernel launch failed (injected)");
     TablesArgs a = {};
     a.before = len_before; a.fresh = n_new; a.free_pages = free_pages; a.table = table; a.after = len_after;

@@ -41,6 +41,16 @@ def test_tables_refuses(L, change, frag):
     _refused(L, "h2o_page_tables", TABLES, change, frag)
 
 
+@pytest.mark.parametrize("change", [
+    dict(after=1 << 20), dict(start=(1 << 20) + 12), dict(table=(1 << 20) - 4 * 4 * 4 + 4), dict(status=2 << 20), dict(slot=(3 << 20) - 28),
+    dict(seq=(3 << 20) + 28), dict(pos=2 << 20),
+])
+def test_tables_refuses_outputs_over_inputs(L, change):
+    apart = dict(TABLES, **{k: (i + 1) << 20 for i, k in enumerate(("before", "new", "free", "table", "after", "start", "seq", "pos",
+                                                                  "slot", "status"))})
+    _refused(L, "h2o_page_tables", apart, change, "overlaps")
+
+
 POOL = [
     (dict(K=None), "non-NULL"), (dict(V=FAKE + 8), "aligned"), (dict(dtype=8), "dtype"), (dict(d=96), "head_dim"),
     (dict(ps=8), "page_size"), (dict(ps=256), "page_size"), (dict(pages=0), "num_pages"), (dict(heads=0), "kv_heads"),
