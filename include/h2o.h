@@ -516,8 +516,8 @@ int h2o_page_attend(const void* q, long long q_stride, const int* row_seq, const
 
 /*
  * h2o_prefix_attend -- attention of a batch whose requests share a prefix:
- * row r attends to the prefix's prefix_len >= 0 tokens, which are on the pages
- * prefix_table lists, and to the tokens 0..row_pos[r] of its request's own
+ * row r attends to the prefix's prefix_len (0 to 2^30) tokens, which are on the
+ * pages prefix_table lists, and to the tokens 0..row_pos[r] of its request's own
  * table (positions and lengths count from the prefix's end; row_pos -1: none).
  * The prefix is read once for all rows, whatever their number, as a product
  * over all queries of a cache head.  With prefix_len 0 (prefix_table NULL)

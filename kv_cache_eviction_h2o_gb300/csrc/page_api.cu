@@ -171,7 +171,7 @@ int h2o_page_attend(const void* q, long long q_stride, const int* row_seq, const
 long long h2o_prefix_work_bytes(int rows, int kv_heads, int groups, int head_dim, int prefix_len, int dtype)
 {
     if (rows < 0 || kv_heads < 1 || groups < 1 || groups > kMaxPageGroups || (head_dim != 64 && head_dim != 128) ||
-        prefix_len < 0 || (dtype != H2O_F32 && dtype != H2O_BF16) || (long long)rows * kv_heads > (1 << 24) / groups)
+        prefix_len < 0 || prefix_len > kMaxPrefix || (dtype != H2O_F32 && dtype != H2O_BF16) || (long long)rows * kv_heads > (1 << 24) / groups)
         return set_last_error(H2O_ERR_ARG, "h2o_prefix_work_bytes: sizes out of range");
     const long long qrows = (long long)rows * kv_heads * groups;
     // at least 16 bytes, so that the buffer is one
@@ -192,7 +192,8 @@ int h2o_prefix_attend(const void* q, long long q_stride, const int* row_seq, con
     r.qscale = (float)(scale * 1.4426950408889634);
     int rc;
     if ((rc = check_pool(p)) || (rc = check_rows(p, r, scale))) return rc;
-    if (prefix_len < 0) return set_last_error(H2O_ERR_ARG, "prefix_len must be >= 0 (got %d)", prefix_len);
+    if (prefix_len < 0 || prefix_len > kMaxPrefix)
+        return set_last_error(H2O_ERR_ARG, "prefix_len must be in [0, 2^30] (got %d)", prefix_len);
     if (prefix_len && (!prefix_table || !aligned4(prefix_table)))
         return set_last_error(H2O_ERR_ARG, "prefix_table must be non-NULL and 4-byte aligned");
     const long long need = h2o_prefix_work_bytes(rows, kv_heads, groups, head_dim, prefix_len, dtype);

@@ -12,6 +12,7 @@ constexpr int kMaxTableWidth = 16384;     // pages of one request
 constexpr int kMaxPickedPages = 4096;     // budget of a call that has to choose
 constexpr int kMaxPageGroups = 16;        // query heads per cache head
 constexpr int kMaxPrefixSplits = 64;      // ranges of a shared prefix
+constexpr int kMaxPrefix = 1 << 30;       // tokens of a shared prefix (positions rounded up to a tile fit an int)
 
 // Lets a kernel use all shared memory a CTA can have, once per device (a
 // kernel's own static object, so a race between threads sets the same twice).

@@ -51,6 +51,15 @@ def test_tables_refuses_outputs_over_inputs(L, change):
     _refused(L, "h2o_page_tables", apart, change, "overlaps")
 
 
+def test_prefixes_beyond_its_range_are_refused(L):
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        _refused(L, "h2o_prefix_attend", PREFIX, dict(plen=n), "prefix_len")
+        with pytest.raises(L.H2OError):
+            L.h2o_prefix_work_bytes(4, 8, 4, 128, n, L.H2O_BF16)
+    for dtype in (L.H2O_BF16, L.H2O_F32):
+        assert L.h2o_prefix_work_bytes(4, 8, 4, 128, 1 << 30, dtype) > 0
+
+
 POOL = [
     (dict(K=None), "non-NULL"), (dict(V=FAKE + 8), "aligned"), (dict(dtype=8), "dtype"), (dict(d=96), "head_dim"),
     (dict(ps=8), "page_size"), (dict(ps=256), "page_size"), (dict(pages=0), "num_pages"), (dict(heads=0), "kv_heads"),
