@@ -119,8 +119,8 @@ __device__ __forceinline__ int v_at(int t, int n, int L) { return t + min(n, t +
 template <int D>
 __device__ __forceinline__ bool wait(Smem<D>& S, uint64_t* bar, int count)
 {
-    // the barrier's phase number `count` (from 0)
-    if (mbar_wait(bar, (uint32_t)count & 1u)) return *(volatile int*)&S.abort == 0;
+    // the barrier's phase number `count` (from 0); once one wait has run out the others do, each for itself
+    if (mbar_wait(bar, (uint32_t)count & 1u)) return true;
     *(volatile int*)&S.abort = 1;
     return false;
 }
@@ -221,9 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             commit(on, &S.s_ready[s][b]);
         };
-        // nth: tiles of this stream before; valid: keys of the tile
+        // nth: tiles of this stream before; valid: keys of the tile, which is there
         auto values = [&](int b, int nth, int i, int valid) {
-            slot_full(i);
             if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.p_ready[s][b], nth));
             if (!ok) return;
             tc_fence_after();
@@ -253,11 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = t0, nth = 0; t < n; t += stride, ++nth) {
             const int v = v_at(t, n, L), k = v + 1;
             const bool more = t + stride < n;
+            slot_full(v);                            // (both before the weights: between them and the products every look at a
+            if (more) slot_full(k);                  // barrier is waited for, and with four of them the loop took a tenth longer)
             for (int b = 0; b < kSteps; ++b) {
                 values(b, nth, v, valid_of(t));
                 if (b == kSteps - 1) release(v);
                 if (more) {
-                    if (b == 0) slot_full(k);
                     score(b, k);
                     if (b == kSteps - 1) release(k);
                 }
