@@ -55,6 +55,9 @@ template <int D> struct Cfg {
     static constexpr int kBoxes = D / 64;
     static constexpr uint32_t kTile = kBoxes * kBox;
     static constexpr int kSlots = D == 128 ? 5 : 8;    // K and V tiles in flight
+    static constexpr int kPitch = D * 4 + 16;          // of a row of sums on its way out (16 bytes more: no bank conflicts)
+    static constexpr int kHandOver = D * kT * 4;       // sums of a stream
+    static_assert(2 * kT * kPitch <= kSlots * (int)kTile && kHandOver + kT * kPitch <= kSlots * (int)kTile, "the ring holds them");
 };
 
 template <int D>
@@ -102,6 +105,16 @@ __device__ __forceinline__ void commit(uint32_t on, uint64_t* bar)
     asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
                  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(on)
                  : "memory");
+}
+
+// a copy of `bytes` (a multiple of 16) out of shared memory by this thread, and the end of all it started
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait()
+{
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // descriptor of the value tile as the K x N operand, N (channels) contiguous:
@@ -397,22 +410,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 
         // ------------------------------------------------ results
-        // one query tile: stream 1 hands its sums over in the ring (nothing is in flight there: both streams are through)
-        bool all = true;
-        if (!two) {
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            all = __all_sync(0xffffffffu, ok && *(volatile int*)&S.abort == 0);
-            float* xo = reinterpret_cast<float*>(S.ring[0]);
+        // Both streams are through, so nothing reads the ring or is in flight to it: rows are put together there and leave
+        // as one bulk copy each (through a swizzled piece and whole-row stores of a warp this took 7000 cycles, much of it
+        // for fetching the code).  One query tile: stream 1 hands its sums over first.
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const bool fine = __all_sync(0xffffffffu, ok && *(volatile int*)&S.abort == 0), join = !two && n > 1;
+        float* xo = reinterpret_cast<float*>(S.ring[0]);
+        if (join) {
             if (s == 1) {
                 S.xml[row] = make_float2(m, l);
-                if (all && steps > 0)
+                if (fine)
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tc_ld16_issue(tO(1) + lanes + (uint32_t)c, o);
-                        tc_ld16_wait(o);
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc_ld32_issue(tO(1) + lanes + (uint32_t)c, o);
+                        tc_ld32_wait(o);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) xo[(c + k) * kT + row] = __uint_as_float(o[k]);
+                        for (int k = 0; k < 32; ++k) xo[(c + k) * kT + row] = __uint_as_float(o[k]);
                     }
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -420,8 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = x0 + s * kT + row;
         if (two || s == 0) {
             float a = 1.f, b = 0.f;                              // of this stream's sums, of the other's
-            const float* xo = reinterpret_cast<const float*>(S.ring[0]);
-            const bool join = !two && n > 1;
             if (join) {
                 const float2 y = S.xml[row];
                 const float mm = fmaxf(m, y.x), base = mm == -INFINITY ? 0.f : mm;
@@ -430,40 +442,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = l * a + y.y * b;
                 m = mm;
             }
-            const bool fine = __all_sync(0xffffffffu, ok && all && *(volatile int*)&S.abort == 0);
             const size_t qr = ((size_t)blockIdx.y * R.rows * pool.heads + (size_t)(x / G) * pool.heads + h) * G + x % G;
             if (x < nx) part.ml[qr] = make_float2(m, fine && *(volatile int*)&S.bad == 0 ? l : NAN);
-            // half the channels at a time through this warp's part of the query tiles (every score is made by now), so
-            // that rows are written whole: 16-byte chunk c of row r at chunk c ^ (r % chunks)
-            constexpr int W = D / 2, CH = W / 4;
-            float4* stage = reinterpret_cast<float4*>(S.q[0]) + ((two ? s * 4 : 0) + w) * (32 * CH);
-            if (fine)
+            if (fine) {
+                uint8_t* mine = S.ring[0] + (two ? (s * kT + row) * C::kPitch : C::kHandOver + row * C::kPitch);
 #pragma unroll 1
-                for (int d0 = 0; d0 < D; d0 += W) {
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tc_ld32_issue(tO(s) + lanes + (uint32_t)c, o);
+                    tc_ld32_wait(o);
 #pragma unroll
-                    for (int c = 0; c < W; c += 16) {
-                        uint32_t o[16];
-                        tc_ld16_issue(tO(s) + lanes + (uint32_t)(d0 + c), o);
-                        tc_ld16_wait(o);
-                        float f[16];
+                    for (int k = 0; k < 32; k += 4) {
+                        float f[4];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            f[k] = __uint_as_float(o[k]) * a;
-                            if (join) f[k] = fmaf(b, xo[(d0 + c + k) * kT + row], f[k]);
+                        for (int e = 0; e < 4; ++e) {
+                            f[e] = __uint_as_float(o[k + e]) * a;
+                            if (join) f[e] = fmaf(b, xo[(c + k + e) * kT + row], f[e]);
                         }
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            stage[lane * CH + (((c + k) / 4) ^ (lane & (CH - 1)))] = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+                        *reinterpret_cast<float4*>(mine + (c + k) * 4) = make_float4(f[0], f[1], f[2], f[3]);
                     }
-                    __syncwarp();
-#pragma unroll 4
-                    for (int r = lane / CH; r < 32; r += 32 / CH) {
-                        const size_t to = __shfl_sync(0xffffffffu, (unsigned)qr, r);   // (below 2^30)
-                        if (x - lane + r < nx)
-                            *reinterpret_cast<float4*>(part.o + to * D + d0 + (lane % CH) * 4) = stage[r * CH + ((lane % CH) ^ (r & (CH - 1)))];
-                    }
-                    __syncwarp();
                 }
+                fence_proxy_async_smem();
+                if (x < nx) bulk_store(part.o + qr * D, mine, D * 4);
+                bulk_store_wait();
+            }
         }
     }
     tc_fence_before();
