@@ -56,15 +56,13 @@ template <int D> struct Cfg {
     static constexpr uint32_t kTile = kBoxes * kBox;
     static constexpr int kSlots = D == 128 ? 5 : 8;    // K and V tiles in flight
     static constexpr int kPitch = D * 4 + 16;          // of a row of sums on its way out (16 bytes more: no bank conflicts)
-    static constexpr int kHandOver = D * kT * 4;       // sums of a stream
-    static_assert(2 * kT * kPitch <= kSlots * (int)kTile && kHandOver + kT * kPitch <= kSlots * (int)kTile, "the ring holds them");
+    static_assert(2 * kT * kPitch <= kSlots * (int)kTile, "the ring holds them");
 };
 
 template <int D>
 struct alignas(1024) Smem {
     uint8_t q[2][Cfg<D>::kTile];
     uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
-    float2 xml[kT];
     uint64_t full[Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
     uint64_t q_ready, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2], last;   // [stream][part of the tile]
     uint32_t tmem;
@@ -107,14 +105,14 @@ __device__ __forceinline__ void commit(uint32_t on, uint64_t* bar)
                  : "memory");
 }
 
-// a copy of `bytes` (a multiple of 16) out of shared memory by this thread, and the end of all it started
+// a copy of `bytes` (a multiple of 16) out of shared memory by this thread, and the end of reading by all it started
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
 {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_store_wait()
 {
-    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // descriptor of the value tile as the K x N operand, N (channels) contiguous:
@@ -142,7 +140,7 @@ __device__ __forceinline__ bool wait(Smem<D>& S, uint64_t* bar, int count)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV, const PagePool pool,
-                     const PageRows R, const int* __restrict__ table, const int prefix_len, const int per, const PrefixPart part)
+                     const PageRows R, const int* __restrict__ table, const int prefix_len, const int per, const PrefixPart part, const unsigned long long inv)
 {
     using C = Cfg<D>;
     constexpr int NS = C::kSlots;
@@ -154,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int L = two ? 1 : 2;
     const int j0 = blockIdx.y * per, j1 = min(prefix_len, j0 + per);
     const int n = (j1 - j0 + kT - 1) / kT;           // key tiles, at least one
+    auto over_G = [&](int x) { return (long long)((unsigned long long)(unsigned)x * inv >> 32); };   // x / G (x < 2^28)
     auto valid_of = [&](int t) { return min(kT, j1 - j0 - t * kT); };
 
     grid_launch_dependents();                        // the rows' own pass may start on what SMs are left; it waits before it reads sums
@@ -288,29 +287,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             // fetched from far away, and the unrolled form took 5000 cycles)
             constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows a step
             const int c = lane % LPR;
-            int r = w * 32 + lane / LPR, x = x0 + s * kT + r, qr = x / G, g = x - qr * G;
-            uint8_t* dst = S.q[s] + (c / 8) * kBox;
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.q) + (size_t)h * G * D + c * 8;
+            const long long gap = R.q_stride - G * D;    // row x of the cache head is at (x / G) q_stride + (x % G) D
+            const uint32_t dst = smem_u32(S.q[s] + (c / 8) * kBox);
 #pragma unroll 1
-            for (int i = 0; i < LPR; ++i) {
+            for (int r = w * 32 + lane / LPR; r < w * 32 + 32; r += RPI) {
+                const int x = x0 + s * kT + r;
                 const bool fill = x < nx;
-                const __nv_bfloat16* from = fill ? src + (size_t)qr * R.q_stride + g * D : src;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4))),
-                             "l"(from), "r"(fill ? 16 : 0)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                             "l"(fill ? src + over_G(x) * gap + (long long)x * D : src), "r"(fill ? 16 : 0)
                              : "memory");
-                r += RPI;
-                x += RPI;
-                g += RPI;
-                while (g >= G) {
-                    g -= G;
-                    ++qr;
-                }
             }
             asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.q_ready);
         }
+        const int x = x0 + s * kT + row, xr = (int)over_G(x);
+        const unsigned qr = ((unsigned)(blockIdx.y * R.rows + xr) * pool.heads + h) * G + (x - xr * G);   // its row of sums (below 2^30)
         const float c2 = R.qscale;
         const int steps = kSteps * (two ? n : (n + 1 - s) / 2);   // parts of this stream's tiles
         float m = -INFINITY, l = 0.f;
@@ -411,62 +405,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // ------------------------------------------------ results
         // Both streams are through, so nothing reads the ring or is in flight to it: rows are put together there and leave
-        // as one bulk copy each (through a swizzled piece and whole-row stores of a warp this took 7000 cycles, much of it
-        // for fetching the code).  One query tile: stream 1 hands its sums over first.
+        // as one bulk copy each.  One query tile: stream 1 leaves its part of the rows first, stream 0 adds its own.
+        // (Little code: at the end of a kernel every line of it is fetched anew, about 230 cycles for 8 instructions.)
+        float2* other = reinterpret_cast<float2*>(S.q[1]);       // both streams' (m, l); one query tile leaves the second's place
+        if (!two) other[s * kT + row] = make_float2(m, l);
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const bool fine = __all_sync(0xffffffffu, ok && *(volatile int*)&S.abort == 0), join = !two && n > 1;
-        float* xo = reinterpret_cast<float*>(S.ring[0]);
+        float a = 1.f;
         if (join) {
-            if (s == 1) {
-                S.xml[row] = make_float2(m, l);
-                if (fine)
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc_ld32_issue(tO(1) + lanes + (uint32_t)c, o);
-                        tc_ld32_wait(o);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) xo[(c + k) * kT + row] = __uint_as_float(o[k]);
-                    }
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const float2 y = other[(s ^ 1) * kT + row];
+            const float mm = fmaxf(m, y.x), base = mm == -INFINITY ? 0.f : mm;
+            a = ex2_fast(m - base);
+            l = fmaf(l, a, y.y * ex2_fast(y.x - base));
+            m = mm;
         }
-        const int x = x0 + s * kT + row;
-        if (two || s == 0) {
-            float a = 1.f, b = 0.f;                              // of this stream's sums, of the other's
-            if (join) {
-                const float2 y = S.xml[row];
-                const float mm = fmaxf(m, y.x), base = mm == -INFINITY ? 0.f : mm;
-                a = ex2_fast(m - base);
-                b = ex2_fast(y.x - base);
-                l = l * a + y.y * b;
-                m = mm;
-            }
-            const size_t qr = ((size_t)blockIdx.y * R.rows * pool.heads + (size_t)(x / G) * pool.heads + h) * G + x % G;
-            if (x < nx) part.ml[qr] = make_float2(m, fine && *(volatile int*)&S.bad == 0 ? l : NAN);
-            if (fine) {
-                uint8_t* mine = S.ring[0] + (two ? (s * kT + row) * C::kPitch : C::kHandOver + row * C::kPitch);
+        const bool adds = join && s == 0, leaves = two || s == 0;
+        if (adds) asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (fine && (leaves || join)) {
+            float* mine = reinterpret_cast<float*>(S.ring[0] + ((two ? s * kT : 0) + row) * C::kPitch);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tc_ld32_issue(tO(s) + lanes + (uint32_t)c, o);
-                    tc_ld32_wait(o);
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tc_ld32_issue(tO(s) + lanes + (uint32_t)c, o);
+                tc_ld32_wait(o);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        float f[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            f[e] = __uint_as_float(o[k + e]) * a;
-                            if (join) f[e] = fmaf(b, xo[(c + k + e) * kT + row], f[e]);
-                        }
-                        *reinterpret_cast<float4*>(mine + (c + k) * 4) = make_float4(f[0], f[1], f[2], f[3]);
-                    }
+                for (int k = 0; k < 32; k += 4) {
+                    float4* to = reinterpret_cast<float4*>(mine + c + k);
+                    float4 f = adds ? *to : make_float4(0.f, 0.f, 0.f, 0.f);
+                    f.x = fmaf(__uint_as_float(o[k]), a, f.x);
+                    f.y = fmaf(__uint_as_float(o[k + 1]), a, f.y);
+                    f.z = fmaf(__uint_as_float(o[k + 2]), a, f.z);
+                    f.w = fmaf(__uint_as_float(o[k + 3]), a, f.w);
+                    *to = f;
                 }
+            }
+            if (leaves && x < nx) {
                 fence_proxy_async_smem();
-                if (x < nx) bulk_store(part.o + qr * D, mine, D * 4);
-                bulk_store_wait();
+                bulk_store(part.o + (size_t)qr * D, mine, D * 4);
             }
         }
+        if (join && s == 1) asm volatile("bar.arrive 2, 256;" ::: "memory");
+        if (leaves && x < nx) part.ml[qr] = make_float2(m, fine && *(volatile int*)&S.bad == 0 ? l : NAN);
+        bulk_store_wait();
     }
     tc_fence_before();
     __syncthreads();
@@ -499,7 +479,8 @@ cudaError_t go(const PagePool& p, const PageRows& r, const int* table, int prefi
     static SmemOnce once;
     const cudaError_t e = once.allow(prefix_tc_kernel<D>);
     if (e != cudaSuccess) return e;
-    prefix_tc_kernel<D><<<grid, kThreads, smem, st>>>(mk, mv, p, r, table, prefix_len, per, part);
+    const unsigned long long inv = ((1ull << 32) + r.G - 1) / r.G;
+    prefix_tc_kernel<D><<<grid, kThreads, smem, st>>>(mk, mv, p, r, table, prefix_len, per, part, inv);
     return cudaGetLastError();
 }
 
