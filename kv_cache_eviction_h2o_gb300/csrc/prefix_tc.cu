@@ -27,14 +27,16 @@
 // of the unrounded weights.  Waits are bounded; one that runs out leaves NaN
 // sums.
 //
-// Measured, 64 requests of 8 x 8 heads behind 32768 tokens (68.7 GFLOP): 55 us,
-// 1.24 PFLOP/s, 0.64 of the bf16 peak measured with a library product.  A tile
-// of both streams takes 3200 cycles, of which its products are 2050.  What
-// bounds it is shared memory: the products of Q K^T read both operands from it,
-// those of P V one, and the loads write into it, which makes 2300 cycles of its
-// 128 bytes a cycle; without the loads the products alone run at 73 cycles
-// each, of 64.  About 7 us are the CTA's start (code that runs once, the first
-// loads) and the writing of its sums.
+// Measured, 64 requests of 8 x 8 heads behind 32768 tokens (68.7 GFLOP): 51 us,
+// 1.35 PFLOP/s, 0.69 of the bf16 peak measured with a library product.  A tile
+// of both streams takes 2850 cycles, of which its products are 2050.  What
+// bounds it is the products and the shared memory that feeds them: those of
+// Q K^T read both operands from it (by halves of 64 keys the queries twice),
+// those of P V one, and the loads write into it, which makes 2300 to 2560 of
+// its 128-byte cycles.  Without the loads, the exponentials or both it takes as
+// long; with the scores of 128 keys made at once the queries are read once, but
+// the threads wait for them (66 us).  Of the rest 3 us pass until the first
+// scores and 3 us in writing the sums.
 #include <algorithm>
 
 #include "paged.h"
@@ -283,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = (warp - 4) >> 2, w = warp & 3, row = w * 32 + lane;
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
         if (two || s == 0) {
-            // the warp's 32 query rows into the swizzled tile, whole rows at a time (a short loop: code that runs once is
-            // fetched from far away, and the unrolled form took 5000 cycles)
+            // the warp's 32 query rows into the swizzled tile, whole rows at a time (they are there 4000 cycles after the
+            // start, whether asked for by this loop, an unrolled one, through registers or before the first barrier)
             constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows a step
             const int c = lane % LPR;
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.q) + (size_t)h * G * D + c * 8;
@@ -406,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ results
         // Both streams are through, so nothing reads the ring or is in flight to it: rows are put together there and leave
         // as one bulk copy each.  One query tile: stream 1 leaves its part of the rows first, stream 0 adds its own.
-        // (Little code: at the end of a kernel every line of it is fetched anew, about 230 cycles for 8 instructions.)
+        // (The 128 KB of two query tiles leave an SM in about 4000 cycles, as whole-row stores of a warp too; half the
+        // channels at a time through the query tiles it was 7000.)
         float2* other = reinterpret_cast<float2*>(S.q[1]);       // both streams' (m, l); one query tile leaves the second's place
         if (!two) other[s * kT + row] = make_float2(m, l);
         asm volatile("bar.sync 1, 256;" ::: "memory");
