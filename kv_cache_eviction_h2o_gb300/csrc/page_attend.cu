@@ -646,6 +646,15 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             const int chunk = ((ncand + C - 1) / C + 3) & ~3, jend = min(ncand, (rank + 1) * chunk);
             const int step = kWarps * 4 * kScan;
             int j0 = rank * chunk + warp * 4 * kScan;
+            // (an arrival waits for all copies under way, 4000 cycles, so it comes before them)
+            if (tid == 0) S.pick.amax = 0u;
+            cluster_arrive();
+            // the queries first, into a stage that the bounds reach later: behind what bounds all CTAs ask for they came 4000
+            // cycles after these
+            static_assert(kMaxPageGroups * D * (int)sizeof(T) <= 2 * TB, "a stage of the ring holds the queries");
+            unsigned char* qs = raw + (NS - 1) * 2 * TB;
+            for (int i = tid; i < G * (D / N); i += kNT) cp_async16(smem_u32(qs + i * 16), qrow + i * N, true);
+            cp_commit();
             // each page's id waits in the place of its score
             for (int j = rank * chunk + tid; j < jend; j += kNT) scores[j] = __int_as_float(table[j]);
             __syncthreads();
@@ -664,19 +673,19 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             };
 #pragma unroll 1
             for (int k = 0; k < NS - 1; ++k) scan(j0 + k * step, k);
-            if (tid == 0) S.pick.amax = 0u;
+            cp_wait<NS - 1>();
+            __syncthreads();
             // (fp32 pairs hold the sums as well as fp64 would, whose pipe is so narrow that its conversions took 3 us here)
             for (int i = tid; i < 2 * D; i += kNT) {
                 float2 s = make_float2(0.f, 0.f);
                 const bool lo = i < D;
                 for (int g = 0; g < G; ++g) {
-                    const float x = Elem<T>::to_f(qrow[g * D + (lo ? i : i - D)]);
+                    const float x = Elem<T>::to_f(reinterpret_cast<const T*>(qs)[g * D + (lo ? i : i - D)]);
                     s = pair_add(s, lo ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x));
                 }
                 S.w[i] = s;
             }
             __syncthreads();
-            cluster_arrive();
             float w[NV][N];
 #pragma unroll
             for (int i = 0; i < NV; ++i)
