@@ -413,7 +413,7 @@ struct CoreSimt {
 // 48 products of 16 x 8 x 16 a tile, a small part of the time its 4 KB of
 // keys and 4 KB of values (head_dim 128) take to arrive; tcgen05's 128 rows
 // would be seven eighths padding here.  There is time for P in two bf16 parts
-// (2^-17 relative a weight, far below the output's own rounding).  The maximum
+// (2^-16 relative a weight, far below the output's own rounding).  The maximum
 // is raised only when a logit passes it by 2^8.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
 {

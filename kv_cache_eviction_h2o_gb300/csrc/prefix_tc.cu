@@ -22,8 +22,8 @@
 // their stream's products, warps 4..7 and 8..11 are the streams' threads.  A
 // row's maximum m is raised, and O scaled, only when a logit passes it by more
 // than 2^8: the weights are relative to m in any case, and l stays in fp32.  P
-// is rounded to bf16 for the product (2^-9 relative a weight, as the output is;
-// a second product of what that leaves took 13 us of 55 more), the sums l are
+// is rounded to bf16 for the product (2^-8 relative a weight, as the output is;
+// a second product of what that leaves took 13 us more), the sums l are
 // of the unrounded weights.  Waits are bounded; one that runs out leaves NaN
 // sums.
 //
@@ -490,7 +490,7 @@ cudaError_t go(const PagePool& p, const PageRows& r, const int* table, int prefi
 }  // namespace
 
 // Keys of each CTA's range, a multiple of 128: the number of ranges for the
-// shortest time.  In key tiles (1.6 us), a CTA costs those of its range and
+// shortest time.  In key tiles (1.5 us), a CTA costs those of its range and
 // about two for its start, its query tiles and its sums; the rows' own pass
 // about three when it finds no SMs left beside this one (8 requests of 8 heads
 // behind 2048 tokens: 16.0 us with 16 ranges, 13.2 with 8); and joining the
