@@ -107,14 +107,14 @@ __device__ __forceinline__ void commit(uint32_t on, uint64_t* bar)
                  : "memory");
 }
 
-// a copy of `bytes` (a multiple of 16) out of shared memory by this thread, and the end of reading by all it started
+// a copy of `bytes` (a multiple of 16) out of shared memory by this thread, and the end of all it started
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
 {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_store_wait()
 {
-    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // descriptor of the value tile as the K x N operand, N (channels) contiguous:
