@@ -346,6 +346,20 @@ def test_prefix_many_rows(dtype, rows, heads, groups, d, plen):
     _check(_prefix(c, q.cuda(), seq, pos, c.table[9], plen, d ** -0.5), want, "rows %d" % rows)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [3, 130])                  # one and two tiles of 128 query rows
+def test_prefix_many_tiles_a_block(rows, d):
+    # as many cache heads as fill the GPU with few ranges each, so that a block sweeps many key tiles
+    heads, ps, plen, scale = 40, 32, 5077, d ** -0.5
+    c = Cache([1, plen], heads, d, ps, BF16, seed=d + rows)
+    q = _queries(rows, heads, d, BF16, 11)
+    out = _prefix(c, q.cuda(), [0] * rows, [-1] * rows, c.table[1], plen, scale)
+    for h in range(heads):
+        k, v = c.rows(c.table[1], h, plen)
+        a = _attention(q[:, h].double().cuda(), k.cuda(), v.cuda(), scale)
+        _check(out[:, h], (a[0].cpu(), _tolerance(BF16, d, plen, *a).cpu()), "head %d" % h)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_prefix_large_and_infinite_logits(dtype):
     c = Cache([60, 700], 1, 128, 64, dtype, seed=3, kscale=20.0)
