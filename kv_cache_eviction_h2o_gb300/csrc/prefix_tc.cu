@@ -65,8 +65,9 @@ template <int D>
 struct alignas(1024) Smem {
     uint8_t q[2][Cfg<D>::kTile];
     uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
-    uint64_t full[Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
+    uint64_t full[2][Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
     uint64_t q_ready, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2], last;   // [stream][part of the tile]
+    uint64_t v_last[2];                // the stream's last value tile is there
     uint32_t tmem;
     int abort, bad;
 };
@@ -126,7 +127,12 @@ __device__ __forceinline__ uint64_t value_desc(const void* p)
 }
 
 // The ring's order of use: K(0) .. K(L - 1), then V(t), K(t + L) for t = 0, 1, ..
-// (L = 1: both streams read each tile; 2: the streams take turns); V(t)'s place:
+// (L = 1: both streams read each tile; 2: the streams take turns).  A wait
+// tells a barrier's phase from its neighbour only, so each barrier's waiters
+// see all its phases: where the streams take turns each has full barriers of
+// its own (with one set a stream could take the landing of the other's tile,
+// two turns of the slot before, for that of its own), and counts their phases
+// by what it has waited for.  V(t)'s place:
 __device__ __forceinline__ int v_at(int t, int n, int L) { return t + min(n, t + L); }
 
 template <int D>
@@ -160,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_launch_dependents();                        // the rows' own pass may start on what SMs are left; it waits before it reads sums
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&S.full[s], 1);
+            mbar_init(&S.full[0][s], 1);
+            mbar_init(&S.full[1][s], 1);
             mbar_init(&S.empty[s], two ? 2 : 1);
         }
         mbar_init(&S.q_ready, two ? 8 : 4);
@@ -170,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&S.p_ready[s][b], 4);
             }
             mbar_init(&S.pv_done[s], 1);
+            mbar_init(&S.v_last[s], 1);
         }
         mbar_init(&S.last, 2);
         S.abort = S.bad = 0;
@@ -191,19 +199,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ps = pool.ps;
         const uint32_t page_bytes = (uint32_t)ps * 128u;   // of one box
         int at = 0;
+        uint32_t turns = 0u, owner = 0u;             // by slot: loads on each set of full barriers (mod 2), set of the last
         bool ok = true;
         auto load = [&](const CUtensorMap* map, int t) {
             if (!ok) return;
-            const int s = at % NS, pages = (valid_of(t) + ps - 1) / ps, i = lane / C::kBoxes, b = lane % C::kBoxes;
+            const int s = at % NS, f = two ? 0 : t & 1, pages = (valid_of(t) + ps - 1) / ps, i = lane / C::kBoxes, b = lane % C::kBoxes;
             const bool mine = i < pages;             // this lane's box
             int pg = mine ? table[(j0 + t * kT) / ps + i] : 0;
             if ((unsigned)pg >= (unsigned)pool.pages) { pg = 0; *(volatile int*)&S.bad = 1; }
             if (at >= NS) ok = __all_sync(0xffffffffu, wait(S, &S.empty[s], at / NS - 1));
             if (!ok) return;
-            if (lane == 0) mbar_arrive_expect_tx(&S.full[s], (uint32_t)pages * page_bytes * C::kBoxes);
+            if (lane == 0) mbar_arrive_expect_tx(&S.full[f][s], (uint32_t)pages * page_bytes * C::kBoxes);
             __syncwarp();
-            if (mine) tma_load_2d(S.ring[s] + b * kBox + i * page_bytes, map, b * 64, (pg * pool.heads + h) * ps, &S.full[s]);
+            if (mine) tma_load_2d(S.ring[s] + b * kBox + i * page_bytes, map, b * 64, (pg * pool.heads + h) * ps, &S.full[f][s]);
             __syncwarp();
+            turns ^= 1u << (16 * f + s);
+            owner = (owner & ~(1u << s)) | (uint32_t)f << s;
             ++at;
         };
         for (int t = 0; t < min(L, n); ++t) load(&mapK, t);
@@ -212,7 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t + L < n) load(&mapK, t + L);
         }
         // every load has landed before the shared memory is given up, those of an abandoned sweep too
-        for (int i = max(0, at - NS); i < at; ++i) mbar_wait(&S.full[i % NS], (uint32_t)(i / NS) & 1u);
+        for (int s = 0; s < min(NS, at); ++s) {
+            const uint32_t f = owner >> s & 1u;
+            mbar_wait(&S.full[f][s], (turns >> (16 * f + s) & 1u) ^ 1u);
+        }
     } else if (warp <= 2) {
         // ------------------------------------------------ products of stream s
         const int s = warp - 1;
@@ -220,8 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q0 = sw128_desc(S.q[two ? s : 0]), k0 = sw128_desc(S.ring[0]), v0 = value_desc(S.ring[0]);
         const uint32_t sS = tS(s), sO = tO(s);
         bool ok = __all_sync(0xffffffffu, wait(S, &S.q_ready, 0));
+        uint64_t* const full = S.full[two ? 0 : s];
+        uint32_t seen = 0u;                          // by slot: this stream's waits on it (mod 2)
         auto slot_full = [&](int i) {
-            if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.full[i % NS], i / NS));
+            if (ok) ok = __all_sync(0xffffffffu, wait(S, full + i % NS, (int)(seen >> i % NS & 1u)));
+            seen ^= 1u << i % NS;
         };
         // scores of step b of the tile in place i
         auto score = [&](int b, int i) {
@@ -268,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = t + stride < n;
             slot_full(v);                            // (both before the weights: between them and the products every look at a
             if (more) slot_full(k);                  // barrier is waited for, and with four of them the loop took a tenth longer)
+            else if (ok && on) mbar_arrive(&S.v_last[s]);
             for (int b = 0; b < kSteps; ++b) {
                 values(b, nth, v, valid_of(t));
                 if (b == kSteps - 1) release(v);
@@ -388,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the value rows behind the range's last key in its group of 16: their weights are 0, but what lies there may be
                 // NaN (two query tiles: both streams write the zeros, each before its own product)
                 const int v = v_at(t, n, L), end = (valid + 15) & ~15;
-                ok = __all_sync(0xffffffffu, wait(S, &S.full[v % NS], v / NS));
+                ok = __all_sync(0xffffffffu, wait(S, &S.v_last[s], 0));
                 if (!ok) break;
                 for (int x = row; x < (end - valid) * C::kBoxes * 8; x += kT)
                     *reinterpret_cast<uint4*>(S.ring[v % NS] + (x >> 3) % C::kBoxes * kBox + (kStep * b + valid + (x >> 3) / C::kBoxes) * 128 +

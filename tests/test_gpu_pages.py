@@ -707,3 +707,31 @@ def test_injected_launch_failure(monkeypatch):
         _prefix(c, q, [0], [19], [], 0, 0.1)
     monkeypatch.delenv("H2O_FAULT")
     assert _sparse(c, q, [0], [19], 2, 1, 0.1)[0].isfinite().all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_tiles_that_arrive_out_of_order(d):
+    # one tile of query rows over key tiles by turns on the same few pages, which the L2 cache holds, and on pages far
+    # apart, which it does not: a tile may be there before the one that was asked for earlier
+    heads, ps, pages, tiles, rows, scale = 40, 32, 6000, 40, 3, d ** -0.5
+    plen = tiles * 128 - 43
+    g = torch.Generator(device="cuda").manual_seed(d)
+    K, V = (torch.randn(pages, heads, ps, d, dtype=BF16, device="cuda", generator=g) for _ in range(2))
+    far = torch.randperm(pages - 4, device="cuda", generator=g)[:tiles // 2 * 4].view(-1, 4) + 4
+    ptable = torch.stack([torch.arange(4, device="cuda").expand_as(far), far], 1).reshape(-1).to(torch.int32)
+    q = torch.randn(rows, heads, d, dtype=BF16, device="cuda", generator=g)
+    seq, pos, table = _i32([0] * rows), _i32([-1] * rows), _i32([[0]])
+    work = torch.empty(L.h2o_prefix_work_bytes(rows, heads, 1, d, plen, L.H2O_BF16), dtype=torch.uint8, device="cuda")
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(20):
+        out = torch.zeros_like(q)
+        flush.zero_()
+        L.h2o_prefix_attend(q, seq, pos, K, V, ptable, plen, table, scale, out, work, torch.cuda.current_stream())
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    at = ptable.long()
+    for h in range(heads):
+        k, v = (x[at, h].reshape(-1, d)[:plen].double() for x in (K, V))
+        a = _attention(q[:, h].double(), k, v, scale)
+        _check(out[:, h], (a[0].cpu(), _tolerance(BF16, d, plen, *a).cpu()), "head %d" % h)
