@@ -66,7 +66,7 @@ struct alignas(1024) Smem {
     uint8_t q[2][Cfg<D>::kTile];
     uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
     uint64_t full[2][Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
-    uint64_t q_ready, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2], last;   // [stream][part of the tile]
+    uint64_t q_ready, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2][kSteps], last;   // [stream][part of the tile]
     uint64_t v_last[2];                // the stream's last value tile is there
     uint32_t tmem;
     int abort, bad;
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < kSteps; ++b) {
                 mbar_init(&S.s_ready[s][b], 1);
                 mbar_init(&S.p_ready[s][b], 4);
+                mbar_init(&S.pv_done[s][b], 1);
             }
-            mbar_init(&S.pv_done[s], 1);
             mbar_init(&S.v_last[s], 1);
         }
         mbar_init(&S.last, 2);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 for (int x = 0; x < nk; ++x) one(x);
             }
-            commit(on, &S.pv_done[s]);
+            commit(on, &S.pv_done[s][b]);
         };
         auto release = [&](int i) {                  // (two query tiles: when both streams have)
             if (ok) commit(on, &S.empty[i % NS]);
@@ -332,7 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < steps; ++i) {
             const int nth = i / kSteps, b = i % kSteps, t = two ? nth : 2 * nth + s, valid = valid_of(t) - kStep * b;
             const uint32_t at = tS(s) + lanes + (uint32_t)(kStep * b);
-            ok = __all_sync(0xffffffffu, wait(S, &S.s_ready[s][b], nth));
+            // (a part's last product is done before its new scores are made, so the second look never waits; it is there to
+            // see every phase: one that was not looked for in time cannot be told from the next but one)
+            ok = __all_sync(0xffffffffu, wait(S, &S.s_ready[s][b], nth) && (nth == 0 || wait(S, &S.pv_done[s][b], nth - 1)));
             if (!ok) break;
             tc_fence_after();
             constexpr int NC = kStep / 32;
@@ -371,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= a;
                 }
                 if (i > 0) {
-                    // (these scores came after all products but, with two parts, the last)
-                    ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s], i - 1));
+                    // (all products but, with two parts, the last are done)
+                    ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][(i - 1) % kSteps], (i - 1) / kSteps));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -418,9 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.p_ready[s][b]);
         }
-        // (the last product but one first: a phase is told from its neighbour only)
-        if (ok && steps > 1) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s], steps - 2));
-        if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s], steps - 1));
+        for (int b = 0; b < kSteps; ++b)
+            if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][b], steps / kSteps - 1));
         tc_fence_after();
 
         // ------------------------------------------------ results

@@ -735,3 +735,30 @@ def test_prefix_tiles_that_arrive_out_of_order(d):
         k, v = (x[at, h].reshape(-1, d)[:plen].double() for x in (K, V))
         a = _attention(q[:, h].double(), k, v, scale)
         _check(out[:, h], (a[0].cpu(), _tolerance(BF16, d, plen, *a).cpu()), "head %d" % h)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [3, 130])                  # one and two tiles of 128 query rows
+def test_prefix_maximum_raised_by_every_part_of_a_tile(rows, d):
+    # logits grow by 2^9 every 64 keys, and values shrink by as much, so that each of the last 13 parts has an equal share
+    heads, ps, parts, scale = 40, 32, 79, 0.125
+    plen = parts * 64 - 21
+    g = torch.Generator().manual_seed(d + rows)
+    c = Cache([1, plen], heads, d, ps, BF16, seed=d)
+    part = torch.arange(plen) // 64
+    k, v = (0.3 * torch.randn(plen, heads, d, generator=g) for _ in range(2))
+    k[..., 0] = 8.0 * part[:, None]
+    v = v * torch.exp2(9.0 * (parts - 1 - part).clamp(max=12))[:, None, None]
+    q = 0.3 * torch.randn(rows, heads, d, generator=g)
+    q[..., 0] = 6.25                                         # 6.25 * 8 * scale * log2(e) = 9.02
+    slot = _i32([int(c.table[1, t // ps]) * ps + t % ps for t in range(plen)])
+    K, V = c.K.cuda(), c.V.cuda()
+    L.h2o_page_write(k.to(BF16).cuda(), v.to(BF16).cuda(), slot, K, V, torch.empty(K.shape[0], heads, 2, d, dtype=BF16, device="cuda"),
+                     torch.cuda.current_stream())
+    c.K, c.V = K.cpu(), V.cpu()
+    q = q.to(BF16)
+    out = _prefix(c, q.cuda(), [0] * rows, [-1] * rows, c.table[1], plen, scale)
+    for h in range(heads):
+        kk, vv = c.rows(c.table[1], h, plen)
+        a = _attention(q[:, h].double().cuda(), kk.cuda(), vv.cuda(), scale)
+        _check(out[:, h], (a[0].cpu(), _tolerance(BF16, d, plen, *a).cpu()), "head %d" % h)
