@@ -67,7 +67,7 @@ struct alignas(1024) Smem {
     uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
     uint64_t full[2][Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
     uint64_t q_ready, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2][kSteps], last;   // [stream][part of the tile]
-    uint64_t v_last[2];                // the stream's last value tile is there
+    uint64_t landed;                   // all loads are there
     uint32_t tmem;
     int abort, bad;
 };
@@ -177,9 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&S.p_ready[s][b], 4);
                 mbar_init(&S.pv_done[s][b], 1);
             }
-            mbar_init(&S.v_last[s], 1);
         }
         mbar_init(&S.last, 2);
+        mbar_init(&S.landed, 1);
         S.abort = S.bad = 0;
         fence_mbar_init();
     }
@@ -227,6 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t f = owner >> s & 1u;
             mbar_wait(&S.full[f][s], (turns >> (16 * f + s) & 1u) ^ 1u);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.landed);
     } else if (warp <= 2) {
         // ------------------------------------------------ products of stream s
         const int s = warp - 1;
@@ -285,7 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = t + stride < n;
             slot_full(v);                            // (both before the weights: between them and the products every look at a
             if (more) slot_full(k);                  // barrier is waited for, and with four of them the loop took a tenth longer)
-            else if (ok && on) mbar_arrive(&S.v_last[s]);
             for (int b = 0; b < kSteps; ++b) {
                 values(b, nth, v, valid_of(t));
                 if (b == kSteps - 1) release(v);
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the value rows behind the range's last key in its group of 16: their weights are 0, but what lies there may be
                 // NaN (two query tiles: both streams write the zeros, each before its own product)
                 const int v = v_at(t, n, L), end = (valid + 15) & ~15;
-                ok = __all_sync(0xffffffffu, wait(S, &S.v_last[s], 0));
+                ok = __all_sync(0xffffffffu, wait(S, &S.landed, 0));
                 if (!ok) break;
                 for (int x = row; x < (end - valid) * C::kBoxes * 8; x += kT)
                     *reinterpret_cast<uint4*>(S.ring[v % NS] + (x >> 3) % C::kBoxes * kBox + (kStep * b + valid + (x >> 3) / C::kBoxes) * 128 +
