@@ -348,11 +348,9 @@ cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t st)
     const int threads = work <= 256 ? 256 : 1024;
     const int grid = (int)std::min<long long>(152, std::max<long long>(1, (work + threads - 1) / threads));
     const size_t smem = 3 * sizeof(int) * (((size_t)a.n + 4) & ~(size_t)3);
-    if (smem > 48 * 1024) {
-        static SmemOnce once;
-        const cudaError_t e = once.allow(page_tables_kernel);
-        if (e != cudaSuccess) return e;
-    }
+    static SmemOnce once;                                  // (the kernel's own arrays count towards the 48 KB too)
+    const cudaError_t e = once.allow(page_tables_kernel);
+    if (e != cudaSuccess) return e;
     page_tables_kernel<<<grid, threads, smem, st>>>(a);
     return cudaGetLastError();
 }

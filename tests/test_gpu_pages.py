@@ -762,3 +762,24 @@ def test_prefix_maximum_raised_by_every_part_of_a_tile(rows, d):
         kk, vv = c.rows(c.table[1], h, plen)
         a = _attention(q[:, h].double().cuda(), kk.cuda(), vv.cuda(), scale)
         _check(out[:, h], (a[0].cpu(), _tolerance(BF16, d, plen, *a).cpu()), "head %d" % h)
+
+
+def test_tables_of_any_size_in_a_fresh_process():
+    # what a kernel may use of shared memory is set once a process: sizes about 48 KB, none larger before them
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from kv_cache_eviction_h2o_gb300 import binding as L
+for n in (4035, 4039, 4040, 4092, 4095):
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    seq, pos, slot, status = i32(n), i32(n), i32(n), i32(4)
+    L.h2o_page_tables(i32(n) + 7, i32(n) + 1, i32(0), 16, torch.arange(n, dtype=torch.int32, device="cuda")[:, None], i32(n),
+                      i32(n + 1), seq, pos, slot, status, torch.cuda.current_stream())
+    assert status.tolist() == [n, 0, 8, 0]
+    assert (slot == 16 * torch.arange(n, device="cuda") + 7).all() and (pos == 7).all()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
