@@ -480,7 +480,7 @@ int h2o_page_tables(const int* len_before, const int* n_new, int requests, const
  * the page's bounds, made from all its keys (a NaN key gives NaN): those of
  * this call and those the page held before it.  Rows of this call that go to
  * one page are adjacent and in the order of their slots, as h2o_page_tables
- * lists them, and no slot comes twice.
+ * lists them (slots may be left out), and no slot comes twice.
  */
 int h2o_page_write(const void* k, const void* v, long long k_stride, long long v_stride, const int* slot, int rows,
                    void* K, void* V, void* bounds, int num_pages, int kv_heads, int page_size, int head_dim, int dtype,

@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const TablesArgs a)
 // made when a page fills, from all its keys, and not kept up to date row by
 // row: a page that is not full is never ranked, and a page that was rolled
 // back and filled again gets bounds of what it holds.  Keys of rows in this
-// call are read from k (the rows before this one, when their slots run up to
-// it), older ones from the page.  Bound: HBM.
+// call are read from k (rows just before this one, which go to the page too),
+// older ones from the page.  Bound: HBM.
 
 template <typename T> struct Vec16;
 template <> struct Vec16<float> {
@@ -310,18 +310,31 @@ __global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const PagePoo
     for (int r = 0; r < nr; ++r) {
         const int end = near[up + r];
         if (end < 0 || (end & up) != up) continue;        // (the same for the whole CTA)
+        // The key at offset o is that of a row of this call, or one of before.  The row lies up - o before this one, or nearer
+        // where the call leaves slots of the page out.
+        bool gaps = false;
+        for (int i = threadIdx.x & 31; i < up; i += 32) gaps |= (near[r + i] >> sh) == (end >> sh) && near[r + i] - i != end - up;
+        gaps = __any_sync(0xffffffffu, gaps);
         Vec16<T> lo, hi;
         if (in) {
             const T* page = K + place(end) - (size_t)up * D;
             lo.load(kc + (r0 + r) * k_stride);
             hi = lo;
-#pragma unroll 8
-            for (int o = y; o < up; o += ty) {
-                // the key at offset o: a row of this call, or one of before
+            auto take = [&](int o, int i) {
                 Vec16<T> w;
-                w.load(near[r + o] == end - up + o ? kc + (r0 + r - up + o) * k_stride : page + o * D);
+                w.load(near[i] == end - up + o ? kc + (r0 - up + i) * k_stride : page + o * D);
                 lo.low(w);
                 hi.high(w);
+            };
+            if (gaps) {
+                for (int o = y; o < up; o += ty) {
+                    int i = r + o;
+                    while (i < r + up && near[i] != end - up + o) ++i;
+                    take(o, i);
+                }
+            } else {
+#pragma unroll 8
+                for (int o = y; o < up; o += ty) take(o, r + o);
             }
             part[0][threadIdx.x] = lo;
             part[1][threadIdx.x] = hi;

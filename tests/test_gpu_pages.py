@@ -783,3 +783,30 @@ for n in (4035, 4039, 4040, 4092, 4095):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("heads,d,ps,pages", [(1, 64, 16, 1), (3, 128, 16, 40), (8, 128, 64, 60), (2, 64, 128, 30), (5, 128, 32, 9)])
+def test_write_leaves_slots_out(dtype, heads, d, ps, pages):
+    # rows of a page in the order of their slots, some of which keep what they held
+    g = np.random.default_rng(ps + pages)
+    c = Cache([ps * pages], heads, d, ps, dtype, seed=d)
+    bounds = torch.full((pages + 3, heads, 2, d), 5.0).to(dtype)
+    K, V, B = c.K.clone(), c.V.clone(), bounds.clone()
+    slots = []
+    for i, p in enumerate(c.table[0]):
+        n = int(g.integers(1, ps + 1))
+        at = [12, 14, 15] if i == 0 and ps == 16 else sorted(g.choice(ps, n, replace=False))
+        if i % 4 != 3 and at[-1] != ps - 1:
+            at[-1] = ps - 1
+        slots += [int(p) * ps + int(x) for x in at]
+    k, v = (torch.randn(len(slots), heads, d, generator=torch.Generator().manual_seed(i)).to(dtype) * 3 for i in (1, 2))
+    for r, s in enumerate(slots):
+        K[s // ps, :, s % ps], V[s // ps, :, s % ps] = k[r], v[r]
+    for s in slots:
+        if s % ps == ps - 1:
+            B[s // ps] = torch.stack([K[s // ps].amin(1), K[s // ps].amax(1)], 1)
+    gk, gv, gb = c.K.cuda(), c.V.cuda(), bounds.cuda()
+    L.h2o_page_write(k.cuda(), v.cuda(), _i32(slots), gk, gv, gb, torch.cuda.current_stream())
+    for got, want in ((gk, K), (gv, V), (gb, B)):
+        torch.testing.assert_close(got.cpu(), want, rtol=0, atol=0, equal_nan=True)
