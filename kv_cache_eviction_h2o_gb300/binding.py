@@ -16,7 +16,7 @@ pointer is passed through unchecked.
 
 The paged-cache calls (``h2o_page_*``, ``h2o_prefix_*``) have no handle: they
 take torch tensors only, read every size from the tensors' shapes and check
-them against one another.
+them against one another; without a `stream` they run on torch's current one.
 """
 import ctypes
 import os
@@ -378,14 +378,15 @@ def h2o_prompt_scores_noalloc(Q, K, batch, heads, T, head_dim, dtype, scale, c, 
 # the cheapest comparisons there are; what is wrong is found out afterwards.
 
 _CODES = {"torch.bfloat16": H2O_BF16, "torch.float32": H2O_F32}
-_types = None          # (int32, uint8, {element type: its code}, the current device's index)
+_types = None          # (int32, uint8, {element type: its code}, the current device's index, its current stream)
 
 
 def _torch_types():
     global _types
     if _types is None:
         import torch
-        _types = (torch.int32, torch.uint8, {getattr(torch, k[6:]): v for k, v in _CODES.items()}, torch.cuda.current_device)
+        _types = (torch.int32, torch.uint8, {getattr(torch, k[6:]): v for k, v in _CODES.items()}, torch.cuda.current_device,
+                  torch.cuda.current_stream)
     return _types
 
 
@@ -462,6 +463,11 @@ def _on_current(x, current):
     return device
 
 
+def _on_stream(stream):
+    """The stream's handle; None: torch's current one, as for any other work on tensors."""
+    return _stream(_types[4]() if stream is None else stream)
+
+
 def _pool(K, V):
     """(device, element type, its code, K's and V's pointers, K's shape) of a page pool."""
     types = _torch_types()
@@ -482,7 +488,8 @@ def h2o_page_tables(len_before, n_new, free_pages, page_size, table, len_after, 
     len_before, n_new, len_after [requests], free_pages [any], table
     [requests][width], row_start [requests + 1], row_seq, row_pos, slot
     [rows_cap], status [4]."""
-    i32, _, _, current = _torch_types()
+    types = _torch_types()
+    i32, current = types[0], types[3]
     n, width = _dim(table, "table", 2)
     dev = _on_current(table, current)
     free, cap = _count(free_pages, "free_pages"), _count(slot, "slot")
@@ -491,7 +498,7 @@ def h2o_page_tables(len_before, n_new, free_pages, page_size, table, len_after, 
         _array(free_pages, "free_pages", i32, free, dev), free, page_size, _array(table, "table", i32, n * width, dev), width,
         _array(len_after, "len_after", i32, n, dev), _array(row_start, "row_start", i32, n + 1, dev),
         _array(row_seq, "row_seq", i32, cap, dev), _array(row_pos, "row_pos", i32, cap, dev), _array(slot, "slot", i32, cap, dev),
-        cap, _array(status, "status", i32, 4, dev), _stream(stream))
+        cap, _array(status, "status", i32, 4, dev), _on_stream(stream))
     if rc:
         _check(rc)
 
@@ -505,7 +512,7 @@ def h2o_page_write(k, v, slot, K, V, bounds, stream=None):
     vp, vs = _head_rows(v, "v", dt, shape, dev)
     rc = lib().h2o_page_write(kp, vp, ks, vs, _array(slot, "slot", _types[0], rows, dev), rows, Kp, Vp,
                               _tensor(bounds, "bounds", dt, (pages, heads, 2, d), dev), pages, heads, ps, d, code,
-                              _stream(stream))
+                              _on_stream(stream))
     if rc:
         _check(rc)
 
@@ -531,7 +538,7 @@ def h2o_page_attend(q, row_seq, row_pos, K, V, bounds, table, budget, recent, sc
     bp = None if bounds is None else _tensor(bounds, "bounds", dt, (pages, heads, 2, d), dev)
     kp = None if picked is None else _tensor(picked, "picked", _types[0], (rows, heads, budget), dev)
     rc = lib().h2o_page_attend(qp, qs, sp, pp, rows, Kp, Vp, bp, pages, heads, groups, ps, d, code, tp, n, width, budget,
-                               recent, scale, op, os_, kp, _stream(stream))
+                               recent, scale, op, os_, kp, _on_stream(stream))
     if rc:
         _check(rc)
 
@@ -556,6 +563,6 @@ def h2o_prefix_attend(q, row_seq, row_pos, K, V, prefix_table, prefix_len, table
             raise ValueError("prefix_table lists %d pages of %d tokens, prefix_len is %d" % (listed, ps, prefix_len))
     size = _count(work, "work")
     rc = lib().h2o_prefix_attend(qp, qs, sp, pp, rows, Kp, Vp, pages, heads, groups, ps, d, code, xp, prefix_len, tp, n,
-                                 width, scale, op, os_, _array(work, "work", _types[1], size, dev), size, _stream(stream))
+                                 width, scale, op, os_, _array(work, "work", _types[1], size, dev), size, _on_stream(stream))
     if rc:
         _check(rc)

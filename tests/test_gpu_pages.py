@@ -810,3 +810,28 @@ def test_write_leaves_slots_out(dtype, heads, d, ps, pages):
     L.h2o_page_write(k.cuda(), v.cuda(), _i32(slots), gk, gv, gb, torch.cuda.current_stream())
     for got, want in ((gk, K), (gv, V), (gb, B)):
         torch.testing.assert_close(got.cpu(), want, rtol=0, atol=0, equal_nan=True)
+
+
+def test_calls_without_a_stream_are_captured():
+    # on the current stream, which a capture wants them on
+    c = Cache([100, 60], 2, 64, 16, BF16, seed=4, extra=4)
+    K, V, B, table = c.K.cuda(), c.V.cuda(), c.bounds().cuda(), _i32(np.pad(c.table, ((0, 0), (0, 1)), constant_values=-1))
+    before, new, free = _i32([99, 59]), _i32([1, 1]), _i32(c.spare)
+    after, start, seq, pos, slot, status = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in (2, 3, 2, 2, 2, 4))
+    k, v, q = (_queries(2, h, 64, BF16, i).cuda() for i, h in enumerate((2, 2, 8)))
+    sparse, full = torch.zeros_like(q), torch.zeros_like(q)
+    work = torch.empty(L.h2o_prefix_work_bytes(2, 2, 4, 64, 40, L.H2O_BF16), dtype=torch.uint8, device="cuda")
+    ptable = table[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.h2o_page_tables(before, new, free, 16, table, after, start, seq, pos, slot, status)
+        L.h2o_page_write(k, v, slot, K, V, B)
+        L.h2o_page_attend(q, seq, pos, K, V, B, table, 4, 2, 0.125, sparse)
+        L.h2o_prefix_attend(q, seq, pos, K, V, ptable, 40, table, 0.125, full, work)
+    graph.replay()
+    torch.cuda.synchronize()
+    c.K, c.V, c.table = K.cpu(), V.cpu(), table.cpu().numpy()
+    assert status.tolist() == [2, 0, 100, 0]
+    _check(sparse, _sparse_ref(c, q.cpu(), [0, 1], [99, 59], 4, 2, 0.125)[0], "sparse")
+    _check(full, _prefix_ref(c, q.cpu(), [0, 1], [99, 59], c.table[0], 40, 0.125), "prefix")

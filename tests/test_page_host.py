@@ -148,3 +148,54 @@ def test_binding_wants_gpu_tensors_of_fitting_shapes(L):
         L._head_rows(wide[:, ::3], "k", torch.float32, (5, 8, 64), cpu)
     with pytest.raises(ValueError, match="contiguous heads"):
         L._head_rows(wide[..., ::2], "k", torch.float32, (5, 24, 32), cpu)
+
+
+class _Gpu:
+    """What the binding asks of a tensor, as one on cuda:0 would answer; a CPU tensor gives the shapes."""
+
+    def __init__(self, x):
+        self.x, self.dtype, self.shape, self.device = x, x.dtype, x.shape, "cuda:0"
+
+    def __getattr__(self, name):
+        return getattr(self.x, name)
+
+    def get_device(self):
+        return 0
+
+
+class _Lib:
+    """Records the last argument, the stream, of each call."""
+
+    def __init__(self):
+        self.streams = {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.streams[name] = args[-1]
+            return 0
+        return call
+
+
+def _all_calls(L, **stream):
+    i32 = lambda *n: _Gpu(torch.zeros(*n, dtype=torch.int32))   # noqa: E731
+    f = lambda *n: _Gpu(torch.zeros(*n))                        # noqa: E731
+    K, V, B, q, out = f(4, 2, 16, 64), f(4, 2, 16, 64), f(4, 2, 2, 64), f(3, 4, 64), f(3, 4, 64)
+    L.h2o_page_tables(i32(2), i32(2), i32(5), 16, i32(2, 3), i32(2), i32(3), i32(3), i32(3), i32(3), i32(4), **stream)
+    L.h2o_page_write(f(3, 2, 64), f(3, 2, 64), i32(3), K, V, B, **stream)
+    L.h2o_page_attend(q, i32(3), i32(3), K, V, B, i32(2, 3), 2, 1, 0.1, out, **stream)
+    L.h2o_prefix_attend(q, i32(3), i32(3), K, V, i32(1), 16, i32(2, 3), 0.1, out, _Gpu(torch.zeros(64, dtype=torch.uint8)), **stream)
+
+
+def test_without_a_stream_calls_run_on_the_current_one(L, monkeypatch):
+    import types
+    lib = _Lib()
+    monkeypatch.setattr(L, "lib", lambda: lib)
+    monkeypatch.setattr(L, "_types", None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=77))
+    _all_calls(L)
+    assert len(lib.streams) == 4 and set(lib.streams.values()) == {77}
+    _all_calls(L, stream=types.SimpleNamespace(cuda_stream=5))
+    assert set(lib.streams.values()) == {5}
+    _all_calls(L, stream=6)
+    assert set(lib.streams.values()) == {6}
