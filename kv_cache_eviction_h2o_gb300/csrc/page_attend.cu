@@ -62,6 +62,27 @@ __device__ __forceinline__ uint32_t tile_at(int row, int byte)
 
 // -------------------------------------------------------------- picking
 
+// A sum of fp32 values of one sign as three fp32 parts: each addition's rounding
+// error goes to the next part, exactly (TwoSum), and the third's is below 2^-70
+// of the sum for 16 values, of which fp64 keeps 2^-53.
+struct Sum3 {
+    float hi = 0.f, mid = 0.f, lo = 0.f;
+    __device__ __forceinline__ static float2 two_sum(float a, float b)
+    {
+        const float s = a + b, bp = s - a;
+        return make_float2(s, (a - (s - bp)) + (b - bp));
+    }
+    __device__ __forceinline__ void add(float x)
+    {
+        const float2 h = two_sum(hi, x), m = two_sum(mid, h.y);
+        hi = h.x;
+        mid = m.x;
+        lo += m.y;
+    }
+    // the sum rounded to fp32, and what that leaves
+    __device__ __forceinline__ float2 rounded() const { return two_sum(hi, mid); }
+};
+
 // the largest |x| of 16-byte vectors, NaN where one is
 template <typename T> struct AbsMax;
 template <> struct AbsMax<__nv_bfloat16> {
@@ -584,7 +605,8 @@ template <int N> __device__ __forceinline__ void ld_cluster_f(uint32_t addr, flo
 
 template <int D, class Core>
 struct alignas(16) AttendSmem {
-    float2 w[2 * D];                   // the page weights, minima's then maxima's, as sums hi + lo
+    float2 w[2 * D];                   // the page weights, minima's then maxima's, as w.x + w.y + w_lo
+    float w_lo[2 * D];
     typename Core::Shared core;
     float2 wml[Core::kWarps][kMaxPageGroups];
     float2 ml[kMaxPageGroups];
@@ -675,15 +697,16 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             for (int k = 0; k < NS - 1; ++k) scan(j0 + k * step, k);
             cp_wait<NS - 1>();
             __syncthreads();
-            // (fp32 pairs hold the sums as well as fp64 would, whose pipe is so narrow that its conversions took 3 us here)
+            // (fp32 parts, since the fp64 pipe is so narrow that its conversions took 3 us here)
             for (int i = tid; i < 2 * D; i += kNT) {
-                float2 s = make_float2(0.f, 0.f);
+                Sum3 s;
                 const bool lo = i < D;
                 for (int g = 0; g < G; ++g) {
                     const float x = Elem<T>::to_f(reinterpret_cast<const T*>(qs)[g * D + (lo ? i : i - D)]);
-                    s = pair_add(s, lo ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x));
+                    s.add(lo ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x));
                 }
-                S.w[i] = s;
+                S.w[i] = s.rounded();
+                S.w_lo[i] = s.lo;
             }
             __syncthreads();
             float w[NV][N];
@@ -752,7 +775,7 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                 const T* b = bounds + ((size_t)p * pool.heads + h) * 2 * D;
                 double s = 0.0;
                 if (__uint_as_float(S.pick.amax) < FLT_MAX) {      // (finite factors; fp64 holds their sum)
-                    for (int e = lane; e < 2 * D; e += 32) s += ((double)S.w[e].x + (double)S.w[e].y) * (double)Elem<T>::to_f(b[e]);
+                    for (int e = lane; e < 2 * D; e += 32) s += ((double)S.w[e].x + ((double)S.w[e].y + (double)S.w_lo[e])) * (double)Elem<T>::to_f(b[e]);
                 } else {
                     // an infinite bound on the side that no query takes counts for nothing: the maxima themselves
                     for (int e = lane; e < D; e += 32)

@@ -835,3 +835,22 @@ def test_calls_without_a_stream_are_captured():
     assert status.tolist() == [2, 0, 100, 0]
     _check(sparse, _sparse_ref(c, q.cpu(), [0, 1], [99, 59], 4, 2, 0.125)[0], "sparse")
     _check(full, _prefix_ref(c, q.cpu(), [0, 1], [99, 59], c.table[0], 40, 0.125), "prefix")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,ps,low", [(64, 16, 2.0 ** -50), (128, 32, 2.0 ** -52), (128, 16, 2.0 ** -50)])
+def test_sparse_ranks_by_all_bits_of_fp64(dtype, d, ps, low):
+    # two pages whose scores are sums of four queries each and differ in one of fp64's last bits; the better one comes second
+    c = Cache([4 * ps], 1, d, ps, dtype, seed=2)
+    pages = torch.as_tensor(c.table[0]).long()
+    c.K[pages] = 0.0
+    c.K[pages[0], :, :, 7] = 1.0
+    c.K[pages[1], :, :, 9] = 1.0
+    q = torch.zeros(1, 4, d, dtype=dtype)
+    q[0, :, 7] = torch.tensor([1.0, 2.0 ** -25, 2.0 ** -48, 0.0])
+    q[0, :, 9] = torch.tensor([1.0, 2.0 ** -25, 2.0 ** -48, low])
+    want, picked = _sparse_ref(c, q, [0], [4 * ps - 1], 2, 1, 0.125)
+    assert picked[0, 0].tolist() == [1, 3]
+    out, got = _sparse(c, q.cuda(), [0], [4 * ps - 1], 2, 1, 0.125)
+    np.testing.assert_array_equal(got.cpu().numpy(), picked)
+    _check(out, want, "picked")
