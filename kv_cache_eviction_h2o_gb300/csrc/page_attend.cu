@@ -954,10 +954,10 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             }
             if (s0 + kAtOnce < ns) ask(s0 + kAtOnce);
         }
-        // no key at all: zero; a bad table entry has made l NaN
-        const float f = l == 0.f ? 0.f : 1.f / l;
+        // no key at all, or none of weight: zero, whatever the values are; a bad table entry has made l NaN
+        const float f = 1.f / l;
 #pragma unroll
-        for (int e = 0; e < V4; ++e) o[e] *= f;
+        for (int e = 0; e < V4; ++e) o[e] = l == 0.f ? 0.f : o[e] * f;
         store_out<V4>(orow + g * D + lane * V4, o);
     }
     cluster_arrive();

@@ -854,3 +854,15 @@ def test_sparse_ranks_by_all_bits_of_fp64(dtype, d, ps, low):
     out, got = _sparse(c, q.cuda(), [0], [4 * ps - 1], 2, 1, 0.125)
     np.testing.assert_array_equal(got.cpu().numpy(), picked)
     _check(out, want, "picked")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_rows_without_weight_are_zero_whatever_the_values(dtype, value):
+    c = Cache([60, 300], 2, 64, 16, dtype, seed=3)
+    c.K[:], c.V[:] = float("-inf"), value
+    q = _queries(3, 8, 64, dtype, 1).abs() + 0.5
+    out, _ = _sparse(c, q.cuda(), [0, 1, 1], [59, 299, 17], 3, 1, 0.125)
+    assert (out == 0).all()
+    assert (_prefix(c, q.cuda(), [0, 0, 0], [59, -1, 5], c.table[1], 290, 0.125) == 0).all()
+    assert (_prefix(c, q.cuda(), [0, 1, 1], [59, 299, 17], [], 0, 0.125) == 0).all()
