@@ -500,7 +500,8 @@ int h2o_page_write(const void* k, const void* v, long long k_stride, long long v
  * own are ranked.  out = softmax(scale q.K) V over the tokens of those pages.
  *   q, out [rows][kv_heads * groups][head_dim] of dtype (sums in fp32; bf16
  *   weights and outputs are rounded once), query head h * groups + g to cache
- *   head h; 1 <= groups <= 16.  out may be q itself.
+ *   head h; 1 <= groups <= 16.  out may be q itself, or other columns of the
+ *   rows that q is a slice of; any other overlap of the two is refused.
  *   bounds may be NULL when budget >= table_width; otherwise budget <= 4096.
  *   picked: int32 [rows][kv_heads][budget] or NULL, receives the pages read,
  *   as indexes into the request's table, ascending, -1 behind them.

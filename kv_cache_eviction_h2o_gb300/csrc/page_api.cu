@@ -55,6 +55,19 @@ int check_stride(long long stride, long long need, int dtype, const char* what)
     return H2O_OK;
 }
 
+// Whether rows of q are written by other rows' results: q and out share memory and are neither the same rows nor different
+// columns of the same rows (of a fused buffer).
+bool rows_collide(const PageRows& r, long long need, int dtype)
+{
+    const long long size = dtype == H2O_BF16 ? 2 : 4, qs = r.q_stride * size, os = r.out_stride * size, n = need * size;
+    const uintptr_t q = reinterpret_cast<uintptr_t>(r.q), o = reinterpret_cast<uintptr_t>(r.out);
+    if (r.rows < 1 || q + (r.rows - 1) * qs + n <= o || o + (r.rows - 1) * os + n <= q) return false;
+    if (r.rows == 1) return q != o;
+    if (qs != os) return true;
+    const long long by = (long long)(o > q ? o - q : q - o) % qs;
+    return q != o && (by < n || by > qs - n);
+}
+
 int check_rows(const PagePool& p, const PageRows& r, double scale)
 {
     if (r.rows < 0) return set_last_error(H2O_ERR_ARG, "rows must be >= 0 (got %d)", r.rows);
@@ -76,6 +89,7 @@ int check_rows(const PagePool& p, const PageRows& r, double scale)
     int rc;
     const long long need = (long long)p.heads * r.G * p.D;
     if ((rc = check_stride(r.q_stride, need, p.dtype, "q")) || (rc = check_stride(r.out_stride, need, p.dtype, "out"))) return rc;
+    if (rows_collide(r, need, p.dtype)) return set_last_error(H2O_ERR_ARG, "out overlaps other rows of q");
     return H2O_OK;
 }
 

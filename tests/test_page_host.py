@@ -199,3 +199,29 @@ def test_without_a_stream_calls_run_on_the_current_one(L, monkeypatch):
     assert set(lib.streams.values()) == {5}
     _all_calls(L, stream=6)
     assert set(lib.streams.values()) == {6}
+
+
+# rows of 1024 elements (2048 bytes), 3 of them; q at FAKE
+@pytest.mark.parametrize("change,refused", [
+    (dict(out=FAKE), False), (dict(out=FAKE, qs=1032, os=1032), False), (dict(out=FAKE + 3 * 2048), False), (dict(out=FAKE - 3 * 2048), False),
+    (dict(out=FAKE + 2048, qs=2048, os=2048), False), (dict(out=FAKE - 2048, qs=2560, os=2560), False), (dict(out=FAKE + 4 * 2048, qs=2048, os=2048), True),
+    (dict(out=FAKE + 16), True), (dict(out=FAKE + 2048), True), (dict(out=FAKE - 2048), True), (dict(out=FAKE + 2 * 2048 + 2032), True),
+    (dict(out=FAKE, os=2048), True), (dict(out=FAKE + 2032, qs=2048, os=2048), True), (dict(out=FAKE - 2048 - 16, qs=2048, os=2048), True),
+    (dict(out=FAKE, qs=1024, os=4096, rows=1), False), (dict(out=FAKE + 16, rows=1), True), (dict(out=FAKE + 2048, rows=1), False),
+    (dict(out=FAKE + 16, rows=0), False),
+])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_outputs_over_other_rows_of_q_are_refused(L, monkeypatch, change, refused, dtype):
+    monkeypatch.setenv("H2O_FAULT", "launch")              # what is not refused stops before its launch
+    change = dict(change, dtype=dtype)
+    if dtype == 0:                                         # the same bytes
+        change["d"] = 64
+        for k in ("qs", "os"):
+            change[k] = change.get(k, 1024) // 2
+    for name, base in (("h2o_page_attend", ATTEND), ("h2o_prefix_attend", PREFIX)):
+        base = dict(base, d=128)
+        rc = getattr(L.lib(), name)(*dict(base, **change).values())
+        if refused:
+            assert rc == L.H2O_ERR_ARG and "overlaps" in L.h2o_last_error(), (change, rc)
+        else:
+            assert rc == (L.H2O_OK if change.get("rows") == 0 else L.H2O_ERR_CUDA), (change, rc, L.h2o_last_error())
