@@ -521,7 +521,7 @@ def _query_rows(q, row_seq, row_pos, table, out, dev, dt, heads, d):
     i32 = _types[0]
     n, width = _dim(table, "table", 2)
     rows, hq, _ = _dim(q, "q", 3)
-    if hq < 1 or hq % heads:
+    if hq < 1 or heads < 1 or hq % heads:
         raise ValueError("q must be [rows][kv_heads * groups][head_dim] (got %s for %d cache heads)" % (list(q.shape), heads))
     shape = (rows, hq, d)
     qp, qs = _head_rows(q, "q", dt, shape, dev)

@@ -225,3 +225,17 @@ def test_outputs_over_other_rows_of_q_are_refused(L, monkeypatch, change, refuse
             assert rc == L.H2O_ERR_ARG and "overlaps" in L.h2o_last_error(), (change, rc)
         else:
             assert rc == (L.H2O_OK if change.get("rows") == 0 else L.H2O_ERR_CUDA), (change, rc, L.h2o_last_error())
+
+
+def test_binding_refuses_pools_without_heads(L, monkeypatch):
+    monkeypatch.setattr(L, "_types", None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: None)
+    K, B, q = (_Gpu(torch.zeros(*n)) for n in ((4, 0, 16, 64), (4, 0, 2, 64), (3, 4, 64)))
+    i, table, work = (_Gpu(torch.zeros(*n, dtype=t)) for n, t in (((3,), torch.int32), ((2, 3), torch.int32), ((64,), torch.uint8)))
+    with pytest.raises(ValueError, match="0 cache heads"):
+        L.h2o_page_attend(q, i, i, K, K, B, table, 2, 1, 0.1, q)
+    with pytest.raises(ValueError, match="0 cache heads"):
+        L.h2o_prefix_attend(q, i, i, K, K, i, 16, table, 0.1, q, work)
+    with pytest.raises(L.H2OError, match="kv_heads"):
+        L.h2o_page_write(_Gpu(torch.zeros(3, 0, 64)), _Gpu(torch.zeros(3, 0, 64)), i, K, K, B)
