@@ -237,5 +237,5 @@ def test_binding_refuses_pools_without_heads(L, monkeypatch):
         L.h2o_page_attend(q, i, i, K, K, B, table, 2, 1, 0.1, q)
     with pytest.raises(ValueError, match="0 cache heads"):
         L.h2o_prefix_attend(q, i, i, K, K, i, 16, table, 0.1, q, work)
-    with pytest.raises(L.H2OError, match="kv_heads"):
+    with pytest.raises(L.H2OError, match="non-NULL"):         # (an empty tensor has no memory)
         L.h2o_page_write(_Gpu(torch.zeros(3, 0, 64)), _Gpu(torch.zeros(3, 0, 64)), i, K, K, B)
