@@ -866,3 +866,84 @@ def test_rows_without_weight_are_zero_whatever_the_values(dtype, value):
     assert (out == 0).all()
     assert (_prefix(c, q.cuda(), [0, 0, 0], [59, -1, 5], c.table[1], 290, 0.125) == 0).all()
     assert (_prefix(c, q.cuda(), [0, 1, 1], [59, 299, 17], [], 0, 0.125) == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("groups", [3, 16])
+def test_weights_of_own_pages_keep_two_parts(d, groups):
+    # Attention to own pages multiplies each softmax weight in two bf16 parts, off by 2^-16 of it, so that an output is off by
+    # its own rounding, and by those 2^-16 and the fp32 terms above (twice the products: 4 n) of sum p|v|.  With small keys and
+    # some hundred tokens these are far below what weights of one part leave.
+    c = Cache([150, 90, 33], 2, d, 32, BF16, seed=7, kscale=0.1)
+    seq, pos = [0, 1, 2, 0], [149, 89, 32, 101]
+    q = _queries(4, 2 * groups, d, BF16, 5)
+    b, scale, one_part_fails = c.bounds(), d ** -0.5, False
+    for budget in (c.width, 3, 0):
+        if budget:
+            out, _ = _sparse(c, q.cuda(), seq, pos, budget, 1, scale)
+        else:
+            out = _prefix(c, q.cuda(), seq, pos, [], 0, scale)
+        for r in range(4):
+            mine = c.table[seq[r], :pos[r] // 32 + 1]
+            for h in range(2):
+                qh = q[r, h * groups:(h + 1) * groups].double()
+                at = _picks(qh, b, mine, h, budget or c.width, 1)
+                n = (len(at) - 1) * 32 + pos[r] % 32 + 1
+                k, v = c.rows(mine[at], h, n)
+                y, av, zmax, smax = _attention(qh, k, v, scale)
+                tol = (U24 * (2 * ((d + 8) * smax + 4 * zmax) + 4 * n + 64) + 2.0 ** -16) * av * (1 + 2.0 ** -7) + (2.0 ** -8 + U24) * y.abs()
+                _check(out[r, h * groups:(h + 1) * groups], (y, tol), "budget %d row %d" % (budget, r))
+                z = (qh @ k.T) * scale
+                e = torch.exp(z - z.amax(1, keepdim=True))
+                rough = ((e.to(BF16).double() @ v) / e.sum(1, keepdim=True)).to(BF16).double()
+                one_part_fails |= bool(((rough - y).abs() > tol).any())
+    assert one_part_fails, "the bound tells one part from two"
+
+
+@pytest.mark.parametrize("d,groups", [(64, 1), (128, 4), (128, 16)])
+def test_sparse_with_many_units_of_few_tiles(d, groups):
+    # a decode batch: more units than two-warp CTAs fit, each of which picks
+    g = np.random.default_rng(d)
+    lengths = [int(x) for x in g.integers(1, 700, 90)]
+    c = Cache(lengths, 8, d, 16, BF16, seed=d + groups)
+    seq, pos = list(range(90)), [n - 1 for n in lengths]
+    q = _queries(90, 8 * groups, d, BF16, 3)
+    for budget, recent in ((7, 2), (20, 20)):
+        want, picked = _sparse_ref(c, q, seq, pos, budget, recent, d ** -0.5)
+        out, got = _sparse(c, q.cuda(), seq, pos, budget, recent, d ** -0.5)
+        np.testing.assert_array_equal(got.cpu().numpy(), picked)
+        _check(out, want, "budget %d" % budget)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", [300, 4096, 16384])
+def test_tables_much_wider_than_the_requests(dtype, width):
+    lengths = [1, 40, 16 * 9, 16 * 21 + 5]
+    c = Cache(lengths, 2, 128, 16, dtype, seed=1, width=width)
+    seq, pos = [0, 1, 2, 3, 3], [0, 39, 16 * 9 - 1, 16 * 21 + 4, 100]
+    q = _queries(5, 6, 128, dtype, 2)
+    for budget, recent in ((4, 1), (19, 3)):
+        want, picked = _sparse_ref(c, q, seq, pos, budget, recent, 0.09)
+        out, got = _sparse(c, q.cuda(), seq, pos, budget, recent, 0.09)
+        np.testing.assert_array_equal(got.cpu().numpy(), picked)
+        _check(out, want, "budget %d" % budget)
+    for plen in (0, 140):
+        _check(_prefix(c, q.cuda(), seq, pos, c.table[2], plen, 0.09), _prefix_ref(c, q, seq, pos, c.table[2], plen, 0.09), "prefix %d" % plen)
+
+
+@pytest.mark.parametrize("dtype,d,groups", [(BF16, 128, 4), (BF16, 64, 1), (F32, 64, 2)])
+def test_one_long_request_among_short_ones(dtype, d, groups):
+    g = np.random.default_rng(d)
+    lengths = [int(x) for x in g.integers(1, 90, 40)]
+    lengths[17] = 20011
+    c = Cache(lengths, 4, d, 32, dtype, seed=d)
+    seq, pos = list(range(40)), [n - 1 for n in lengths]
+    q = _queries(40, 4 * groups, d, dtype, 2)
+    for budget, recent in ((30, 4), (500, 1)):
+        want, picked = _sparse_ref(c, q, seq, pos, budget, recent, d ** -0.5)
+        out, got = _sparse(c, q.cuda(), seq, pos, budget, recent, d ** -0.5)
+        np.testing.assert_array_equal(got.cpu().numpy(), picked)
+        _check(out, want, "budget %d" % budget)
+    for plen in (0, 70):
+        _check(_prefix(c, q.cuda(), seq, pos, c.table[17], plen, d ** -0.5), _prefix_ref(c, q, seq, pos, c.table[17], plen, d ** -0.5),
+               "prefix %d" % plen)
