@@ -27,7 +27,6 @@ namespace {
 
 constexpr int kKeys = 16;              // keys of a tile (page sizes are its multiples)
 constexpr float kEps = 1.4305115e-6f;  // 24 * 2^-24
-constexpr int kSMs = 152;
 // tiles in flight per warp
 template <typename T> constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
 
@@ -393,12 +392,7 @@ struct CoreSimt {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const unsigned char* a = vt + tile_at<T, D>(k0 + i, lane * E * (int)sizeof(T));
-                if constexpr (sizeof(T) == 2 || E == 4) load_vec<T, E>(reinterpret_cast<const T*>(a), v[i]);
-                else {
-                    const float2 w = *reinterpret_cast<const float2*>(a);
-                    v[i][0] = w.x;
-                    v[i][1] = w.y;
-                }
+                load_vec<T, E>(reinterpret_cast<const T*>(a), v[i]);
             }
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
@@ -964,23 +958,25 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
     cluster_wait();                                        // no CTA leaves while another reads its sums
 }
 
-// Warps of a CTA: two where there are more units than CTAs fit and each has
-// few tiles, so that more units are under way (6400 units of 12 tiles: 201 us
-// with four, 153 with two; 512 of 24: 81, 80; 512 of 96: 83, 89), and in fp32,
-// whose ring of four leaves an SM one CTA (832 units of 3 tiles and a prefix:
-// 40 us, 23 with two), unless the units are few.
-int attend_warps(long long units, int tiles, int dtype)
+// Warps of a CTA.  bf16: two where there are more units than CTAs fit and each
+// has few tiles, so that more units are under way (6400 units of 12 tiles: 201
+// us with four, 153 with two; 512 of 24: 81, 80; 512 of 96: 83, 89).  fp32,
+// whose ring of four leaves an SM one CTA: two (832 units of 3 tiles and a
+// prefix: 40 us, 23 with two) unless the units are few.
+int attend_warps(long long units, int tiles, bool bf16)
 {
-    if (dtype) return units > 4 * kSMs && tiles <= 32 ? 2 : 4;
+    if (bf16) return units > 4 * kSMs && tiles <= 32 ? 2 : 4;
     return units > kSMs / 8 ? 2 : 4;
 }
 
-// Clusters of c CTAs that the GPU holds at once, about: what is left over of
-// each group of SMs makes larger ones fit worse (at two CTAs an SM 152, 74, 36
-// and 14 of 2, 4, 8 and 16; at one 76, 36, 15 and 7).
+// Clusters of c CTAs (2 to 16) that the GPU holds at once, about: what is left
+// over of each group of SMs makes larger ones fit worse (at two CTAs an SM 152,
+// 74, 36 and 14 of 2, 4, 8 and 16; at one 76, 36, 15 and 7).  per_sm goes by
+// shared memory alone; at head_dim 64 in bf16, registers leave an SM three CTAs
+// of four warps where it says four.
 int clusters_that_fit(int c, int per_sm)
 {
-    return c == 1 ? 152 * per_sm : c == 2 ? 76 * per_sm : c == 4 ? 36 * per_sm : c == 8 ? (per_sm == 1 ? 15 : 17 * per_sm) : 7 * per_sm;
+    return c == 2 ? 76 * per_sm : c == 4 ? 36 * per_sm : c == 8 ? (per_sm == 1 ? 15 : 17 * per_sm) : 7 * per_sm;
 }
 
 // CTAs of a unit: as many, up to 16, as leave all clusters at once on the GPU
@@ -1045,7 +1041,7 @@ template <int D>
 cudaError_t by_warps(const PagePool& p, const PageRows& r, int budget, int recent, int* picked, const PrefixPart& part, cudaStream_t st)
 {
     const int tiles = (budget > 0 ? std::min(budget, r.width) : r.width) * (p.ps / kKeys);
-    if (attend_warps((long long)r.rows * p.heads, tiles, p.dtype) == 2) return by_groups<D, 2>(p, r, budget, recent, picked, part, st);
+    if (attend_warps((long long)r.rows * p.heads, tiles, p.dtype != 0) == 2) return by_groups<D, 2>(p, r, budget, recent, picked, part, st);
     return by_groups<D, 4>(p, r, budget, recent, picked, part, st);
 }
 

@@ -359,7 +359,7 @@ cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t st)
 {
     const long long work = std::max<long long>(a.n, ((long long)a.cap + 3) / 4);
     const int threads = work <= 256 ? 256 : 1024;
-    const int grid = (int)std::min<long long>(152, std::max<long long>(1, (work + threads - 1) / threads));
+    const int grid = (int)std::min<long long>(kSMs, std::max<long long>(1, (work + threads - 1) / threads));
     const size_t smem = 3 * sizeof(int) * (((size_t)a.n + 4) & ~(size_t)3);
     static SmemOnce once;                                  // (the kernel's own arrays count towards the 48 KB too)
     const cudaError_t e = once.allow(page_tables_kernel);
@@ -385,7 +385,7 @@ cudaError_t launch_page_write(const PagePool& p, const void* k, const void* v, l
                                                                                     k_stride, v_stride, slot, rows, tx);
     };
     auto by_rows = [&](auto t, auto d) {
-        if (tiles >= 2 * 152) go(t, d, std::integral_constant<int, 4>());
+        if (tiles >= 2 * kSMs) go(t, d, std::integral_constant<int, 4>());
         else go(t, d, std::integral_constant<int, 1>());
     };
     using D64 = std::integral_constant<int, 64>;

@@ -7,6 +7,7 @@
 
 namespace h2o {
 
+constexpr int kSMs = 152;
 constexpr int kMaxPageRequests = 16384;   // requests of one h2o_page_tables call
 constexpr int kMaxTableWidth = 16384;     // pages of one request
 constexpr int kMaxPickedPages = 4096;     // budget of a call that has to choose

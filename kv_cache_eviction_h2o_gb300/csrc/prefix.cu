@@ -12,8 +12,6 @@ namespace h2o {
 
 namespace {
 
-constexpr int kSMs = 152;
-
 // fp32 on the CUDA cores (bf16: prefix_tc.cu).  64 query rows x 64 keys a step: 16 x 16
 // threads, 4 x 4 logits and 4 x D / 16 output channels each.
 

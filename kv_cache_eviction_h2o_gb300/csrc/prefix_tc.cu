@@ -46,7 +46,6 @@ namespace h2o {
 
 namespace {
 
-constexpr int kSMs = 152;
 constexpr int kT = 128;
 constexpr int kThreads = 384;
 constexpr uint32_t kBox = kT * 64 * 2;             // 128 rows x 64 channels: 16 KB
