@@ -424,7 +424,9 @@ int h2o_selftest_wait_timeout(h2o_handle h);
  * h2o_page_attend and h2o_prefix_attend keep every token and read what a
  * query needs, where the handles above keep a budget and forget the rest.
  * The pages have no counterpart for them.  They hold no state and allocate
- * nothing: the caller owns all buffers and gives the stream with each call;
+ * nothing: the caller owns all buffers and gives the stream with each call
+ * (NULL: the legacy default stream; the Python binding's None: torch's current
+ * one);
  * every call may be captured into a CUDA graph.  Calls that share a buffer
  * one of them writes must be ordered by the caller.  There is no handle and
  * so no h2o_sync: what a device-side check finds is told by the outputs, as
@@ -460,8 +462,10 @@ int h2o_selftest_wait_timeout(h2o_handle h);
  *   row_seq, row_pos, slot [rows_cap]: request, position and slot of each
  *             new token, requests in order; -1 in the rows past the last
  *             (slot is also -1 where a table or free-list entry is no page
- *             number);
- *   status    [4]: {rows, pages taken, longest len_after, error bits}.
+ *             number: no error bit, the token is not written, and rows that
+ *             attend to that entry are NaN);
+ *   status    [4]: {rows, pages taken, longest len_after, error bits}; with an
+ *             error bit the first three are 0.
  * All arrays are device int32; an output that overlaps an input is refused
  * (so len_after is not len_before).  free_pages is only read: the caller
  * drops the first status[1] of it.  All or nothing: with an error bit (1: a
@@ -498,8 +502,9 @@ int h2o_page_write(const void* k, const void* v, long long k_stride, long long v
  * that keys within page b's bounds allow (by s_b in fp64 where fp32 does not
  * settle the order, ties to the lower page; a NaN ranks first).  Only full pages older than the row's
  * own are ranked.  out = softmax(scale q.K) V over the tokens of those pages.
- *   q, out [rows][kv_heads * groups][head_dim] of dtype (sums in fp32; bf16
- *   weights and outputs are rounded once), query head h * groups + g to cache
+ *   q, out [rows][kv_heads * groups][head_dim] of dtype (sums in fp32; with
+ *   bf16, softmax weights are multiplied in two bf16 parts, 2^-16 of each off
+ *   at most, and outputs are rounded once), query head h * groups + g to cache
  *   head h; 1 <= groups <= 16.  out may be q itself, or other columns of the
  *   rows that q is a slice of; any other overlap of the two is refused.
  *   bounds may be NULL when budget >= table_width; otherwise budget <= 4096.
@@ -522,8 +527,10 @@ int h2o_page_attend(const void* q, long long q_stride, const int* row_seq, const
  * table (positions and lengths count from the prefix's end; row_pos -1: none).
  * The prefix is read once for all rows, whatever their number, as a product
  * over all queries of a cache head.  With prefix_len 0 (prefix_table NULL)
- * this is attention over whole paged caches.  Other arguments, padding rows
- * and bad entries as h2o_page_attend (a bad prefix page: NaN in every row).
+ * this is attention over whole paged caches.  With bf16 the prefix's softmax
+ * weights are rounded to bf16 once (2^-8 of each off at most), those of own
+ * pages as in h2o_page_attend.  Other arguments, padding rows and bad entries
+ * as h2o_page_attend (a bad prefix page: NaN in every row).
  *   work: device buffer of h2o_prefix_work_bytes for the same sizes; what it
  *   holds before and after does not matter, and calls that may overlap need
  *   one each.
