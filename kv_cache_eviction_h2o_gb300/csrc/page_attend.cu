@@ -200,10 +200,10 @@ struct Held {
 
 // Leaves s[j] >= the returned bound exactly for the `take` best of the n
 // pages' scores s (0 < take < n).  `again(j)` is page j's score in fp64, made
-// by a whole warp.  big: room for n keys of 64 bits; s may be overwritten,
+// by a whole warp, after `wide` and a barrier.  big: room for n keys of 64 bits; s may be overwritten,
 // after `settle`, which is called once.
-template <int NW, class Settle, class Again>
-__device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned long long* big, Settle settle, Again again)
+template <int NW, class Settle, class Wide, class Again>
+__device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned long long* big, Settle settle, Wide wide, Again again)
 {
     constexpr int NT = NW * 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -251,6 +251,7 @@ __device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned
         if (open <= kFew) {
             // a few: their fp64 scores, each compared with every other
             if (tid == 0) P.n_open = 0;
+            wide();
             __syncthreads();
             for (int j = tid; j < n; j += NT)
                 if (s[j] <= above && s[j] >= below) P.at[atomicAdd(&P.n_open, 1)] = j;
@@ -273,6 +274,8 @@ __device__ float pick_bound(PickSmem<NW>& P, float* s, int n, int take, unsigned
         settle();
     }
     // the open pages by their fp64 scores
+    wide();
+    __syncthreads();
     for (int j = warp; j < n; j += NW) {
         const float x = s[j];
         const bool open = !(x > above) && !(x < below);
@@ -599,7 +602,7 @@ template <int N> __device__ __forceinline__ void ld_cluster_f(uint32_t addr, flo
 
 template <int D, class Core>
 struct alignas(16) AttendSmem {
-    float2 w[2 * D];                   // the page weights, minima's then maxima's, as w.x + w.y + w_lo
+    float2 w[2 * D];                   // the page weights, minima's then maxima's, as w.x + w.y + w_lo; later in fp64
     float w_lo[2 * D];
     typename Core::Shared core;
     float2 wml[Core::kWarps][kMaxPageGroups];
@@ -763,13 +766,17 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             }
             __syncthreads();
             cluster_arrive();                              // (its wait: before scores are overwritten)
-            const float bound = pick_bound(S.pick, scores, ncand, take, big, [] { cluster_wait(); }, [&](int j) {
+            const float bound = pick_bound(S.pick, scores, ncand, take, big, [] { cluster_wait(); }, [&] {
+                // (in their place: the fp32 scores are made)
+                for (int i = tid; i < 2 * D; i += kNT)
+                    reinterpret_cast<double*>(S.w)[i] = (double)S.w[i].x + ((double)S.w[i].y + (double)S.w_lo[i]);
+            }, [&](int j) {
                 const int p = table[j];
                 if ((unsigned)p >= (unsigned)pool.pages) return (double)NAN;
                 const T* b = bounds + ((size_t)p * pool.heads + h) * 2 * D;
                 double s = 0.0;
                 if (__uint_as_float(S.pick.amax) < FLT_MAX) {      // (finite factors; fp64 holds their sum)
-                    for (int e = lane; e < 2 * D; e += 32) s += ((double)S.w[e].x + ((double)S.w[e].y + (double)S.w_lo[e])) * (double)Elem<T>::to_f(b[e]);
+                    for (int e = lane; e < 2 * D; e += 32) s += reinterpret_cast<const double*>(S.w)[e] * (double)Elem<T>::to_f(b[e]);
                 } else {
                     // an infinite bound on the side that no query takes counts for nothing: the maxima themselves
                     for (int e = lane; e < D; e += 32)
