@@ -603,11 +603,13 @@ template <int N> __device__ __forceinline__ void ld_cluster_f(uint32_t addr, flo
 template <int D, class Core>
 struct alignas(16) AttendSmem {
     float2 w[2 * D];                   // the page weights, minima's then maxima's, as w.x + w.y + w_lo; later in fp64
-    float w_lo[2 * D];
     typename Core::Shared core;
     float2 wml[Core::kWarps][kMaxPageGroups];
     float2 ml[kMaxPageGroups];
     PickSmem<Core::kWarps> pick;
+    // (the marks are made when pages are ranked)
+    __device__ __forceinline__ float* w_lo() { return reinterpret_cast<float*>(pick.mark); }
+    static_assert(sizeof(pick.mark) >= 2 * D * sizeof(float), "w_lo fits");
 };
 
 // Shared memory: the warps' rings (fp64 keys while picking), AttendSmem, and
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
                     s.add(lo ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x));
                 }
                 S.w[i] = s.rounded();
-                S.w_lo[i] = s.lo;
+                S.w_lo()[i] = s.lo;
             }
             __syncthreads();
             float w[NV][N];
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(Core::kWarps * 32, sizeof(T) == 2 ? 8 / Core::
             const float bound = pick_bound(S.pick, scores, ncand, take, big, [] { cluster_wait(); }, [&] {
                 // (in their place: the fp32 scores are made)
                 for (int i = tid; i < 2 * D; i += kNT)
-                    reinterpret_cast<double*>(S.w)[i] = (double)S.w[i].x + ((double)S.w[i].y + (double)S.w_lo[i]);
+                    reinterpret_cast<double*>(S.w)[i] = (double)S.w[i].x + ((double)S.w[i].y + (double)S.w_lo()[i]);
             }, [&](int j) {
                 const int p = table[j];
                 if ((unsigned)p >= (unsigned)pool.pages) return (double)NAN;
