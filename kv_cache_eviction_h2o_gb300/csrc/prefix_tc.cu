@@ -27,9 +27,9 @@
 // of the unrounded weights.  Waits are bounded; one that runs out leaves NaN
 // sums.
 //
-// Measured, 64 requests of 8 x 8 heads behind 32768 tokens (68.7 GFLOP): 51 us,
-// 1.35 PFLOP/s, 0.69 of the bf16 peak measured with a library product.  A tile
-// of both streams takes 2850 cycles, of which its products are 2050.  What
+// Measured, 64 requests of 8 x 8 heads behind 32768 tokens (68.7 GFLOP): 52 us,
+// 1.31 PFLOP/s, 0.67 of the bf16 peak measured with a library product.  A tile
+// of both streams takes 2900 cycles, of which its products are 2050.  What
 // bounds it is the products and the shared memory that feeds them: those of
 // Q K^T read both operands from it (by halves of 64 keys the queries twice),
 // those of P V one, and the loads write into it, which makes 2300 to 2560 of
