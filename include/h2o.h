@@ -544,6 +544,133 @@ int h2o_prefix_attend(const void* q, long long q_stride, const int* row_seq, con
 /* Bytes of h2o_prefix_attend's workspace (negative: an h2o_status). */
 long long h2o_prefix_work_bytes(int rows, int kv_heads, int groups, int head_dim, int prefix_len, int dtype);
 
+/*
+ * Prompts and quantised paged caches -- h2o_rope, h2o_prompt_attend and
+ * h2o_page_quant_*: what stands between a projection's query, key and value
+ * rows and a paged cache of 8- or 4-bit codes.  The pages have no counterpart
+ * for them, but for the codes' form (H2O_KV8, H2O_KV4).  As the paged-cache
+ * calls they hold no state and allocate nothing, take the caller's buffers,
+ * strided rows and stream, and may be captured into a CUDA graph.
+ */
+
+/* the channels of a pair that is turned together: i and rot_dim / 2 + i, or 2i and 2i + 1 */
+enum { H2O_ROPE_HALF = 0, H2O_ROPE_PAIRS = 1 };
+/* how h2o_rope_table scales the frequencies for contexts longer than a model's own */
+enum { H2O_ROPE_PLAIN = 0, H2O_ROPE_LINEAR = 1, H2O_ROPE_BASE = 2, H2O_ROPE_PARTS = 3 };
+
+/*
+ * h2o_rope_table -- the turns a position of each channel pair, to a HOST buffer
+ * table [rot_dim / 2]: pair i turns by f_i radians a position, f_i = base^(-2i /
+ * rot_dim), which is table[i] = rint(f_i / (2 pi) 2^64), so that the angle of
+ * any position is a whole product modulo 2^64 and as exact as that of position 1.
+ *   H2O_ROPE_PLAIN:  f_i as it is (factor, original_len, low, high not read);
+ *   H2O_ROPE_LINEAR: f_i / factor;
+ *   H2O_ROPE_BASE:   the base times factor^(rot_dim / (rot_dim - 2)): the
+ *                    fastest pair as it is, the slowest divided by factor
+ *                    (rot_dim >= 4);
+ *   H2O_ROPE_PARTS:  f_i ((1 - g) / factor + g), g = (t - low) / (high - low)
+ *                    within 0 and 1, t = original_len f_i / (2 pi) the pair's
+ *                    turns in the original context: pairs that turn at least
+ *                    `high` times there as they are, those that turn at most
+ *                    `low` times divided by factor.  0 <= low < high.
+ * rot_dim even and in [2, 128]; base >= 1, factor >= 1.  A caller may make a table of its
+ * own (device int64); with the negated table h2o_rope turns back, which is also the
+ * gradient of its outputs with respect to its inputs.
+ */
+int h2o_rope_table(int rot_dim, double base, int kind, double factor, double original_len, double low, double high,
+                   long long* table);
+
+/*
+ * h2o_rope -- rotary positions: of the first rot_dim channels of every head of
+ * row r, pair (a, b) becomes amplitude (a cos t - b sin t, b cos t + a sin t),
+ * t = 2 pi row_pos[r] table[i] 2^-64; the other channels stay as they are.
+ *   q, q_out [rows][heads][head_dim], k, k_out [rows][kv_heads][head_dim] of
+ *   dtype H2O_F32 or H2O_BF16 (arithmetic in fp32, one rounding at the end); k
+ *   and k_out NULL with kv_heads 0: queries only.  q_out may be q and k_out k
+ *   (the same rows), or other columns of the same rows; other overlaps of an
+ *   output with an input or with the other output are refused.
+ *   row_pos [rows]: positions; a row with row_pos < 0 is a padding row, and its
+ *   rows of the outputs are left as they were.
+ *   table: device int64 [rot_dim / 2], 8-byte aligned; form H2O_ROPE_HALF or
+ *   H2O_ROPE_PAIRS; amplitude finite (1, or the factor that scaled tables ask
+ *   for).  rot_dim even and in [2, head_dim]; head_dim 64 or 128;
+ *   rows * (heads + kv_heads) <= 2^28.
+ */
+int h2o_rope(const void* q, long long q_stride, void* q_out, long long q_out_stride, int heads, const void* k,
+             long long k_stride, void* k_out, long long k_out_stride, int kv_heads, const int* row_pos, int rows,
+             const long long* table, int rot_dim, int form, double amplitude, int head_dim, int dtype,
+             void* cuda_stream);
+
+/*
+ * h2o_prompt_attend -- causal attention over the packed rows of several
+ * requests.  Request i has query rows q_start[i] .. q_start[i + 1] - 1 and key
+ * rows k_start[i] .. k_start[i + 1] - 1; the queries are its newest tokens, so
+ * query x of n_q sees keys 0 .. n_k - n_q + x (those with none, where n_k < n_q,
+ * give zero).  out = softmax(scale q.k) v.
+ *   q, out [rows][kv_heads * groups][head_dim], k, v [k_rows][kv_heads][head_dim]
+ *   of dtype H2O_F32 or H2O_BF16; query head h * groups + g to key head h, 1 <=
+ *   groups <= 16.  Sums and statistics in fp32; with bf16 each softmax weight is
+ *   rounded to bf16 for its product (2^-8 of it off at most) and outputs once.
+ *   out may not overlap q, k or v.
+ *   q_start, k_start [requests + 1]: device int32, ascending, within rows and
+ *   k_rows; k_start NULL: the same as q_start.  Rows of out outside all
+ *   requests are left as they were, and so are those of a request whose rows
+ *   or keys are none of the call's.  With starts that descend, which rows are
+ *   written is not defined; nothing else is.
+ * A row all of whose logits are -inf is zero.  Keys and values a query does not
+ * see do not touch it, whatever they hold.  rows * kv_heads * groups and k_rows
+ * * kv_heads <= 2^28, 1 <= requests <= 16384.
+ */
+int h2o_prompt_attend(const void* q, long long q_stride, int rows, const void* k, long long k_stride, const void* v,
+                      long long v_stride, int k_rows, int kv_heads, int groups, int head_dim, int dtype,
+                      const int* q_start, const int* k_start, int requests, double scale, void* out,
+                      long long out_stride, void* cuda_stream);
+
+/*
+ * A quantised pool: K, V [num_pages][kv_heads][page_size][head_dim] int8 codes
+ * (dtype with H2O_KV8) or [num_pages][kv_heads][page_size][head_dim / 2] bytes
+ * of two 4-bit codes (H2O_KV4), and kscale, vscale fp32 [num_pages][kv_heads]
+ * [page_size]; dtype's H2O_F32 or H2O_BF16 is that of the rows outside the
+ * pool.  Codes and scales follow the rule of the two flags; a row that holds an
+ * infinity or a NaN has codes of zero and the scale NaN, and reads back as NaN.
+ * Other sizes, tables, slots and rows as for the paged caches above.
+ *
+ * h2o_page_quant_write -- key and value rows k, v [rows][kv_heads][head_dim]
+ * into their slots, as codes.  Rows whose slot is outside the pool (-1: a
+ * padding row) are skipped; no slot comes twice.
+ */
+int h2o_page_quant_write(const void* k, const void* v, long long k_stride, long long v_stride, const int* slot,
+                         int rows, void* K, void* V, float* kscale, float* vscale, int num_pages, int kv_heads,
+                         int page_size, int head_dim, int dtype, void* cuda_stream);
+
+/*
+ * h2o_page_quant_read -- the rows of slots, k and v [rows][kv_heads][head_dim]:
+ * code * scale in fp32, then in dtype (keys and values of a cached context for
+ * h2o_prompt_attend).  Slots may come more than once; rows of k and v whose
+ * slot is outside the pool are left as they were.  k and v are different
+ * memory, or other columns of the same rows.
+ */
+int h2o_page_quant_read(const void* K, const void* V, const float* kscale, const float* vscale, int num_pages,
+                        int kv_heads, int page_size, int head_dim, int dtype, const int* slot, int rows, void* k,
+                        long long k_stride, void* v, long long v_stride, void* cuda_stream);
+
+/*
+ * h2o_page_quant_attend -- attention over whole quantised paged caches: row r
+ * sees the tokens 0..row_pos[r] of request row_seq[r],
+ *   out = softmax(scale q.K) V,  K = kscale * codes, V = vscale * codes.
+ * Codes are multiplied as they are (exact in fp16, scales apart in fp32); queries are multiplied
+ * as fp16 numbers with a power of two apart, two of them where dtype is H2O_F32
+ * (off by 2^-23 of the row's largest at most; bf16 by 2^-25), and weights, with the value's
+ * scale and a power of two apart, as one fp16 number (2^-12 of each off at most) or,
+ * with H2O_F32, two (2^-23).  Other arguments,
+ * padding rows, empty rows and bad entries as h2o_page_attend.
+ */
+int h2o_page_quant_attend(const void* q, long long q_stride, const int* row_seq, const int* row_pos, int rows,
+                          const void* K, const void* V, const float* kscale, const float* vscale, int num_pages,
+                          int kv_heads, int groups, int page_size, int head_dim, int dtype, const int* table,
+                          int requests, int table_width, double scale, void* out, long long out_stride,
+                          void* cuda_stream);
+
 /* Thread-local description of the last failure in this thread ("" if none). */
 const char* h2o_last_error(void);
 

@@ -14,7 +14,8 @@ and checks the type and size of every host array, and of every tensor it
 is given, before the library writes into or reads from it; a raw integer
 pointer is passed through unchecked.
 
-The paged-cache calls (``h2o_page_*``, ``h2o_prefix_*``) have no handle: they
+The paged-cache and prompt calls (``h2o_page_*``, ``h2o_prefix_*``, ``h2o_rope``,
+``h2o_prompt_attend``) have no handle: they
 take torch tensors only, read every size from the tensors' shapes and check
 them against one another; without a `stream` they run on torch's current one.
 """
@@ -37,6 +38,12 @@ H2O_F32 = 0
 H2O_BF16 = 1
 H2O_KV8 = 2
 H2O_KV4 = 4
+H2O_ROPE_HALF = 0
+H2O_ROPE_PAIRS = 1
+H2O_ROPE_PLAIN = 0
+H2O_ROPE_LINEAR = 1
+H2O_ROPE_BASE = 2
+H2O_ROPE_PARTS = 3
 
 # every symbol include/h2o.h declares, with (restype, argtypes)
 _vp = ctypes.c_void_p
@@ -77,6 +84,13 @@ SIGNATURES = {
     "h2o_prefix_attend": (_i, [_vp, _ll, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _vp, _i, _i, _d,
                                _vp, _ll, _vp, _ll, _vp]),
     "h2o_prefix_work_bytes": (_ll, [_i, _i, _i, _i, _i, _i]),
+    "h2o_rope_table": (_i, [_i, _d, _i, _d, _d, _d, _d, _vp]),
+    "h2o_rope": (_i, [_vp, _ll, _vp, _ll, _i, _vp, _ll, _vp, _ll, _i, _vp, _i, _vp, _i, _i, _d, _i, _i, _vp]),
+    "h2o_prompt_attend": (_i, [_vp, _ll, _i, _vp, _ll, _vp, _ll, _i, _i, _i, _i, _i, _vp, _vp, _i, _d, _vp, _ll, _vp]),
+    "h2o_page_quant_write": (_i, [_vp, _vp, _ll, _ll, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "h2o_page_quant_read": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _ll, _vp, _ll, _vp]),
+    "h2o_page_quant_attend": (_i, [_vp, _ll, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _d, _vp, _ll,
+                                   _vp]),
 }
 
 H2O_NOALLOC_MAX_TOKENS = 1 << 20
@@ -378,7 +392,7 @@ def h2o_prompt_scores_noalloc(Q, K, batch, heads, T, head_dim, dtype, scale, c, 
 # the cheapest comparisons there are; what is wrong is found out afterwards.
 
 _CODES = {"torch.bfloat16": H2O_BF16, "torch.float32": H2O_F32}
-_types = None          # (int32, uint8, {element type: its code}, the current device's index, its current stream)
+_types = None          # (int32, uint8, {element type: its code}, the current device's index, its current stream, {code type: its flag}, float32, int64)
 
 
 def _torch_types():
@@ -386,7 +400,7 @@ def _torch_types():
     if _types is None:
         import torch
         _types = (torch.int32, torch.uint8, {getattr(torch, k[6:]): v for k, v in _CODES.items()}, torch.cuda.current_device,
-                  torch.cuda.current_stream)
+                  torch.cuda.current_stream, {torch.int8: H2O_KV8, torch.uint8: H2O_KV4}, torch.float32, torch.int64)
     return _types
 
 
@@ -564,5 +578,134 @@ def h2o_prefix_attend(q, row_seq, row_pos, K, V, prefix_table, prefix_len, table
     size = _count(work, "work")
     rc = lib().h2o_prefix_attend(qp, qs, sp, pp, rows, Kp, Vp, pages, heads, groups, ps, d, code, xp, prefix_len, tp, n,
                                  width, scale, op, os_, _array(work, "work", _types[1], size, dev), size, _on_stream(stream))
+    if rc:
+        _check(rc)
+
+
+# ------------------------------------------- prompts and quantised paged caches
+
+def h2o_rope_table(rot_dim, base=10000.0, kind=H2O_ROPE_PLAIN, factor=1.0, original_len=0.0, low=0.0, high=0.0):
+    """The turns a position of each channel pair, as a numpy int64 array
+    [rot_dim / 2] to be copied to the GPU; see include/h2o.h."""
+    table = np.empty(max(1, rot_dim // 2), np.int64)
+    _check(lib().h2o_rope_table(rot_dim, base, kind, factor, original_len, low, high, table.ctypes.data))
+    return table
+
+
+def _rows_type(x, what):
+    """(element type, its code) of rows."""
+    code = _torch_types()[2].get(getattr(x, "dtype", None))
+    if code is None:
+        raise TypeError("%s must be a tensor of dtype float32 or bfloat16 (got %s)" % (what, getattr(x, "dtype", type(x))))
+    return x.dtype, code
+
+
+def h2o_rope(q, k, row_pos, table, form, amplitude, q_out, k_out, stream=None):
+    """Rotary positions of q [rows][heads][head_dim] and k [rows][kv_heads]
+    [head_dim] (k and k_out None: queries only) into q_out and k_out, which may
+    be q and k; table: int64 [rot_dim / 2] on the GPU.  See include/h2o.h."""
+    dt, code = _rows_type(q, "q")
+    types = _types
+    shape = _dim(q, "q", 3)
+    rows, heads, d = shape
+    dev = _on_current(q, types[3])
+    qp, qs = _head_rows(q, "q", dt, shape, dev)
+    op, os_ = _head_rows(q_out, "q_out", dt, shape, dev)
+    kv_heads, kp, ks, kop, kos = 0, None, 0, None, 0
+    if k is not None:
+        kshape = _dim(k, "k", 3)
+        kv_heads = kshape[1]
+        kshape = (rows, kv_heads, d)
+        kp, ks = _head_rows(k, "k", dt, kshape, dev)
+        kop, kos = _head_rows(k_out, "k_out", dt, kshape, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    half = _count(table, "table")
+    rc = lib().h2o_rope(qp, qs, op, os_, heads, kp, ks, kop, kos, kv_heads, _array(row_pos, "row_pos", types[0], rows, dev), rows,
+                        _array(table, "table", types[7], half, dev), 2 * half, form, amplitude, d, code, _on_stream(stream))
+    if rc:
+        _check(rc)
+
+
+def h2o_prompt_attend(q, k, v, q_start, k_start, scale, out, stream=None):
+    """Causal attention of packed requests: q, out [rows][kv_heads * groups]
+    [head_dim], k, v [k_rows][kv_heads][head_dim], q_start and k_start int32
+    [requests + 1] (k_start None: q_start).  See include/h2o.h."""
+    dt, code = _rows_type(q, "q")
+    types = _types
+    shape = _dim(q, "q", 3)
+    rows, hq, d = shape
+    dev = _on_current(q, types[3])
+    krows, heads, _ = _dim(k, "k", 3)
+    if hq < 1 or heads < 1 or hq % heads:
+        raise ValueError("q must be [rows][kv_heads * groups][head_dim] (got %s for %d key heads)" % (list(shape), heads))
+    kshape = (krows, heads, d)
+    qp, qs = _head_rows(q, "q", dt, shape, dev)
+    kp, ks = _head_rows(k, "k", dt, kshape, dev)
+    vp, vs = _head_rows(v, "v", dt, kshape, dev)
+    op, os_ = _head_rows(out, "out", dt, shape, dev)
+    n = _count(q_start, "q_start")
+    rc = lib().h2o_prompt_attend(qp, qs, rows, kp, ks, vp, vs, krows, heads, hq // heads, d, code, _array(q_start, "q_start", types[0], n, dev),
+                                 None if k_start is None else _array(k_start, "k_start", types[0], n, dev), n - 1, scale, op, os_,
+                                 _on_stream(stream))
+    if rc:
+        _check(rc)
+
+
+def _quant_pool(K, V, kscale, vscale):
+    """(device, flag of the codes, pointers, (pages, heads, page_size, head_dim)) of a quantised pool."""
+    types = _torch_types()
+    kt = getattr(K, "dtype", None)
+    flag = types[5].get(kt)
+    if flag is None:
+        raise TypeError("K must be a tensor of dtype int8 or uint8 (got %s)" % getattr(K, "dtype", type(K)))
+    shape = K.shape
+    if len(shape) != 4:
+        raise ValueError("K must be [pages][kv_heads][page_size][head_dim] codes, or [..][head_dim / 2] bytes of two (got %s)" % list(shape))
+    dev = _on_current(K, types[3])
+    pages, heads, ps, d = shape
+    scales = (pages, heads, ps)
+    return dev, flag, (_tensor(K, "K", kt, shape, dev), _tensor(V, "V", kt, shape, dev), _tensor(kscale, "kscale", types[6], scales, dev),
+                       _tensor(vscale, "vscale", types[6], scales, dev)), (pages, heads, ps, d if flag == H2O_KV8 else 2 * d)
+
+
+def h2o_page_quant_write(k, v, slot, K, V, kscale, vscale, stream=None):
+    """Key and value rows [rows][kv_heads][head_dim] into their slots of a
+    quantised pool (int8 codes: K, V int8; 4-bit codes: uint8 [..][head_dim / 2];
+    scales float32 [pages][kv_heads][page_size]); see include/h2o.h."""
+    dev, flag, pool, (pages, heads, ps, d) = _quant_pool(K, V, kscale, vscale)
+    dt, code = _rows_type(k, "k")
+    rows = _count(slot, "slot")
+    shape = (rows, heads, d)
+    kp, ks = _head_rows(k, "k", dt, shape, dev)
+    vp, vs = _head_rows(v, "v", dt, shape, dev)
+    rc = lib().h2o_page_quant_write(kp, vp, ks, vs, _array(slot, "slot", _types[0], rows, dev), rows, *pool, pages, heads, ps, d, code | flag,
+                                    _on_stream(stream))
+    if rc:
+        _check(rc)
+
+
+def h2o_page_quant_read(K, V, kscale, vscale, slot, k, v, stream=None):
+    """The rows that slots of a quantised pool hold, into k and v [rows][kv_heads]
+    [head_dim]; see include/h2o.h."""
+    dev, flag, pool, (pages, heads, ps, d) = _quant_pool(K, V, kscale, vscale)
+    dt, code = _rows_type(k, "k")
+    rows = _count(slot, "slot")
+    shape = (rows, heads, d)
+    kp, ks = _head_rows(k, "k", dt, shape, dev)
+    vp, vs = _head_rows(v, "v", dt, shape, dev)
+    rc = lib().h2o_page_quant_read(*pool, pages, heads, ps, d, code | flag, _array(slot, "slot", _types[0], rows, dev), rows, kp, ks, vp, vs,
+                                   _on_stream(stream))
+    if rc:
+        _check(rc)
+
+
+def h2o_page_quant_attend(q, row_seq, row_pos, K, V, kscale, vscale, table, scale, out, stream=None):
+    """Attention over whole quantised paged caches; see include/h2o.h."""
+    dev, flag, pool, (pages, heads, ps, d) = _quant_pool(K, V, kscale, vscale)
+    dt, code = _rows_type(q, "q")
+    qp, qs, sp, pp, rows, groups, tp, n, width, op, os_ = _query_rows(q, row_seq, row_pos, table, out, dev, dt, heads, d)
+    rc = lib().h2o_page_quant_attend(qp, qs, sp, pp, rows, *pool, pages, heads, groups, ps, d, code | flag, tp, n, width, scale, op, os_,
+                                     _on_stream(stream))
     if rc:
         _check(rc)
