@@ -618,8 +618,8 @@ int h2o_rope(const void* q, long long q_stride, void* q_out, long long q_out_str
  *   or keys are none of the call's.  With starts that descend, which rows are
  *   written is not defined; nothing else is.
  * A row all of whose logits are -inf is zero.  Keys and values a query does not
- * see do not touch it, whatever they hold.  rows * kv_heads * groups and k_rows
- * * kv_heads <= 2^28, 1 <= requests <= 16384.
+ * see do not touch it, whatever they hold.  rows, k_rows <= 2^24, rows * kv_heads
+ * * groups and k_rows * kv_heads <= 2^28, 1 <= requests <= 16384.
  */
 int h2o_prompt_attend(const void* q, long long q_stride, int rows, const void* k, long long k_stride, const void* v,
                       long long v_stride, int k_rows, int kv_heads, int groups, int head_dim, int dtype,

@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libh2o_gb300.so")
 SOURCES = ["h2o_api.cu", "decode.cu", "decode_warp.cu", "prompt.cu", "prompt_tc.cu", "noalloc.cu", "page_api.cu",
-           "paged.cu", "page_attend.cu", "prefix.cu", "prefix_tc.cu", "prompt_api.cu", "rope.cu", "prompt_attend.cu",
+           "paged.cu", "page_attend.cu", "prefix.cu", "prefix_tc.cu", "prompt_api.cu", "rope.cu", "prompt_attend.cu", "prompt_attend_tc.cu",
            "page_quant.cu", "quant_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

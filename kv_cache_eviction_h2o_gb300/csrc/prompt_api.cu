@@ -159,7 +159,8 @@ int h2o_prompt_attend(const void* q, long long q_stride, int rows, const void* k
 {
     int rc;
     if ((rc = check_row_type(dtype)) || (rc = check_head_dim(head_dim))) return rc;
-    if (rows < 0 || k_rows < 0) return set_last_error(H2O_ERR_ARG, "rows and k_rows must be >= 0 (got %d and %d)", rows, k_rows);
+    if (rows < 0 || rows > kMaxPromptRows || k_rows < 0 || k_rows > kMaxPromptRows)
+        return set_last_error(H2O_ERR_ARG, "rows and k_rows must be in [0, 2^24] (got %d and %d)", rows, k_rows);
     if (kv_heads < 1 || kv_heads > 65535) return set_last_error(H2O_ERR_ARG, "kv_heads must be in [1, 65535] (got %d)", kv_heads);
     if (groups < 1 || groups > kMaxPageGroups) return set_last_error(H2O_ERR_ARG, "groups must be in [1, %d] (got %d)", kMaxPageGroups, groups);
     if (requests < 1 || requests > kMaxPromptRequests)

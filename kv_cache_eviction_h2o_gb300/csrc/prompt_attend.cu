@@ -3,8 +3,7 @@
 //
 // A warp a query row of one head: a running maximum m (base 2) and sum l, keys
 // one after another.
-#include "common.cuh"
-#include "prompts.h"
+#include "prompt_rows.cuh"
 
 namespace h2o {
 
@@ -27,8 +26,7 @@ __device__ __forceinline__ int request_of(const int* start, int n, int r)
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32) prompt_rows_kernel(const PackedArgs A)
 {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, hq = A.heads * A.G;
+    const int hq = A.heads * A.G;
     const long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int row = (int)(u / hq), h = (int)(u % hq);
     if (row >= A.rows) return;
@@ -36,33 +34,10 @@ __global__ void __launch_bounds__(kWarps * 32) prompt_rows_kernel(const PackedAr
     if (i < 0) return;
     const int q0 = A.q_start[i], q1 = A.q_start[i + 1], k0 = A.k_start[i], k1 = A.k_start[i + 1];
     if (q0 < 0 || q1 > A.rows || row < q0 || row >= q1 || k0 < 0 || k1 < k0 || k1 > A.k_rows) return;
-    const int n = k1 - k0 - (q1 - q0) + (row - q0) + 1;    // keys it sees
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-    load_vec<T, E>(static_cast<const T*>(A.q) + row * A.q_stride + h * D + lane * E, q);
-    const T* k = static_cast<const T*>(A.k) + k0 * A.k_stride + h / A.G * D + lane * E;
-    const T* v = static_cast<const T*>(A.v) + k0 * A.v_stride + h / A.G * D + lane * E;
-    for (int j = 0; j < n; ++j) {
-        float x[E], y[E], z = 0.f;
-        load_vec<T, E>(k + j * A.k_stride, x);
-        load_vec<T, E>(v + j * A.v_stride, y);
-#pragma unroll
-        for (int e = 0; e < E; ++e) z = fmaf(q[e], x[e], z);
-        z = warp_sum(z) * A.qscale;
-        const float mn = z > m || z != z ? z : m, base = mn == -INFINITY ? 0.f : mn;
-        const float a = ex2_approx(m - base), p = ex2_approx(z - base);
-        m = mn;
-        l = fmaf(l, a, p);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(p, y[e], o[e] * a);
-    }
-    const float f = 1.f / l;
-    T* out = static_cast<T*>(A.out) + row * A.out_stride + h * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float x = l == 0.f ? 0.f : o[e] * f;
-        if constexpr (sizeof(T) == 2) out[e] = __float2bfloat16_rn(x);
-        else out[e] = x;
-    }
+    const int n = min(k1 - k0, k1 - k0 - (q1 - q0) + (row - q0) + 1);    // keys it sees
+    prompt_row<T, D>(static_cast<const T*>(A.q) + row * A.q_stride + h * D, static_cast<const T*>(A.k) + k0 * A.k_stride + h / A.G * D, A.k_stride,
+                     static_cast<const T*>(A.v) + k0 * A.v_stride + h / A.G * D, A.v_stride, n, A.qscale,
+                     static_cast<T*>(A.out) + row * A.out_stride + h * D);
 }
 
 }  // namespace
@@ -71,6 +46,7 @@ cudaError_t launch_prompt_attend(const PackedArgs& a, int D, int dtype, cudaStre
 {
     const long long warps = (long long)a.rows * a.heads * a.G;
     const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
+    if (dtype && a.k_rows) return launch_prompt_tc(a, D, st);
     if (dtype) {
         if (D == 64) prompt_rows_kernel<__nv_bfloat16, 64><<<grid, kWarps * 32, 0, st>>>(a);
         else prompt_rows_kernel<__nv_bfloat16, 128><<<grid, kWarps * 32, 0, st>>>(a);

@@ -1,0 +1,614 @@
+// prompt_attend_tc.cu -- causal attention over packed prompts on the
+// 5th-generation tensor cores (bf16).
+//
+// A work item is a pair of query tiles of one key head: np = 128 / groups
+// positions a tile, whose query heads lie side by side as np * groups rows.
+// Keys go in tiles of 128, and a CTA runs two score streams:
+//   S = Q K^T        (SMEM x SMEM -> TMEM, M = 128, K = D)
+//   P = 2^(c S - m)  (128 threads a stream, thread = TMEM lane = query row)
+//   O += P V         (TMEM x SMEM -> TMEM, M = 128, N = D)
+// one for each query tile over the same keys; where a request has queries for one tile only,
+// for the even and the odd key tiles of that one, joined at the end.  S and P go
+// by halves of 64 keys, so that neither the threads nor the products wait for
+// the other's latency.
+//
+// CTAs are persistent, one an SM: warp 3 finds the items (a request's longest
+// rows first), warp 0 loads queries, keys and values with TMA, warps 1 and 2
+// issue their stream's products, warps 4..7 and 8..11 are the streams' threads.
+// The next item's queries, keys and scores are under way while the last one's
+// rows leave.  A row's maximum m is raised, and O scaled, only when a logit
+// passes it by more than 2^8.  P is rounded to bf16 for the product, the sums
+// l are of the unrounded weights.
+//
+// Keys that a row does not see have the weight 0, which leaves a row as it is
+// unless their values are infinite or NaN: a row whose result is no number is
+// made again from the keys it sees alone (prompt_row).  Value rows behind a
+// request's last, which may be anything, are zeroed in shared memory.  Waits are
+// bounded; one that runs out leaves NaN.
+#include <algorithm>
+
+#include "paged.h"
+#include "prompt_rows.cuh"
+#include "tc.cuh"
+
+namespace h2o {
+
+namespace {
+
+constexpr int kT = 128;
+constexpr int kThreads = 384;
+constexpr uint32_t kBox = kT * 64 * 2;             // 128 rows x 64 channels: 16 KB
+constexpr float kRaise = 8.f;
+constexpr int kSteps = 2, kStep = kT / kSteps;     // S and P go by parts of a tile
+
+template <int D> struct Cfg {
+    static constexpr int kBoxes = D / 64;
+    static constexpr uint32_t kTile = kBoxes * kBox;
+    static constexpr int kSlots = D == 128 ? 5 : 8;    // K and V tiles in flight
+};
+
+// a pair of query tiles; n: key tiles; ring: tiles the ring has taken before
+struct Item {
+    int q0, nq, p, k0, nk, h, n, ring, stop;
+};
+
+template <int D>
+struct alignas(1024) Smem {
+    uint8_t q[2][Cfg<D>::kTile];
+    uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
+    uint64_t full[Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
+    uint64_t q_full, q_empty, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2][kSteps], o_free[2], last;   // [stream][part of the tile]
+    uint64_t item_full[2], item_empty[2], joined;
+    float2 ml[2][kT];
+    Item item[2];
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(Smem<128>) <= 227 * 1024, "one CTA's shared memory");
+
+// accumulator fp32, bf16 A and B, A K-major, B K-major or (bit 16) N-major
+template <int N, bool BMN>
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((BMN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kT >> 4) << 24);
+
+// The issuing warp runs its loop as a whole, so that descriptors stay in uniform registers, and one lane (`on`) issues.
+__device__ __forceinline__ uint32_t elect_lane()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(acc), "r"(on)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"(acc), "r"(on)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t on, uint64_t* bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(on)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// descriptor of the value tile as the K x N operand, N (channels) contiguous:
+// 64-channel boxes 16 KB apart (leading offset), 8 keys every 1024 B
+__device__ __forceinline__ uint64_t value_desc(const void* p)
+{
+    return (uint64_t)((smem_u32(p) & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// An item's tiles in the ring's order of use: K(0) .. K(L - 1), then V(t), K(t + L) for t = 0, 1, ..
+// (L = 1: both streams use each tile; 2: they take turns).  Both streams wait for each tile and give each back, so that
+// every barrier's phases are seen.  V(t)'s place:
+__device__ __forceinline__ int v_at(int t, int n, int L) { return t + min(n, t + L); }
+
+template <int D>
+__device__ __forceinline__ bool wait(Smem<D>& S, uint64_t* bar, int count)
+{
+    // the barrier's phase number `count` (from 0)
+    if (mbar_wait(bar, (uint32_t)count & 1u)) return true;
+    *(volatile int*)&S.abort = 1;
+    return false;
+}
+
+// The request of work index x, by the whole warp: the last i with f(i) = q_start[i] / pair + i <= x, or -1.  f's values
+// leave room for every pair of tiles of a request before the next one's: f(i + 1) - f(i) >= ceil(length / pair).
+__device__ __forceinline__ int request_at(const PackedArgs& A, int x, int pair)
+{
+    const int lane = threadIdx.x & 31;
+    auto f = [&](int i) { return min(max(A.q_start[i], 0), A.rows) / pair + i; };
+    int lo = 0, hi = A.requests;
+    if (f(0) > x) return -1;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const unsigned in = __ballot_sync(0xffffffffu, i < hi && f(i) <= x);
+        const int k = max(1, __ffs(~in) - 1);              // (all 32: ffs is 0)
+        lo += (in == 0xffffffffu ? 31 : k - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                     const PackedArgs A, const int np, const int works)
+{
+    using C = Cfg<D>;
+    constexpr int NS = C::kSlots;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (known to be uniform)
+    const int G = A.G;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&S.full[s], 1);
+            mbar_init(&S.empty[s], 2);
+        }
+        mbar_init(&S.q_full, 1);
+        mbar_init(&S.q_empty, 2);
+        for (int s = 0; s < 2; ++s) {
+            for (int b = 0; b < kSteps; ++b) {
+                mbar_init(&S.s_ready[s][b], 1);
+                mbar_init(&S.p_ready[s][b], 4);
+                mbar_init(&S.pv_done[s][b], 1);
+            }
+            mbar_init(&S.o_free[s], 4);
+            mbar_init(&S.item_full[s], 1);
+            mbar_init(&S.item_empty[s], 11);
+        }
+        mbar_init(&S.last, 2);
+        mbar_init(&S.joined, 8);
+        S.abort = (smem_u32(raw) & 1023u) != 0;          // (the swizzle goes by address bits; there is no other shared memory, so it is 0)
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&S.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    auto tS = [&](int s) { return tmem + (uint32_t)(s * kT); };
+    auto tO = [&](int s) { return tmem + (uint32_t)(2 * kT + s * D); };
+
+    // each role's walk through the items; false: no more
+    int nth_item = 0;
+    Item it;
+    auto next = [&]() {
+        const int k = nth_item++;
+        const bool ok = __all_sync(0xffffffffu, wait(S, &S.item_full[k & 1], k >> 1));
+        if (!ok) return false;
+        it = S.item[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.item_empty[k & 1]);
+        return it.stop == 0;
+    };
+    auto aborted = [&]() { return __any_sync(0xffffffffu, *(volatile int*)&S.abort != 0); };
+    // key tiles of stream s's rows, and how many keys those see
+    auto keys_of = [&](int s) {
+        const int end = min(it.nq, it.p + (it.p + np < it.nq ? s + 1 : 1) * np);
+        return max(0, min(it.nk, it.nk - it.nq + end));
+    };
+
+    if (warp == 3) {
+        // ------------------------------------------------ items
+        int ring = 0, put = 0;
+        const int pair = 2 * np;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            // in turn and back, so that each CTA gets its share of the long ones
+            const long long w = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if ((long long)k * gridDim.x >= works) break;
+            if (w >= works) continue;
+            const int x = works / A.heads - 1 - (int)(w / A.heads), i = request_at(A, x, pair);
+            if (i < 0) continue;
+            Item m;
+            m.q0 = A.q_start[i];
+            m.k0 = A.k_start[i];
+            const int q1 = A.q_start[i + 1], k1 = A.k_start[i + 1];
+            if (m.q0 < 0 || q1 <= m.q0 || q1 > A.rows || m.k0 < 0 || k1 < m.k0 || k1 > A.k_rows) continue;
+            m.nq = q1 - m.q0;
+            m.nk = k1 - m.k0;
+            const long long p = (long long)(x - (m.q0 / pair + i)) * pair;
+            if (p >= m.nq) continue;
+            m.p = (int)p;
+            m.h = (int)(w % A.heads);
+            const int seen = max(0, min(m.nk, m.nk - m.nq + min(m.nq, m.p + pair)));
+            m.n = (seen + kT - 1) / kT;
+            m.ring = ring;
+            m.stop = 0;
+            if (put >= 2) ok = __all_sync(0xffffffffu, wait(S, &S.item_empty[put & 1], put / 2 - 1));
+            if (!ok) break;
+            if (lane == 0) {
+                S.item[put & 1] = m;
+                mbar_arrive(&S.item_full[put & 1]);
+            }
+            __syncwarp();
+            ++put;
+            ring += 2 * m.n;
+        }
+        if (put >= 2) wait(S, &S.item_empty[put & 1], put / 2 - 1);
+        if (lane == 0) {
+            S.item[put & 1].stop = 1;
+            mbar_arrive(&S.item_full[put & 1]);
+        }
+    } else if (warp == 0) {
+        // ------------------------------------------------ loads
+        int at = 0, queries = 0;
+        bool ok = true;
+        const uint32_t q_bytes = (uint32_t)(np * G) * 128u * C::kBoxes;
+        while (next()) {
+            if (!ok || aborted() || it.n == 0) continue;
+            const bool two = it.p + np < it.nq;
+            const int L = two ? 1 : 2;
+            auto load = [&](const CUtensorMap* map, int t) {
+                if (!ok) return;
+                const int s = at % NS;
+                if (at >= NS) ok = __all_sync(0xffffffffu, wait(S, &S.empty[s], at / NS - 1));
+                if (!ok) return;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&S.full[s], C::kTile);
+#pragma unroll
+                    for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(S.ring[s] + b * kBox, map, b * 64, it.h, it.k0 + t * kT, &S.full[s]);
+                }
+                __syncwarp();
+                ++at;
+            };
+            if (queries) ok = __all_sync(0xffffffffu, wait(S, &S.q_empty, queries - 1));
+            if (!ok) continue;
+            ++queries;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&S.q_full, two ? 2 * q_bytes : q_bytes);
+                for (int s = 0; s < (two ? 2 : 1); ++s)
+#pragma unroll
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        tma_load_3d(S.q[s] + b * kBox, &mapQ, b * 64, it.h * G, it.q0 + it.p + s * np, &S.q_full);
+            }
+            __syncwarp();
+            for (int t = 0; t < min(L, it.n); ++t) load(&mapK, t);
+            for (int t = 0; t < it.n; ++t) {
+                load(&mapV, t);
+                if (t + L < it.n) load(&mapK, t + L);
+            }
+        }
+        // every load has landed before the shared memory is given up, those of an abandoned sweep too
+        if (queries) mbar_wait(&S.q_full, (uint32_t)(queries - 1) & 1u);
+        for (int s = 0; s < min(NS, at); ++s) mbar_wait(&S.full[s], (uint32_t)((at - 1 - s) / NS) & 1u);
+    } else if (warp <= 2) {
+        // ------------------------------------------------ products of stream s
+        const int s = warp - 1;
+        const uint32_t on = elect_lane();
+        const uint64_t k0 = sw128_desc(S.ring[0]), v0 = value_desc(S.ring[0]);
+        const uint32_t sS = tS(s), sO = tO(s);
+        bool ok = true;
+        int at = 0, queries = 0, tiles = 0, outs = 0;    // ring tiles, items, this stream's tiles and results so far
+        while (next()) {
+            if (!ok || aborted() || it.n == 0) continue;
+            const bool two = it.p + np < it.nq;
+            const uint64_t q0 = sw128_desc(S.q[two ? s : 0]);
+            const int L = two ? 1 : 2, keys = keys_of(s), n = (keys + kT - 1) / kT;
+            const int base = at;
+            at += 2 * it.n;
+            ok = __all_sync(0xffffffffu, wait(S, &S.q_full, queries));
+            ++queries;
+            auto slot_full = [&](int i) {
+                if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.full[i % NS], i / NS));
+            };
+            auto release = [&](int i) {                  // when all products so far are done
+                if (ok) commit(on, &S.empty[i % NS]);
+            };
+            // scores of part b of the tile in place i
+            auto score = [&](int b, int i) {
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t k = k0 + (uint64_t)((uint32_t)(i % NS) * (C::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint64_t off = (uint64_t)(((uint32_t)(x / 4) * kBox + (uint32_t)(x % 4) * 32u) >> 4);
+                    mma_ss(on, sS + (uint32_t)(kStep * b), q0 + off, k + off, kIdesc<kStep, false>, x > 0);
+                }
+                commit(on, &S.s_ready[s][b]);
+            };
+            // nth: tiles of this stream before in this item; valid: its keys of the tile
+            auto values = [&](int b, int nth, int i, int valid) {
+                if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.p_ready[s][b], tiles));
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t v = v0 + (uint64_t)((uint32_t)(i % NS) * (C::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
+                const int nk = (min(kStep, valid - kStep * b) + 15) / 16;
+                auto one = [&](int x) {
+                    mma_ts(on, sO, sS + (uint32_t)(kStep * b + 8 * x), v + (uint64_t)((uint32_t)x * 2048u >> 4), kIdesc<D, true>,
+                           nth > 0 || b > 0 || x > 0);
+                };
+                if (nk == kStep / 16) {
+#pragma unroll
+                    for (int x = 0; x < kStep / 16; ++x) one(x);
+                } else {
+                    for (int x = 0; x < nk; ++x) one(x);
+                }
+                commit(on, &S.pv_done[s][b]);
+            };
+            // where in the ring: K(t) and V(t)
+            auto k_place = [&](int t) { return base + (t < L ? t : v_at(t - L, it.n, L) + 1); };
+            auto v_place = [&](int t) { return base + v_at(t, it.n, L); };
+            // The tiles in the ring's order; those that are the other stream's, or whose keys no row of this one sees, go back at once.
+            auto mine = [&](int t) { return t < n && (two || (t & 1) == s); };
+            bool freed = false;                          // the last result has left O
+            for (int t = 0; t < min(L, it.n); ++t) {
+                slot_full(k_place(t));
+                if (mine(t))
+                    for (int b = 0; b < kSteps; ++b) score(b, k_place(t));
+                release(k_place(t));
+            }
+            if (it.n <= L && ok) commit(on, &S.q_empty);
+            int nth = 0;
+            for (int t = 0; t < it.n; ++t) {
+                const bool more = t + L < it.n;
+                const int v = v_place(t), k = v + 1;
+                slot_full(v);
+                if (more) slot_full(k);
+                const bool values_mine = mine(t), scores_mine = more && mine(t + L);
+                if (values_mine && !freed) {
+                    if (ok && outs) ok = __all_sync(0xffffffffu, wait(S, &S.o_free[s], outs - 1));
+                    freed = true;
+                    ++outs;
+                }
+                for (int b = 0; b < kSteps; ++b) {
+                    if (values_mine) values(b, nth, v, keys - t * kT);
+                    if (scores_mine) score(b, k);
+                }
+                release(v);
+                if (more) release(k);
+                if (t + L + 1 == it.n && ok) commit(on, &S.q_empty);   // the item's last scores
+                if (values_mine) { ++nth; ++tiles; }
+            }
+        }
+        // everything issued is done before TMEM is given back
+        commit(on, &S.last);
+        mbar_wait(&S.last, 0);
+    } else {
+        // ------------------------------------------------ softmax
+        const int s = (warp - 4) >> 2, w = warp & 3, row = w * 32 + lane;
+        const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        const float c2 = A.qscale;
+        const int prow = row / G, g = row - prow * G;    // position and head of the row within its tile
+        int tiles = 0, meets = 0;                        // of this stream so far
+        bool ok = true;
+        // all softmax warps, and what they have written
+        auto meet = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.joined);
+            if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.joined, meets));
+            ++meets;
+            tc_fence_after();
+        };
+        while (next()) {
+            const bool two = it.p + np < it.nq;
+            const int pos = it.p + (two ? s * np : 0) + prow;
+            const bool live = row < np * G && pos < it.nq;
+            const int sees = min(it.nk, it.nk - it.nq + pos + 1);    // keys of this row (not live: of no matter)
+            const int keys = keys_of(s), n = (keys + kT - 1) / kT, first = two ? 0 : s, stride = two ? 1 : 2;
+            const int nt = n > first ? (n - first + stride - 1) / stride : 0;    // this stream's tiles
+            float m = -INFINITY, l = 0.f;
+            if (ok && aborted()) ok = false;
+            for (int i = 0; i < kSteps * nt && ok; ++i) {
+                const int nth = i / kSteps, b = i % kSteps, t = first + nth * stride, j0 = t * kT + kStep * b;
+                const uint32_t at = tS(s) + lanes + (uint32_t)(kStep * b);
+                // (a part's last product is done before its new scores are made, so the second look never waits; it is there to
+                // see every phase)
+                ok = __all_sync(0xffffffffu, wait(S, &S.s_ready[s][b], tiles + nth) && (nth == 0 || wait(S, &S.pv_done[s][b], tiles + nth - 1)));
+                if (!ok) break;
+                tc_fence_after();
+                constexpr int NC = kStep / 32;
+                uint32_t z[NC][32];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tc_ld32_issue(at + 32u * c, z[c]);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tc_ld32_wait(z[c]);
+                const int valid = sees - j0;
+                if (__any_sync(0xffffffffu, valid < kStep)) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (c * 32 + k >= valid) z[c][k] = 0xff800000u;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    float mx[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t* y = z[c] + 16 * e;
+                        mx[e] = __uint_as_float(y[0]);
+#pragma unroll
+                        for (int k = 1; k < 15; k += 2) mx[e] = max3f(mx[e], __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+                        mx[e] = fmaxf(mx[e], __uint_as_float(y[15]));
+                    }
+                    top = max3f(top, mx[0], mx[1]);
+                }
+                top *= c2;
+                const bool raise = top > m + kRaise;                 // (m = -inf: any finite logit)
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float a = raise ? ex2_fast(m - top) : 1.f;
+                    if (raise) {
+                        m = top;
+                        l *= a;
+                    }
+                    if (i > 0) {
+                        // (all products but the last are done)
+                        ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][(i - 1) % kSteps], tiles + (i - 1) / kSteps));
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tc_ld16_issue(tO(s) + lanes + (uint32_t)c, o);
+                            tc_ld16_wait(o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                            tc_st16(tO(s) + lanes + (uint32_t)c, o);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                const float2 cc = make_float2(c2, c2), nb = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 e = __ffma2_rn(make_float2(__uint_as_float(z[c][2 * k]), __uint_as_float(z[c][2 * k + 1])), cc, nb);
+                        const float2 x = make_float2(ex2_fast(e.x), ex2_fast(e.y));
+                        sum[k & 1] = __fadd2_rn(sum[k & 1], x);
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[k]) : "f"(x.y), "f"(x.x));
+                    }
+                    tc_st16(at + 16u * c, p);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                // value rows behind the request's last key in its group of 16: zeros (both streams may write them, each before
+                // its own product)
+                const int left = it.nk - j0, end = (min(keys - j0, kStep) + 15) & ~15;
+                if (left < end && left > 0 && keys > j0) {
+                    const int v = it.ring + v_at(t, it.n, two ? 1 : 2);
+                    ok = __all_sync(0xffffffffu, wait(S, &S.full[v % NS], v / NS));
+                    if (!ok) break;
+                    for (int x = row; x < (end - left) * C::kBoxes * 8; x += kT)
+                        *reinterpret_cast<uint4*>(S.ring[v % NS] + (x >> 3) % C::kBoxes * kBox + (kStep * b + left + (x >> 3) / C::kBoxes) * 128 +
+                                                  (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                tc_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.p_ready[s][b]);
+            }
+            for (int b = 0; b < kSteps; ++b)
+                if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][b], tiles + nt - 1));
+            tc_fence_after();
+            tiles += nt;
+
+            // ------------------------------------------------ results
+            // One query tile: both streams' sums, half of the channels each.
+            float a0 = 1.f, a1 = 0.f;
+            if (!two) {
+                S.ml[s][row] = make_float2(m, l);
+                meet();
+                const float2 x = S.ml[0][row], y = S.ml[1][row];
+                const float mm = fmaxf(x.x, y.x), base = mm == -INFINITY ? 0.f : mm;
+                a0 = ex2_fast(x.x - base);
+                a1 = ex2_fast(y.x - base);
+                l = fmaf(x.y, a0, y.y * a1);
+                if (it.n == 1) a1 = 0.f;                 // (the odd stream's O is none of this item)
+            }
+            const bool fine = ok && !aborted();
+            const float f = l == 0.f ? 0.f : 1.f / l;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out) + (long long)(it.q0 + pos) * A.out_stride + (it.h * G + g) * D;
+            bool odd = false;
+            const int c0 = two ? 0 : s * (D / 2), c1 = two ? D : c0 + D / 2;
+#pragma unroll 1
+            for (int c = c0; c < c1; c += 32) {
+                uint32_t o[32];
+                tc_ld32_issue(tO(two ? s : 0) + lanes + (uint32_t)c, o);
+                tc_ld32_wait(o);
+                if (!two && it.n > 1) {
+                    uint32_t y[32];
+                    tc_ld32_issue(tO(1) + lanes + (uint32_t)c, y);
+                    tc_ld32_wait(y);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), a0, __uint_as_float(y[k]) * a1));
+                }
+                uint32_t r[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float x = l == 0.f ? 0.f : __uint_as_float(o[2 * k]) * f, y = l == 0.f ? 0.f : __uint_as_float(o[2 * k + 1]) * f;
+                    odd |= !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY);
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[k]) : "f"(y), "f"(x));
+                    if (!fine) r[k] = 0x7fff7fffu;
+                }
+                if (live)
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) *reinterpret_cast<uint4*>(out + c + 2 * k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+            }
+            tc_fence_before();
+            // the sums have been read: by the other stream's threads too
+            if (!two) meet();
+            __syncwarp();
+            if (lane == 0 && nt > 0) mbar_arrive(&S.o_free[s]);
+            // rows whose result is no number: what they do not see may have made it so
+            unsigned redo = __ballot_sync(0xffffffffu, live && odd && fine);
+            while (redo) {
+                const int r = __ffs(redo) - 1;
+                redo &= redo - 1;
+                const int rp = __shfl_sync(0xffffffffu, pos, r), rg = __shfl_sync(0xffffffffu, g, r), rn = __shfl_sync(0xffffffffu, sees, r);
+                const long long qrow = it.q0 + rp;
+                prompt_row<__nv_bfloat16, D>(static_cast<const __nv_bfloat16*>(A.q) + qrow * A.q_stride + (it.h * G + rg) * D,
+                                             static_cast<const __nv_bfloat16*>(A.k) + it.k0 * A.k_stride + it.h * D, A.k_stride,
+                                             static_cast<const __nv_bfloat16*>(A.v) + it.k0 * A.v_stride + it.h * D, A.v_stride, rn, c2,
+                                             static_cast<__nv_bfloat16*>(A.out) + qrow * A.out_stride + (it.h * G + rg) * D);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(S.tmem, 512);
+}
+
+// rows [n][heads][D] bf16, `stride` elements apart; boxes of 64 channels x bh heads x bn rows, 128-byte swizzle
+bool rows_map(CUtensorMap* m, const void* base, int D, int heads, int n, long long stride, int bh, int bn)
+{
+    EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)n};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)bh, (cuuint32_t)bn};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t go(const PackedArgs& a, cudaStream_t st)
+{
+    const int np = kT / a.G;
+    CUtensorMap mq, mk, mv;
+    if (!rows_map(&mq, a.q, D, a.heads * a.G, a.rows, a.q_stride, a.G, np) || !rows_map(&mk, a.k, D, a.heads, a.k_rows, a.k_stride, 1, kT) ||
+        !rows_map(&mv, a.v, D, a.heads, a.k_rows, a.v_stride, 1, kT))
+        return cudaErrorInvalidValue;
+    const int smem = (int)sizeof(Smem<D>);
+    static SmemOnce once;
+    const cudaError_t e = once.allow(prompt_tc_kernel<D>);
+    if (e != cudaSuccess) return e;
+    const long long works = ((long long)a.rows / (2 * np) + a.requests) * a.heads;
+    if (works > INT32_MAX) return cudaErrorInvalidValue;
+    prompt_tc_kernel<D><<<(unsigned)std::min<long long>(works, kSMs), kThreads, smem, st>>>(mq, mk, mv, a, np, (int)works);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_tc(const PackedArgs& a, int D, cudaStream_t st) { return D == 64 ? go<64>(a, st) : go<128>(a, st); }
+
+}  // namespace h2o

@@ -7,6 +7,7 @@
 namespace h2o {
 
 constexpr int kMaxPromptRequests = 16384;   // requests of one h2o_prompt_attend call
+constexpr int kMaxPromptRows = 1 << 24;     // its query rows and its key rows (one query tile's keys take less than a wait's limit)
 
 struct RopeArgs {
     const void* in[2];             // q, k: [rows][heads][D], rows `stride` elements apart
@@ -42,6 +43,7 @@ struct QuantPool {
 
 cudaError_t launch_rope(const RopeArgs& a, int form, int D, int dtype, cudaStream_t st);
 cudaError_t launch_prompt_attend(const PackedArgs& a, int D, int dtype, cudaStream_t st);
+cudaError_t launch_prompt_tc(const PackedArgs& a, int D, cudaStream_t st);   // bf16, at least one key row
 cudaError_t launch_page_quant_write(const QuantPool& p, const void* k, const void* v, long long k_stride, long long v_stride,
                                     const int* slot, int rows, cudaStream_t st);
 cudaError_t launch_page_quant_read(const QuantPool& p, const int* slot, int rows, void* k, long long k_stride, void* v,
