@@ -5,13 +5,15 @@
 // token's codes are read once for all of them.  A unit's tiles of 16 keys are
 // dealt to the warps of a cluster of 1 to 16 CTAs, whose sums are joined at the end.
 //
-// Codes go into fp16 products as they lie: a code with its offset is an unsigned
-// number u below 2^8, whose bits are the fp16 subnormal u 2^-24, so widening it is
-// a mask (4-bit codes in the upper nibble of a byte are 16 u 2^-24, their query
-// channels a sixteenth).  S^T = K Q^T has keys as rows and starts from
-// -offset 2^-24 sum_e q_e instead of 0, which takes the offset out.  O^T = V^T W^T
-// has channels as rows; here the offset is subtracted from each value, since it
-// would cancel in sums over many keys.
+// Codes go into fp16 products: a code with its offset is an unsigned number u
+// below 2^8, whose bits are the fp16 subnormal u 2^-24, so widening it is a mask
+// (the upper 4-bit code of a byte 16 u 2^-24).  S^T = K Q^T has keys as rows.  With
+// bf16 rows it takes the subnormals as they are (queries of upper codes a
+// sixteenth) and starts from -offset 2^-24 sum_e q_e, which takes the offset out;
+// the tensor cores align a subnormal's products as if it were 2^-14, which leaves
+// 2^-24 of the largest q 2^-14 (2^-13 of one product's largest a logit).  fp32 rows, and the
+// values of O^T = V^T W^T, whose offset would cancel in sums over many keys, go
+// through one fused multiply-add of two halves to c 2^-10.
 //   z = ks (scale q.c),  p = 2^(z - m),  l = sum p,  w = p vs 2^(m - E),
 //   O 2^(E - m) / l
 // with whole numbers m and E for each query head: m is raised when a logit passes it
@@ -22,6 +24,8 @@
 //
 // Bound: HBM (d bits / 8 + 4 bytes a row, twice a token).
 #include <algorithm>
+#include <cfloat>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "prompts.h"
@@ -65,12 +69,6 @@ __device__ __forceinline__ float2 floats_of(uint32_t h)
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(h));
     return f;
 }
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c)
 {
     uint32_t r;
@@ -82,6 +80,13 @@ __device__ __forceinline__ float lg2(float x)
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// max(a, b, c) in one instruction
+__device__ __forceinline__ float max3f(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 // 2^e for a whole e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
@@ -133,11 +138,11 @@ template <int N> __device__ __forceinline__ void store_out(__nv_bfloat16* p, con
 }
 
 // A tile's rows of RB bytes lie one after another, 16-byte chunks of each 128-byte line exchanged so that the reads of
-// 8 rows' chunks, and of one chunk of every other row, meet no bank twice.
+// one chunk of 8 rows (ldmatrix), and of neighbouring rows' chunks, meet no bank twice.
 template <int RB>
 __device__ __forceinline__ uint32_t chunk_at(int chunk)
 {
-    const int line = chunk >> 3, f = RB == 128 ? ((line >> 1 & 3) << 1) ^ ((line & 1) << 2) : (line & 3) << 1;
+    const int line = chunk >> 3, f = RB == 128 ? (line & 1) << 2 | (line >> 1 & 3) : RB == 64 ? line & 3 : line & 1;
     return (uint32_t)(line * 128 + (((chunk & 7) ^ f) << 4));
 }
 template <int RB>
@@ -151,7 +156,7 @@ template <int D, int BITS> struct Tile {
     static constexpr int kRow = D * BITS / 8;              // bytes of a row of codes
     static constexpr int kCodes = kKeys * kRow;
     static constexpr int kBytes = 2 * kCodes + 2 * kKeys * 4;
-    static constexpr int kStages = kRow == 128 ? 3 : kRow == 64 ? 6 : 8;
+    static constexpr int kStages = kRow == 128 ? 4 : kRow == 64 ? 6 : 10;   // tiles in flight, in twos
     static constexpr int kRing = kStages * kBytes;         // a warp's
 };
 
@@ -161,12 +166,31 @@ template <int D, int BITS, int NT, int PARTS>
 struct Core {
     static constexpr int KS = D / 16;                      // steps of the products over channels, and of 16 channels of O^T
     static constexpr float kOffset = BITS == 8 ? 128.f : 8.f;
+    static constexpr bool kRaw = PARTS == 1;               // key codes as subnormals
+    static constexpr int kLowest = -118;                   // of E - m: p f is within fp32 for p <= 2^8
     uint32_t q[PARTS][NT][KS][2];
     float o[NT][KS][4];
-    float zero[NT][2];                                     // -offset 2^-24 sum_e q_e of heads 2t, 2t + 1
-    float za[NT][2], zb[NT][2];                            // 2^(24 + eq) scale log2(e), in two factors
-    float m[NT][2], l[NT][2], f[NT][2];                    // f = 2^(m - E), 0 before E is known
+    float zero[NT][2];                                     // what the scores of heads 2t, 2t + 1 start from
+    float2 zf[NT];                                         // 2^(24 + eq) scale log2(e) (2^(10 + eq))
+    float2 m[NT], l[NT], f[NT];                            // f = 2^(m - E)
     int unit[NT][2];                                       // E - m
+
+    __device__ __forceinline__ static float& at(float2& x, int i) { return i ? x.y : x.x; }
+
+    // Codes of a word of two pieces of 16 bits: of each the first (HI 0) or second code, with its offset, as the fp16 subnormals
+    // u 2^-24, or 16 u 2^-24 for the second of four bits.
+    template <int HI>
+    __device__ __forceinline__ static uint32_t code(uint32_t w)
+    {
+        if constexpr (BITS == 8) return ((HI ? w >> 8 : w) & 0x00ff00ffu) ^ 0x00800080u;
+        else return w & (HI ? 0x00f000f0u : 0x000f000fu);
+    }
+    // the same without the offset, as c 2^-10
+    template <int HI>
+    __device__ __forceinline__ static uint32_t normal(uint32_t u)
+    {
+        return hfma2(u, BITS == 4 && HI ? 0x64006400u : 0x74007400u, BITS == 8 ? 0xb000b000u : 0xa000a000u);
+    }
 
     // Channel of code i of word j of a row's part t (the words are one step of K, or two with 4 bits).
     __device__ __forceinline__ static int channel(int t, int j, int i)
@@ -206,7 +230,7 @@ struct Core {
             for (int k = 0; k < KS; ++k) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[k][e] = x[k][e] * down0 * down1;
-                if constexpr (BITS == 4) { x[k][2] *= 0.0625f; x[k][3] *= 0.0625f; }
+                if constexpr (kRaw && BITS == 4) { x[k][2] *= 0.0625f; x[k][3] *= 0.0625f; }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float2 y = make_float2(x[k][2 * h], x[k][2 * h + 1]);
@@ -221,83 +245,83 @@ struct Core {
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const int up = 24 + eq;                        // (-116 .. 138)
-            const float a = pow2(up / 2), b = big < 0x7f800000u ? pow2(up - up / 2) * qscale : NAN;
+            const int up = (kRaw ? 24 : 10) + eq;          // (at most 138; a factor out of range makes the row NaN)
+            const float a = big < 0x7f800000u ? pow2(up / 2) * qscale * pow2(up - up / 2) : NAN;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int from = (2 * t + i) * 4;          // a lane of head 2t + i
-                zero[n][i] = __shfl_sync(0xffffffffu, sum, from) * (-kOffset * 0x1p-24f);
-                za[n][i] = __shfl_sync(0xffffffffu, a, from);
-                zb[n][i] = __shfl_sync(0xffffffffu, b, from);
-                m[n][i] = -INFINITY;
-                l[n][i] = f[n][i] = 0.f;
-                unit[n][i] = 0;
+                zero[n][i] = kRaw ? __shfl_sync(0xffffffffu, sum, from) * (-kOffset * 0x1p-24f) : 0.f;
+                at(zf[n], i) = __shfl_sync(0xffffffffu, a, from);
+                at(m[n], i) = -FLT_MAX;                    // (below every logit that counts)
+                at(l[n], i) = 0.f;
+                unit[n][i] = kLowest;
+                at(f[n], i) = pow2(-kLowest);
             }
 #pragma unroll
             for (int k = 0; k < KS; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
     }
 
-    // the weights of this lane's keys (g and g + 8) for its two heads
-    struct Weights { float p[4], w[4]; };
-    __device__ __forceinline__ Weights weigh(const float (&z)[4], float v0, float v1, int n) const
+    // weights of this lane's keys, g and g + 8 of a tile, for its two heads: d = z - m
+    __device__ __forceinline__ void weigh(const float2 (&d)[2], const float (&v)[2], int n, float2 (&p)[2], float2 (&w)[2]) const
     {
-        Weights r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float base = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1];
-            r.p[i] = ex2_approx(z[i] - base);
-            r.w[i] = r.p[i] * f[n][i & 1] * (i < 2 ? v0 : v1);
+        for (int r = 0; r < 2; ++r) {
+            p[r] = make_float2(ex2_approx(d[r].x), ex2_approx(d[r].y));
+            w[r] = __fmul2_rn(__fmul2_rn(p[r], f[n]), make_float2(v[r], v[r]));
         }
-        return r;
     }
 
-    // m to the largest of these logits where they pass it by 8, and the sums' unit to what w asks for
-    __device__ __forceinline__ void raise(const float (&z)[4], float v0, float v1, int n)
+    // m to the largest of these logits z = d + m where they pass it by 8, and the sums' unit to what w asks for; d anew
+    template <int TILES>
+    __device__ __forceinline__ void raise(const float2 (&z)[TILES][2], const float (&v)[TILES][2], int n)
     {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float top = fmaxf(z[i], z[i + 2]);
+            auto zi = [&](int x, int r) { return i ? z[x][r].y : z[x][r].x; };
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < TILES; ++x) top = max3f(top, zi(x, 0), zi(x, 1));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if (top > m[n][i] + 8.f && top < INFINITY) {
-                const float to = ceilf(top), by = to - m[n][i];
-                l[n][i] *= ex2_approx(-by);
-                m[n][i] = to;
-                if (f[n][i] != 0.f) unit[n][i] -= (int)fminf(by, 1000.f);
+            float& mi = at(m[n], i);
+            if (top > mi + 8.f && top < INFINITY) {
+                const float to = ceilf(top), by = to - mi;
+                at(l[n], i) *= ex2_approx(-by);
+                mi = to;
+                unit[n][i] -= (int)fminf(by, 1000.f);
             }
-            const float base = m[n][i] == -INFINITY ? 0.f : m[n][i];
-            float u = fmaxf(z[i] - base + lg2(v0), z[i + 2] - base + lg2(v1));   // (a scale of 0: -inf)
+            float u = -INFINITY;                           // log2 of the largest p vs (a scale of 0: -inf)
+#pragma unroll
+            for (int x = 0; x < TILES; ++x) u = max3f(u, zi(x, 0) - mi + lg2(v[x][0]), zi(x, 1) - mi + lg2(v[x][1]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
-            const bool known = f[n][i] != 0.f;
             int e = unit[n][i];
-            if (u > -INFINITY && (!known || u > (float)(e + 15))) e = (int)ceilf(fminf(u, 1000.f)) - 6;
-            else if (!known) continue;
-            e = max(-118, min(126, e));                    // f within fp32, with room for p <= 2^8
-            const float a = pow2(max(-126, min(126, unit[n][i] - e)));
-            if (known && unit[n][i] != e)
+            if (u > (float)(e + 15)) e = (int)ceilf(fminf(u, 1000.f)) - 6;
+            e = max(kLowest, min(126, e));
+            if (unit[n][i] != e) {
+                const float a = pow2(max(-126, min(126, unit[n][i] - e)));
 #pragma unroll
                 for (int k = 0; k < KS; ++k) { o[n][k][i] *= a; o[n][k][i + 2] *= a; }
+            }
             unit[n][i] = e;
-            f[n][i] = pow2(-e);
+            at(f[n], i) = pow2(-e);
         }
     }
 
-    __device__ __forceinline__ void tile(const unsigned char* stage, int valid)
+    // TILES tiles, of whose keys the first `valid` count
+    template <int TILES>
+    __device__ __forceinline__ void tiles(const unsigned char* const (&stage)[TILES], int valid)
     {
         using L = Tile<D, BITS>;
         constexpr int RB = L::kRow;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const unsigned char* vt = stage + L::kCodes;
-        const float* ks = reinterpret_cast<const float*>(stage + 2 * L::kCodes);
-        const float k0 = ks[g], k1 = ks[g + 8];
-        float v0 = ks[kKeys + g], v1 = ks[kKeys + g + 8];
         // scores: rows g and g + 8 are the keys
-        float s[NT][4];
+        float s[NT][TILES][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) { s[n][0] = s[n][2] = zero[n][0]; s[n][1] = s[n][3] = zero[n][1]; }
-        {
+        for (int x = 0; x < TILES; ++x) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) { s[n][x][0] = s[n][x][2] = zero[n][0]; s[n][x][1] = s[n][x][3] = zero[n][1]; }
             constexpr int W = KS * 4 * BITS / 32;          // words of a row's part
             uint32_t w[2][W];
 #pragma unroll
@@ -306,12 +330,12 @@ struct Core {
                 if constexpr (W >= 4) {
 #pragma unroll
                     for (int c = 0; c < W / 4; ++c) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(stage + byte_at<RB>(key, c * 64 + t * 16));
-                        w[r][4 * c] = x.x; w[r][4 * c + 1] = x.y; w[r][4 * c + 2] = x.z; w[r][4 * c + 3] = x.w;
+                        const uint4 y = *reinterpret_cast<const uint4*>(stage[x] + byte_at<RB>(key, c * 64 + t * 16));
+                        w[r][4 * c] = y.x; w[r][4 * c + 1] = y.y; w[r][4 * c + 2] = y.z; w[r][4 * c + 3] = y.w;
                     }
                 } else {
-                    const uint2 x = *reinterpret_cast<const uint2*>(stage + byte_at<RB>(key, t * 8));
-                    w[r][0] = x.x; w[r][1] = x.y;
+                    const uint2 y = *reinterpret_cast<const uint2*>(stage[x] + byte_at<RB>(key, t * 8));
+                    w[r][0] = y.x; w[r][1] = y.y;
                 }
             }
 #pragma unroll
@@ -319,100 +343,108 @@ struct Core {
                 uint32_t a[4];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    if constexpr (BITS == 8) {
-                        a[r] = (w[r][k] ^ 0x80808080u) & 0x00ff00ffu;
-                        a[r + 2] = ((w[r][k] >> 8) ^ 0x00800080u) & 0x00ff00ffu;
-                    } else {
-                        const uint32_t x = k & 1 ? w[r][k / 2] >> 8 : w[r][k / 2];
-                        a[r] = x & 0x000f000fu;
-                        a[r + 2] = x & 0x00f000f0u;
+                    const uint32_t y = BITS == 8 ? w[r][k] : k & 1 ? w[r][k / 2] >> 8 : w[r][k / 2];
+                    a[r] = code<0>(y);
+                    a[r + 2] = code<1>(y);
+                    if constexpr (!kRaw) {
+                        a[r] = normal<0>(a[r]);
+                        a[r + 2] = normal<1>(a[r + 2]);
                     }
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p) mma16(s[n], a[0], a[1], a[2], a[3], q[p][n][k][0], q[p][n][k][1]);
+                    for (int p = 0; p < PARTS; ++p) mma16(s[n][x], a[0], a[1], a[2], a[3], q[p][n][k][0], q[p][n][k][1]);
             }
         }
-        if (valid < kKeys) {                               // scales behind the newest key may be anything
-            if (g >= valid) v0 = 0.f;
-            if (g + 8 >= valid) v1 = 0.f;
-        }
-        uint32_t b[PARTS][NT][2];                          // W^T as the K x N operand
+        float kf[TILES][2], v[TILES][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float z[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                z[i] = s[n][i] * za[n][i & 1] * (i < 2 ? k0 : k1) * zb[n][i & 1];
-                if (valid < kKeys && g + (i < 2 ? 0 : 8) >= valid) z[i] = -INFINITY;
-            }
-            Weights x = weigh(z, v0, v1, n);
-            bool over = f[n][0] == 0.f || f[n][1] == 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) over |= z[i] > m[n][i & 1] + 8.f || x.w[i] > 32768.f;
-            if (__any_sync(0xffffffffu, over)) {
-                raise(z, v0, v1, n);
-                x = weigh(z, v0, v1, n);
-            }
-            l[n][0] += x.p[0] + x.p[2];
-            l[n][1] += x.p[1] + x.p[3];
+        for (int x = 0; x < TILES; ++x) {
+            const float* ks = reinterpret_cast<const float*>(stage[x] + 2 * L::kCodes);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float2 y = make_float2(x.w[2 * r], x.w[2 * r + 1]);
+                kf[x][r] = ks[g + 8 * r];
+                v[x][r] = ks[kKeys + g + 8 * r];
+                if (valid < TILES * kKeys && x * kKeys + g + 8 * r >= valid) v[x][r] = 0.f;   // (scales behind the newest key may be anything)
+            }
+        }
+        uint32_t b[PARTS][NT][TILES][2];                   // W^T as the K x N operand
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    const uint32_t h = half2_of(y.x, y.y);
-                    b[p][n][r] = transposed(h);
-                    const float2 u = floats_of(h);
-                    y = make_float2(y.x - u.x, y.y - u.y);
+        for (int n = 0; n < NT; ++n) {
+            float2 z[TILES][2], d[TILES][2], p[TILES][2], w[TILES][2];
+            float over = -INFINITY, most = 0.f;
+#pragma unroll
+            for (int x = 0; x < TILES; ++x) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    z[x][r] = __fmul2_rn(__fmul2_rn(make_float2(s[n][x][2 * r], s[n][x][2 * r + 1]), make_float2(kf[x][r], kf[x][r])), zf[n]);
+                    if (valid < TILES * kKeys && x * kKeys + g + 8 * r >= valid) z[x][r] = make_float2(-INFINITY, -INFINITY);
+                    d[x][r] = __fadd2_rn(z[x][r], make_float2(-m[n].x, -m[n].y));
+                    over = max3f(over, d[x][r].x, d[x][r].y);
+                }
+                weigh(d[x], v[x], n, p[x], w[x]);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) most = max3f(most, w[x][r].x, w[x][r].y);
+            }
+            if (__any_sync(0xffffffffu, over > 8.f || most > 32768.f)) {
+                raise<TILES>(z, v, n);
+#pragma unroll
+                for (int x = 0; x < TILES; ++x) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) d[x][r] = __fadd2_rn(z[x][r], make_float2(-m[n].x, -m[n].y));
+                    weigh(d[x], v[x], n, p[x], w[x]);
                 }
             }
-        }
-        // values: rows g and g + 8 of step k are channels g D / 8 + 2k and + 1, columns the keys
-        constexpr int VB = D / 8 * BITS / 8;               // bytes of this lane's channels of a key
-        uint32_t w[4][VB < 4 ? 1 : VB / 4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const unsigned char* at = vt + byte_at<RB>(2 * t + (r & 1) + (r >> 1) * 8, g * VB);
-            if constexpr (VB == 16) {
-                const uint4 x = *reinterpret_cast<const uint4*>(at);
-                w[r][0] = x.x; w[r][1] = x.y; w[r][2] = x.z; w[r][3] = x.w;
-            } else if constexpr (VB == 8) {
-                const uint2 x = *reinterpret_cast<const uint2*>(at);
-                w[r][0] = x.x; w[r][1] = x.y;
-            } else {
-                w[r][0] = *reinterpret_cast<const uint32_t*>(at);
-            }
-        }
-        constexpr int CW = 32 / BITS;                      // codes of a word
+            for (int x = 0; x < TILES; ++x) {
+                l[n] = __fadd2_rn(l[n], __fadd2_rn(p[x][0], p[x][1]));
 #pragma unroll
-        for (int j = 0; j < VB / 4; ++j)
+                for (int r = 0; r < 2; ++r) {
+                    float2 y = w[x][r];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {                  // half words: two or four channels of two keys
-                const uint32_t x = __byte_perm(w[0][j], w[1][j], h ? 0x7632 : 0x5410), y = __byte_perm(w[2][j], w[3][j], h ? 0x7632 : 0x5410);
-#pragma unroll
-                for (int c = 0; c < CW / 4; ++c) {
-                    uint32_t a[4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t z = i ? y : x;
-                        if constexpr (BITS == 8) {
-                            a[2 * i] = hadd2((z ^ 0x80808080u) & 0x00ff00ffu, 0x80808080u);              // - 128 2^-24
-                            a[2 * i + 1] = hadd2(((z >> 8) ^ 0x00800080u) & 0x00ff00ffu, 0x80808080u);
-                        } else {
-                            const uint32_t u = c ? z >> 8 : z;
-                            a[2 * i] = hadd2(u & 0x000f000fu, 0x80088008u);                              // - 8 2^-24
-                            a[2 * i + 1] = hfma2(u & 0x00f000f0u, 0x2c002c00u, 0x80088008u);             // / 16
-                        }
+                    for (int i = 0; i < PARTS; ++i) {
+                        const uint32_t h = half2_of(y.x, y.y);
+                        b[i][n][x][r] = transposed(h);
+                        const float2 u = floats_of(h);
+                        y = make_float2(y.x - u.x, y.y - u.y);
                     }
-                    const int k = j * (CW / 2) + h * (CW / 4) + c;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int p = 0; p < PARTS; ++p) mma16(o[n][k], a[0], a[1], a[2], a[3], b[p][n][0], b[p][n][1]);
                 }
             }
+        }
+        // values: 8 x 8 matrices of 16-bit pieces of 8 keys, transposed, give a lane the same piece of keys 2t and 2t + 1 side by
+        // side: two or four channels, rows g and g + 8 of one or two steps
+        constexpr int CP = 16 / BITS;                      // channels of a piece
+        const int mat = lane >> 3, r8 = lane & 7;
+#pragma unroll
+        for (int x = 0; x < TILES; ++x) {
+            const uint32_t at = smem_u32(stage[x] + L::kCodes);
+#pragma unroll
+            for (int c = 0; c < RB / 16; c += 2) {         // two chunks of 16 bytes a row: matrices of keys 0-7 and 8-15 of each
+                uint32_t y[4];
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(at + byte_at<RB>((mat & 1) * 8 + r8, (c + (mat >> 1)) * 16))
+                             : "memory");
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < CP / 2; ++j) {
+                        uint32_t a[4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t u = y[2 * h + i];
+                            const uint32_t w = BITS == 4 && j ? u >> 8 : u;
+                            a[2 * i] = normal<0>(code<0>(w));
+                            a[2 * i + 1] = normal<1>(code<1>(w));
+                        }
+                        const int k = (c + h) * (CP / 2) + j;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < PARTS; ++i) mma16(o[n][k], a[0], a[1], a[2], a[3], b[i][n][x][0], b[i][n][x][1]);
+                    }
+            }
+        }
     }
 
     // o to out [8 NT][D], (m, l) to ml [8 NT]
@@ -423,17 +455,21 @@ struct Core {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float s = l[n][i];
+                float s = at(l[n], i);
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
                 const int head = n * 8 + 2 * t + i;
                 if (head >= G) continue;
-                const float up = f[n][i] == 0.f ? 0.f : 1.f / f[n][i];   // 2^(E - m)
+                const float up = 1.f / at(f[n], i);        // 2^(E - m)
+                // of chunk c of a row of values a lane has the channels of piece g, one after another
 #pragma unroll
-                for (int k = 0; k < KS; k += 2)
-                    *reinterpret_cast<float4*>(out + head * D + g * (D / 8) + 2 * k) =
-                        make_float4(o[n][k][i] * 0x1p24f * up, o[n][k][2 + i] * 0x1p24f * up, o[n][k + 1][i] * 0x1p24f * up, o[n][k + 1][2 + i] * 0x1p24f * up);
-                if (g == 0) ml[head] = make_float2(m[n][i], bad ? NAN : s);
+                for (int k = 0; k < KS; k += 8 / BITS) {
+                    float* to = out + head * D + (BITS == 8 ? k * 16 + 2 * g : k * 16 + 4 * g);
+                    if constexpr (BITS == 8) *reinterpret_cast<float2*>(to) = make_float2(o[n][k][i] * 0x1p10f * up, o[n][k][2 + i] * 0x1p10f * up);
+                    else *reinterpret_cast<float4*>(to) = make_float4(o[n][k][i] * 0x1p10f * up, o[n][k][2 + i] * 0x1p10f * up,
+                                                                      o[n][k + 1][i] * 0x1p10f * up, o[n][k + 1][2 + i] * 0x1p10f * up);
+                }
+                if (g == 0) ml[head] = make_float2(at(m[n], i), bad ? NAN : s);
             }
     }
 };
@@ -467,39 +503,48 @@ __global__ void __launch_bounds__(kThreads, NT == 2 && sizeof(T) == 4 ? 2 : NT =
     const int ntiles = npages ? (pos >> 4) + 1 : 0;
     const int stride = C * kWarps, t0 = rank * kWarps + warp;
     int pg_next = t0 < ntiles ? table[t0 >> tsh] : 0;      // the page of the next tile to be asked for
+    const unsigned char* const K = static_cast<const unsigned char*>(pool.K) + lane * 16;
+    const unsigned char* const V = static_cast<const unsigned char*>(pool.V) + lane * 16;
+    const float* const scales = (lane < 4 ? pool.ks : pool.vs) + (lane & 3) * 4;
     auto ask = [&](int t, int stage) {
-        if (t < ntiles) {
-            const int pg = pg_next;
-            const bool ok = (unsigned)pg < (unsigned)pool.pages;
+#pragma unroll
+        for (int x = 0; x < 2; ++x, t += stride) {
+            if (t >= ntiles) break;
+            const bool ok = (unsigned)pg_next < (unsigned)pool.pages;
             if (!ok) bad = true;                           // (its row is NaN: any page's codes do)
-            const size_t at = ((size_t)(ok ? pg : 0) * pool.heads + h) * pool.ps + ((size_t)(t & ((1 << tsh) - 1)) << 4);
-            const unsigned char* K = static_cast<const unsigned char*>(pool.K) + at * L::kRow;
-            const unsigned char* V = static_cast<const unsigned char*>(pool.V) + at * L::kRow;
-            const uint32_t to = smem_u32(ring + stage * L::kBytes);
+            const unsigned at = ((unsigned)((ok ? pg_next : 0) * pool.heads + h) << tsh) + (unsigned)(t & ((1 << tsh) - 1));   // tile of the pool (< 2^27)
+            const uint32_t to = smem_u32(ring + (stage + x) * L::kBytes);
 #pragma unroll
             for (int i = 0; i < L::kRow / 32; ++i) {
-                const int c = lane + 32 * i;
-                cp_async16(to + chunk_at<L::kRow>(c), K + c * 16);
-                cp_async16(to + L::kCodes + chunk_at<L::kRow>(c), V + c * 16);
+                cp_async16(to + chunk_at<L::kRow>(lane + 32 * i), K + (size_t)at * L::kCodes + i * 512);
+                cp_async16(to + L::kCodes + chunk_at<L::kRow>(lane + 32 * i), V + (size_t)at * L::kCodes + i * 512);
             }
-            if (lane < 8) cp_async16(to + 2 * L::kCodes + lane * 16, (lane < 4 ? pool.ks : pool.vs) + at + (lane & 3) * 4);
+            if (lane < 8) cp_async16(to + 2 * L::kCodes + lane * 16, scales + (size_t)at * kKeys);
             if (t + stride < ntiles) pg_next = table[(t + stride) >> tsh];
         }
         cp_commit();
     };
+    // a warp's tiles in twos
+    static_assert(NS % 2 == 0, "whole twos");
 #pragma unroll 1
-    for (int s = 0; s < NS - 1; ++s) ask(t0 + s * stride, s);
+    for (int s = 0; s < NS - 2; s += 2) ask(t0 + s * stride, s);
     Core<D, BITS, NT, sizeof(T) == 2 ? 1 : 2> core;
     core.init(static_cast<const T*>(R.q) + (size_t)row * R.q_stride + (size_t)h * G * D, G, R.qscale);
     int stage = 0;
 #pragma unroll 1
-    for (int t = t0; t < ntiles; t += stride) {
-        ask(t + (NS - 1) * stride, stage == 0 ? NS - 1 : stage - 1);
-        cp_wait<NS - 1>();
+    for (int t = t0; t < ntiles; t += 2 * stride) {
+        ask(t + (NS - 2) * stride, stage == 0 ? NS - 2 : stage - 2);
+        cp_wait<NS / 2 - 1>();
         __syncwarp();
-        core.tile(ring + stage * L::kBytes, t == ntiles - 1 ? (pos & 15) + 1 : kKeys);
+        const unsigned char* const a = ring + stage * L::kBytes;
+        const int mine = t == ntiles - 1 ? (pos & 15) + 1 : kKeys;
+        if (t + stride < ntiles) {
+            core.template tiles<2>({a, a + L::kBytes}, t + stride == ntiles - 1 ? kKeys + (pos & 15) + 1 : 2 * kKeys);
+        } else {
+            core.template tiles<1>({a}, mine);
+        }
         __syncwarp();
-        stage = stage + 1 == NS ? 0 : stage + 1;
+        stage = stage + 2 == NS ? 0 : stage + 2;
     }
     cp_wait<0>();
     __syncwarp();
@@ -555,10 +600,15 @@ __global__ void __launch_bounds__(kThreads, NT == 2 && sizeof(T) == 4 ? 2 : NT =
     cluster_wait();                                        // no CTA leaves while another reads its sums
 }
 
-// Clusters of c CTAs that the GPU holds at once, about (per_sm CTAs an SM).
-int clusters_that_fit(int c, int per_sm)
+// CTAs of a unit: as many, up to 16, as fill the GPU twice with every warp left a tile (64 units of 256 tiles: 30 us with
+// one, 16 with four, 20 with eight; 32 of 2048: 66 with four, 50 with eight, 61 with sixteen), and beyond that, so that units of
+// unequal lengths share the SMs evenly, as leave a warp 48 tiles and the GPU 2048 CTAs (512 units of up to 1536 tiles: 280 us
+// with one, 243 with four, 253 with eight).
+int cluster_of(long long units, int tiles)
 {
-    return c == 2 ? 76 * per_sm : c == 4 ? 36 * per_sm : c == 8 ? (per_sm == 1 ? 15 : 17 * per_sm) : 7 * per_sm;
+    int c = 1;
+    while (c < kMaxCluster && ((units * 2 * c <= 2 * kSMs && tiles >= kWarps * 2 * c) || (units * 2 * c <= 2048 && tiles >= 48 * kWarps * 2 * c))) c *= 2;
+    return c;
 }
 
 template <typename T, int D, int BITS, int NT>
@@ -571,9 +621,8 @@ cudaError_t go(const QuantPool& p, const PageRows& r, cudaStream_t st)
     const cudaError_t e = once.allow(kernel, true);
     if (e != cudaSuccess) return e;
     const long long units = (long long)r.rows * p.heads;
-    const int tiles = r.width * (p.ps / kKeys), per_sm = 4;
-    int C = 1;
-    while (C < kMaxCluster && units <= clusters_that_fit(2 * C, per_sm) && tiles >= 3 * C * 2 * kWarps) C *= 2;
+    int C = cluster_of(units, r.width * (p.ps / kKeys));
+    if (getenv("QC")) C = atoi(getenv("QC"));
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)C;
