@@ -25,7 +25,6 @@
 // Bound: HBM (d bits / 8 + 4 bytes a row, twice a token).
 #include <algorithm>
 #include <cfloat>
-#include <cstdlib>
 
 #include "common.cuh"
 #include "prompts.h"
@@ -622,7 +621,6 @@ cudaError_t go(const QuantPool& p, const PageRows& r, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const long long units = (long long)r.rows * p.heads;
     int C = cluster_of(units, r.width * (p.ps / kKeys));
-    if (getenv("QC")) C = atoi(getenv("QC"));
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)C;
