@@ -39,17 +39,22 @@ constexpr int kT = 128;
 constexpr int kThreads = 384;
 constexpr uint32_t kBox = kT * 64 * 2;             // 128 rows x 64 channels: 16 KB
 constexpr float kRaise = 8.f;
+constexpr int kMaxCluster = 16;
 constexpr int kSteps = 2, kStep = kT / kSteps;     // S and P go by parts of a tile
 
 template <int D> struct Cfg {
     static constexpr int kBoxes = D / 64;
     static constexpr uint32_t kTile = kBoxes * kBox;
     static constexpr int kSlots = D == 128 ? 5 : 8;    // K and V tiles in flight
+    static constexpr int kPitch = D * 4 + 16;          // of a row of sums (16 bytes more: no bank conflicts)
+    static_assert(2 * kT * kPitch <= (2 + kSlots) * (int)kTile, "the queries' and keys' place holds them");
 };
 
-// a pair of query tiles; n: key tiles; ring: tiles the ring has taken before
+// A pair of query tiles: the request's first query row, its queries, the pair's first position; the first key row of
+// this CTA's range, the request's keys before it and those of it; n: key tiles of the range; ring: tiles the ring has
+// taken before; all: the request's keys.
 struct Item {
-    int q0, nq, p, k0, nk, h, n, ring, stop;
+    int q0, nq, p, k0, before, nk, h, n, ring, all, stop;
 };
 
 template <int D>
@@ -62,7 +67,7 @@ struct alignas(1024) Smem {
     float2 ml[2][kT];
     Item item[2];
     uint32_t tmem;
-    int abort;
+    int abort, any;                    // any: there was an item
 };
 static_assert(sizeof(Smem<128>) <= 227 * 1024, "one CTA's shared memory");
 
@@ -97,6 +102,21 @@ __device__ __forceinline__ void commit(uint32_t on, uint64_t* bar)
                  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(on)
                  : "memory");
 }
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+template <int N> __device__ __forceinline__ void ld_cluster_f(uint32_t addr, float* x)
+{
+    if constexpr (N == 4) {
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(addr) : "memory");
+    } else {
+        const float2 w = ld_cluster_f2(addr);
+        x[0] = w.x; x[1] = w.y;
+    }
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
 {
     asm volatile(
@@ -127,31 +147,14 @@ __device__ __forceinline__ bool wait(Smem<D>& S, uint64_t* bar, int count)
     return false;
 }
 
-// The request of work index x, by the whole warp: the last i with f(i) = q_start[i] / pair + i <= x, or -1.  f's values
-// leave room for every pair of tiles of a request before the next one's: f(i + 1) - f(i) >= ceil(length / pair).
-__device__ __forceinline__ int request_at(const PackedArgs& A, int x, int pair)
-{
-    const int lane = threadIdx.x & 31;
-    auto f = [&](int i) { return min(max(A.q_start[i], 0), A.rows) / pair + i; };
-    int lo = 0, hi = A.requests;
-    if (f(0) > x) return -1;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-        const unsigned in = __ballot_sync(0xffffffffu, i < hi && f(i) <= x);
-        const int k = max(1, __ffs(~in) - 1);              // (all 32: ffs is 0)
-        lo += (in == 0xffffffffu ? 31 : k - 1) * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
-
-template <int D>
+// SPLIT: a cluster takes one item, its CTAs ranges of the item's keys, and their sums are joined at the end.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                      const PackedArgs A, const int np, const int works)
 {
-    using C = Cfg<D>;
-    constexpr int NS = C::kSlots;
+    using C_ = Cfg<D>;
+    constexpr int NS = C_::kSlots;
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (known to be uniform)
@@ -206,8 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // key tiles of stream s's rows, and how many keys those see
     auto keys_of = [&](int s) {
         const int end = min(it.nq, it.p + (it.p + np < it.nq ? s + 1 : 1) * np);
-        return max(0, min(it.nk, it.nk - it.nq + end));
+        return max(0, min(it.nk, it.all - it.nq + end - it.before));
     };
+    const int C = SPLIT ? (int)cluster_nctarank() : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
 
     if (warp == 3) {
         // ------------------------------------------------ items
@@ -216,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int k = 0; ok; ++k) {
             // in turn and back, so that each CTA gets its share of the long ones
-            const long long w = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if ((long long)k * gridDim.x >= works) break;
+            const long long w = SPLIT ? blockIdx.x / C : (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (SPLIT ? k > 0 : (long long)k * gridDim.x >= works) break;
             if (w >= works) continue;
             const int x = works / A.heads - 1 - (int)(w / A.heads), i = request_at(A, x, pair);
             if (i < 0) continue;
@@ -227,13 +231,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int q1 = A.q_start[i + 1], k1 = A.k_start[i + 1];
             if (m.q0 < 0 || q1 <= m.q0 || q1 > A.rows || m.k0 < 0 || k1 < m.k0 || k1 > A.k_rows) continue;
             m.nq = q1 - m.q0;
-            m.nk = k1 - m.k0;
+            m.all = k1 - m.k0;
             const long long p = (long long)(x - (m.q0 / pair + i)) * pair;
             if (p >= m.nq) continue;
             m.p = (int)p;
             m.h = (int)(w % A.heads);
-            const int seen = max(0, min(m.nk, m.nk - m.nq + min(m.nq, m.p + pair)));
-            m.n = (seen + kT - 1) / kT;
+            const int seen = max(0, min(m.all, m.all - m.nq + min(m.nq, m.p + pair))), tiles = (seen + kT - 1) / kT;
+            const int t0 = SPLIT ? (int)((long long)tiles * rank / C) : 0;
+            m.n = (SPLIT ? (int)((long long)tiles * (rank + 1) / C) : tiles) - t0;
+            m.before = t0 * kT;
+            m.k0 += m.before;
+            m.nk = max(0, min(m.all - m.before, m.n * kT));
             m.ring = ring;
             m.stop = 0;
             if (put >= 2) ok = __all_sync(0xffffffffu, wait(S, &S.item_empty[put & 1], put / 2 - 1));
@@ -248,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (put >= 2) wait(S, &S.item_empty[put & 1], put / 2 - 1);
         if (lane == 0) {
+            S.any = put > 0;
             S.item[put & 1].stop = 1;
             mbar_arrive(&S.item_full[put & 1]);
         }
@@ -255,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ loads
         int at = 0, queries = 0;
         bool ok = true;
-        const uint32_t q_bytes = (uint32_t)(np * G) * 128u * C::kBoxes;
+        const uint32_t q_bytes = (uint32_t)(np * G) * 128u * C_::kBoxes;
         while (next()) {
             if (!ok || aborted() || it.n == 0) continue;
             const bool two = it.p + np < it.nq;
@@ -266,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (at >= NS) ok = __all_sync(0xffffffffu, wait(S, &S.empty[s], at / NS - 1));
                 if (!ok) return;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&S.full[s], C::kTile);
+                    mbar_arrive_expect_tx(&S.full[s], C_::kTile);
 #pragma unroll
-                    for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(S.ring[s] + b * kBox, map, b * 64, it.h, it.k0 + t * kT, &S.full[s]);
+                    for (int b = 0; b < C_::kBoxes; ++b) tma_load_3d(S.ring[s] + b * kBox, map, b * 64, it.h, it.k0 + t * kT, &S.full[s]);
                 }
                 __syncwarp();
                 ++at;
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(&S.q_full, two ? 2 * q_bytes : q_bytes);
                 for (int s = 0; s < (two ? 2 : 1); ++s)
 #pragma unroll
-                    for (int b = 0; b < C::kBoxes; ++b)
+                    for (int b = 0; b < C_::kBoxes; ++b)
                         tma_load_3d(S.q[s] + b * kBox, &mapQ, b * 64, it.h * G, it.q0 + it.p + s * np, &S.q_full);
             }
             __syncwarp();
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto score = [&](int b, int i) {
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t k = k0 + (uint64_t)((uint32_t)(i % NS) * (C::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
+                const uint64_t k = k0 + (uint64_t)((uint32_t)(i % NS) * (C_::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const uint64_t off = (uint64_t)(((uint32_t)(x / 4) * kBox + (uint32_t)(x % 4) * 32u) >> 4);
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.p_ready[s][b], tiles));
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t v = v0 + (uint64_t)((uint32_t)(i % NS) * (C::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
+                const uint64_t v = v0 + (uint64_t)((uint32_t)(i % NS) * (C_::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
                 const int nk = (min(kStep, valid - kStep * b) + 15) / 16;
                 auto one = [&](int x) {
                     mma_ts(on, sO, sS + (uint32_t)(kStep * b + 8 * x), v + (uint64_t)((uint32_t)x * 2048u >> 4), kIdesc<D, true>,
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool two = it.p + np < it.nq;
             const int pos = it.p + (two ? s * np : 0) + prow;
             const bool live = row < np * G && pos < it.nq;
-            const int sees = min(it.nk, it.nk - it.nq + pos + 1);    // keys of this row (not live: of no matter)
+            const int sees = min(it.nk, it.all - it.nq + pos + 1 - it.before);    // keys of this row in the range (not live: of no matter)
             const int keys = keys_of(s), n = (keys + kT - 1) / kT, first = two ? 0 : s, stride = two ? 1 : 2;
             const int nt = n > first ? (n - first + stride - 1) / stride : 0;    // this stream's tiles
             float m = -INFINITY, l = 0.f;
@@ -489,13 +498,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 // value rows behind the request's last key in its group of 16: zeros (both streams may write them, each before
                 // its own product)
-                const int left = it.nk - j0, end = (min(keys - j0, kStep) + 15) & ~15;
+                const int left = it.all - it.before - j0, end = (min(keys - j0, kStep) + 15) & ~15;
                 if (left < end && left > 0 && keys > j0) {
                     const int v = it.ring + v_at(t, it.n, two ? 1 : 2);
                     ok = __all_sync(0xffffffffu, wait(S, &S.full[v % NS], v / NS));
                     if (!ok) break;
-                    for (int x = row; x < (end - left) * C::kBoxes * 8; x += kT)
-                        *reinterpret_cast<uint4*>(S.ring[v % NS] + (x >> 3) % C::kBoxes * kBox + (kStep * b + left + (x >> 3) / C::kBoxes) * 128 +
+                    for (int x = row; x < (end - left) * C_::kBoxes * 8; x += kT)
+                        *reinterpret_cast<uint4*>(S.ring[v % NS] + (x >> 3) % C_::kBoxes * kBox + (kStep * b + left + (x >> 3) / C_::kBoxes) * 128 +
                                                   (x & 7) * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
@@ -512,6 +521,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------ results
             // One query tile: both streams' sums, half of the channels each.
             float a0 = 1.f, a1 = 0.f;
+            if constexpr (SPLIT) {
+                // both streams are through (each has seen its last product's end, and all tiles have been waited for), so the
+                // queries' and keys' place is free
+                meet();
+                S.ml[s][row] = make_float2(m, !ok || aborted() ? NAN : nt > 0 ? l : -1.f);
+                float* mine = reinterpret_cast<float*>(S.q[0] + (s * kT + row) * C_::kPitch);
+                if (nt > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc_ld32_issue(tO(s) + lanes + (uint32_t)c, o);
+                        tc_ld32_wait(o);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) *reinterpret_cast<uint4*>(mine + c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    }
+                }
+                tc_fence_before();
+                continue;
+            }
             if (!two) {
                 S.ml[s][row] = make_float2(m, l);
                 meet();
@@ -574,6 +602,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(S.tmem, 512);
+    if constexpr (SPLIT) {
+        // the cluster's sums, a warp a row: of both streams where they had one tile's keys in turn
+        cluster_arrive();
+        cluster_wait();
+        if (S.any) {
+            const Item it = S.item[0];
+            const bool two = it.p + np < it.nq;
+            const int rows = min(it.nq - it.p, 2 * np) * G;
+            constexpr int V4 = D / 32;
+#pragma unroll 1
+            for (int x = rank * (kThreads / 32) + warp; x < rows; x += C * (kThreads / 32)) {
+                const int s = x / (np * G), r = x - s * np * G, pos = it.p + x / G, g = x % G;
+                float m = -INFINITY, l = 0.f, o[V4] = {};
+#pragma unroll 1
+                for (int c = 0; c < (two ? 1 : 2) * C; ++c) {
+                    const int from = two ? c : c >> 1, st = two ? s : c & 1;
+                    const float2 y = ld_cluster_f2(map_to_rank(&S.ml[st][r], from));
+                    if (y.y < 0.f) continue;                     // no keys, and no sums
+                    float v[V4];
+                    ld_cluster_f<V4>(map_to_rank(S.q[0] + (st * kT + r) * C_::kPitch, from) + lane * V4 * 4, v);
+                    const float mn = fmaxf(m, y.x), base = mn == -INFINITY ? 0.f : mn, a = ex2_fast(m - base), b = ex2_fast(y.x - base);
+                    m = mn;
+                    l = fmaf(l, a, y.y * b);
+#pragma unroll
+                    for (int e = 0; e < V4; ++e) o[e] = fmaf(o[e], a, v[e] * b);
+                }
+                const float f = 1.f / l;
+                bool odd = false;
+#pragma unroll
+                for (int e = 0; e < V4; ++e) {
+                    o[e] = l == 0.f ? 0.f : o[e] * f;
+                    odd |= !(fabsf(o[e]) < INFINITY);
+                }
+                const long long qrow = it.q0 + pos, k0 = it.k0 - it.before;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out) + qrow * A.out_stride + (it.h * G + g) * D;
+                if (__any_sync(0xffffffffu, odd) && l == l) {
+                    // no number, though the weights are: what the row does not see may have made it so
+                    prompt_row<__nv_bfloat16, D>(static_cast<const __nv_bfloat16*>(A.q) + qrow * A.q_stride + (it.h * G + g) * D,
+                                                 static_cast<const __nv_bfloat16*>(A.k) + k0 * A.k_stride + it.h * D, A.k_stride,
+                                                 static_cast<const __nv_bfloat16*>(A.v) + k0 * A.v_stride + it.h * D, A.v_stride,
+                                                 min(it.all, it.all - it.nq + pos + 1), A.qscale, out);
+                    continue;
+                }
+                uint32_t w[V4 / 2];
+#pragma unroll
+                for (int i = 0; i < V4 / 2; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(o[2 * i + 1]), "f"(o[2 * i]));
+                if constexpr (V4 == 4) *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<uint32_t*>(out + lane * 2) = w[0];
+            }
+        }
+        cluster_arrive();
+        cluster_wait();                                    // no CTA leaves while another reads its sums
+    }
 }
 
 // rows [n][heads][D] bf16, `stride` elements apart; boxes of 64 channels x bh heads x bn rows, 128-byte swizzle
@@ -598,12 +679,35 @@ cudaError_t go(const PackedArgs& a, cudaStream_t st)
         !rows_map(&mv, a.v, D, a.heads, a.k_rows, a.v_stride, 1, kT))
         return cudaErrorInvalidValue;
     const int smem = (int)sizeof(Smem<D>);
-    static SmemOnce once;
-    const cudaError_t e = once.allow(prompt_tc_kernel<D>);
-    if (e != cudaSuccess) return e;
     const long long works = ((long long)a.rows / (2 * np) + a.requests) * a.heads;
-    if (works > INT32_MAX) return cudaErrorInvalidValue;
-    prompt_tc_kernel<D><<<(unsigned)std::min<long long>(works, kSMs), kThreads, smem, st>>>(mq, mk, mv, a, np, (int)works);
+    // Where there are fewer items than SMs, a cluster of CTAs for each, with at least four key tiles a CTA.
+    const long long items = (long long)a.heads * a.requests * (((long long)a.rows / a.requests + 2 * np - 1) / (2 * np) + (a.rows < a.requests));
+    int C = 1;
+    while (C < kMaxCluster && items * 2 * C <= kSMs && (long long)a.k_rows / a.requests >= 4 * kT * 2 * C) C *= 2;
+    if (works * C > INT32_MAX) return cudaErrorInvalidValue;
+    if (C > 1) {
+        const auto kernel = prompt_tc_kernel<D, true>;
+        static SmemOnce once;
+        const cudaError_t e = once.allow(kernel, true);
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)C;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(works * C));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, np, (int)works);
+    }
+    const auto kernel = prompt_tc_kernel<D, false>;
+    static SmemOnce once;
+    const cudaError_t e = once.allow(kernel);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)std::min<long long>(works, kSMs), kThreads, smem, st>>>(mq, mk, mv, a, np, (int)works);
     return cudaGetLastError();
 }
 

@@ -1,5 +1,6 @@
-// prompt_rows.cuh -- one query row of a prompt's attention by one warp on the
-// CUDA cores: what the tiled kernels leave to it, and what they are not for.
+// prompt_rows.cuh -- what the tiled kernels of prompt attention share: one query
+// row by one warp on the CUDA cores, which they leave some rows to, and the
+// request of a tile.
 #pragma once
 
 #include "common.cuh"
@@ -38,6 +39,25 @@ __device__ __noinline__ void prompt_row(const T* q, const T* k, long long kstrid
         if constexpr (sizeof(T) == 2) out[lane * E + e] = __float2bfloat16_rn(r);
         else out[lane * E + e] = r;
     }
+}
+
+// The request of work index x, by the whole warp: the last i with f(i) = q_start[i] / per + i <= x, or -1.  f's values
+// leave room for every tile of `per` positions of a request before the next one's, f(i + 1) - f(i) >= ceil(length / per),
+// so x - f(i) is the tile of request i if it has as many, and all requests' tiles are within rows / per + requests.
+__device__ __forceinline__ int request_at(const PackedArgs& A, int x, int per)
+{
+    const int lane = threadIdx.x & 31;
+    auto f = [&](int i) { return min(max(A.q_start[i], 0), A.rows) / per + i; };
+    int lo = 0, hi = A.requests;
+    if (f(0) > x) return -1;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const unsigned in = __ballot_sync(0xffffffffu, i < hi && f(i) <= x);
+        const int k = in == 0xffffffffu ? 32 : max(1, __ffs(~in) - 1);
+        lo += (k - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
 }
 
 }  // namespace h2o
