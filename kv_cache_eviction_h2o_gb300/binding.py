@@ -392,15 +392,18 @@ def h2o_prompt_scores_noalloc(Q, K, batch, heads, T, head_dim, dtype, scale, c, 
 # the cheapest comparisons there are; what is wrong is found out afterwards.
 
 _CODES = {"torch.bfloat16": H2O_BF16, "torch.float32": H2O_F32}
-_types = None          # (int32, uint8, {element type: its code}, the current device's index, its current stream, {code type: its flag}, float32, int64)
+_types = None          # (int32, uint8, {element type: its code}, the current device's index, its current stream, {code type: its flag}, float32, int64,
+                       # the handle of a device's current stream)
 
 
 def _torch_types():
     global _types
     if _types is None:
         import torch
+        # (a stream object takes 3 us to make, its handle alone 0.1)
+        handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
         _types = (torch.int32, torch.uint8, {getattr(torch, k[6:]): v for k, v in _CODES.items()}, torch.cuda.current_device,
-                  torch.cuda.current_stream, {torch.int8: H2O_KV8, torch.uint8: H2O_KV4}, torch.float32, torch.int64)
+                  torch.cuda.current_stream, {torch.int8: H2O_KV8, torch.uint8: H2O_KV4}, torch.float32, torch.int64, handle)
     return _types
 
 
@@ -441,11 +444,11 @@ def _head_rows(x, what, dtype, shape, device):
     """Pointer and row stride of [rows][heads][channels] whose rows may lie apart."""
     try:
         if x.dtype is dtype and x.shape == shape and x.get_device() == device:
-            rows, heads, d = shape
             s = x.stride()
-            if s[2] != 1 or (heads > 1 and s[1] != d):
-                raise ValueError("%s must have contiguous heads and channels" % what)
-            return x.data_ptr(), s[0] if rows > 1 else heads * d
+            rows, heads, d = shape
+            if s[2] == 1 and (s[1] == d or heads <= 1):
+                return x.data_ptr(), s[0] if rows > 1 else heads * d
+            raise ValueError("%s must have contiguous heads and channels" % what)
     except AttributeError:
         pass
     _wrong(x, what, dtype, shape, device)
@@ -453,18 +456,22 @@ def _head_rows(x, what, dtype, shape, device):
 
 def _dim(x, what, rank):
     """x's shape, which has `rank` dimensions."""
-    shape = getattr(x, "shape", None)
-    if shape is None or not hasattr(x, "data_ptr"):
-        raise TypeError("%s must be a tensor" % what)
+    try:
+        x.data_ptr
+        shape = x.shape
+    except AttributeError:
+        raise TypeError("%s must be a tensor" % what) from None
     if len(shape) != rank:
         raise ValueError("%s must have %d dimensions (got %s)" % (what, rank, list(shape)))
     return shape
 
 
 def _count(x, what):
-    if not hasattr(x, "data_ptr"):
-        raise TypeError("%s must be a tensor" % what)
-    return x.numel()
+    try:
+        x.data_ptr
+        return x.numel()
+    except AttributeError:
+        raise TypeError("%s must be a tensor" % what) from None
 
 
 def _on_current(x, current):
@@ -480,6 +487,11 @@ def _on_current(x, current):
 def _on_stream(stream):
     """The stream's handle; None: torch's current one, as for any other work on tensors."""
     return _stream(_types[4]() if stream is None else stream)
+
+
+def _on_handle(stream, device):
+    """The same, without making a stream object."""
+    return _types[8](device) if stream is None else _stream(stream)
 
 
 def _pool(K, V):
@@ -594,10 +606,11 @@ def h2o_rope_table(rot_dim, base=10000.0, kind=H2O_ROPE_PLAIN, factor=1.0, origi
 
 def _rows_type(x, what):
     """(element type, its code) of rows."""
-    code = _torch_types()[2].get(getattr(x, "dtype", None))
-    if code is None:
-        raise TypeError("%s must be a tensor of dtype float32 or bfloat16 (got %s)" % (what, getattr(x, "dtype", type(x))))
-    return x.dtype, code
+    try:
+        dt = x.dtype
+        return dt, (_types or _torch_types())[2][dt]
+    except (AttributeError, KeyError):
+        raise TypeError("%s must be a tensor of dtype float32 or bfloat16 (got %s)" % (what, getattr(x, "dtype", type(x)))) from None
 
 
 def h2o_rope(q, k, row_pos, table, form, amplitude, q_out, k_out, stream=None):
@@ -622,7 +635,7 @@ def h2o_rope(q, k, row_pos, table, form, amplitude, q_out, k_out, stream=None):
         raise ValueError("k_out without k")
     half = _count(table, "table")
     rc = lib().h2o_rope(qp, qs, op, os_, heads, kp, ks, kop, kos, kv_heads, _array(row_pos, "row_pos", types[0], rows, dev), rows,
-                        _array(table, "table", types[7], half, dev), 2 * half, form, amplitude, d, code, _on_stream(stream))
+                        _array(table, "table", types[7], half, dev), 2 * half, form, amplitude, d, code, _on_handle(stream, dev))
     if rc:
         _check(rc)
 
@@ -647,7 +660,7 @@ def h2o_prompt_attend(q, k, v, q_start, k_start, scale, out, stream=None):
     n = _count(q_start, "q_start")
     rc = lib().h2o_prompt_attend(qp, qs, rows, kp, ks, vp, vs, krows, heads, hq // heads, d, code, _array(q_start, "q_start", types[0], n, dev),
                                  None if k_start is None else _array(k_start, "k_start", types[0], n, dev), n - 1, scale, op, os_,
-                                 _on_stream(stream))
+                                 _on_handle(stream, dev))
     if rc:
         _check(rc)
 
@@ -680,7 +693,7 @@ def h2o_page_quant_write(k, v, slot, K, V, kscale, vscale, stream=None):
     kp, ks = _head_rows(k, "k", dt, shape, dev)
     vp, vs = _head_rows(v, "v", dt, shape, dev)
     rc = lib().h2o_page_quant_write(kp, vp, ks, vs, _array(slot, "slot", _types[0], rows, dev), rows, *pool, pages, heads, ps, d, code | flag,
-                                    _on_stream(stream))
+                                    _on_handle(stream, dev))
     if rc:
         _check(rc)
 
@@ -695,7 +708,7 @@ def h2o_page_quant_read(K, V, kscale, vscale, slot, k, v, stream=None):
     kp, ks = _head_rows(k, "k", dt, shape, dev)
     vp, vs = _head_rows(v, "v", dt, shape, dev)
     rc = lib().h2o_page_quant_read(*pool, pages, heads, ps, d, code | flag, _array(slot, "slot", _types[0], rows, dev), rows, kp, ks, vp, vs,
-                                   _on_stream(stream))
+                                   _on_handle(stream, dev))
     if rc:
         _check(rc)
 
@@ -706,6 +719,6 @@ def h2o_page_quant_attend(q, row_seq, row_pos, K, V, kscale, vscale, table, scal
     dt, code = _rows_type(q, "q")
     qp, qs, sp, pp, rows, groups, tp, n, width, op, os_ = _query_rows(q, row_seq, row_pos, table, out, dev, dt, heads, d)
     rc = lib().h2o_page_quant_attend(qp, qs, sp, pp, rows, *pool, pages, heads, groups, ps, d, code | flag, tp, n, width, scale, op, os_,
-                                     _on_stream(stream))
+                                     _on_handle(stream, dev))
     if rc:
         _check(rc)
