@@ -40,12 +40,12 @@ constexpr int kThreads = 384;
 constexpr uint32_t kBox = kT * 64 * 2;             // 128 rows x 64 channels: 16 KB
 constexpr float kRaise = 8.f;
 constexpr int kMaxCluster = 16;
-constexpr int kSteps = 2, kStep = kT / kSteps;     // S and P go by parts of a tile
+constexpr int kSteps = 2, kStep = kT / kSteps;     // S and P go by two parts of a tile
 
 template <int D> struct Cfg {
     static constexpr int kBoxes = D / 64;
     static constexpr uint32_t kTile = kBoxes * kBox;
-    static constexpr int kSlots = D == 128 ? 5 : 8;    // K and V tiles in flight
+    static constexpr int kSlots = D == 128 ? 4 : 6;    // K and V tiles in flight
     static constexpr int kPitch = D * 4 + 16;          // of a row of sums (16 bytes more: no bank conflicts)
     static_assert(2 * kT * kPitch <= (2 + kSlots) * (int)kTile, "the queries' and keys' place holds them");
 };
@@ -61,9 +61,11 @@ template <int D>
 struct alignas(1024) Smem {
     uint8_t q[2][Cfg<D>::kTile];
     uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
+    uint8_t out[8][32 * 128];          // of each softmax warp: 64 channels of its rows on their way out
     uint64_t full[Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
     uint64_t q_full, q_empty, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2][kSteps], o_free[2], last;   // [stream][part of the tile]
-    uint64_t item_full[2], item_empty[2], joined;
+    uint64_t item_full[2], item_empty[2], joined, taken;
+    alignas(16) uint4 taken_at;
     float2 ml[2][kT];
     Item item[2];
     uint32_t tmem;
@@ -117,6 +119,29 @@ template <int N> __device__ __forceinline__ void ld_cluster_f(uint32_t addr, flo
         x[0] = w.x; x[1] = w.y;
     }
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)) : "memory");
+}
+// Ask for the block index of a CTA of this grid that has not started, which then never does; 16 bytes to dst.
+__device__ __forceinline__ void take_cta(void* dst, uint64_t* bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(dst)), "r"(smem_u32(bar)) : "memory");
+}
+// What take_cta left: its index (x), or -1 when none was left.
+__device__ __forceinline__ int taken_cta(const void* src)
+{
+    unsigned long long lo, hi;
+    uint32_t ok, x;
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(lo), "=l"(hi) : "r"(smem_u32(src)) : "memory");
+    asm volatile("{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tmov.b128 r, {%2, %3};\n\tmov.u32 %1, 0;\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+                 : "=r"(ok), "=r"(x)
+                 : "l"(lo), "l"(hi)
+                 : "memory");
+    return ok ? (int)x : -1;
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
 {
     asm volatile(
@@ -151,7 +176,7 @@ __device__ __forceinline__ bool wait(Smem<D>& S, uint64_t* bar, int count)
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                     const PackedArgs A, const int np, const int works)
+                     const __grid_constant__ CUtensorMap mapO, const PackedArgs A, const int np, const int boxes, const int works)
 {
     using C_ = Cfg<D>;
     constexpr int NS = C_::kSlots;
@@ -179,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&S.last, 2);
         mbar_init(&S.joined, 8);
+        mbar_init(&S.taken, 1);
         S.abort = (smem_u32(raw) & 1023u) != 0;          // (the swizzle goes by address bits; there is no other shared memory, so it is 0)
         fence_mbar_init();
     }
@@ -215,15 +241,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 3) {
         // ------------------------------------------------ items
+        // This CTA's own, then those of CTAs that have not started, one ahead of what the others work on, so that each CTA takes
+        // what its time allows (8 x 2048 tokens of 8 x 4 heads: dealt out in turn and back, the longest share was a fifth above the mean).
         int ring = 0, put = 0;
         const int pair = 2 * np;
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-            // in turn and back, so that each CTA gets its share of the long ones
-            const long long w = SPLIT ? blockIdx.x / C : (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if (SPLIT ? k > 0 : (long long)k * gridDim.x >= works) break;
-            if (w >= works) continue;
-            const int x = works / A.heads - 1 - (int)(w / A.heads), i = request_at(A, x, pair);
+        int w = SPLIT ? blockIdx.x / C : blockIdx.x;
+        for (int k = 0; ok && w >= 0; ++k) {
+            if (k > 0) {
+                if (SPLIT) break;
+                if (put > 0) ok = __all_sync(0xffffffffu, wait(S, &S.item_empty[(put - 1) & 1], (put - 1) / 2));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&S.taken, 16);
+                    take_cta(&S.taken_at, &S.taken);
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, wait(S, &S.taken, k - 1));
+                if (!ok) break;
+                w = taken_cta(&S.taken_at);
+                fence_proxy_async_smem();                  // (read before it is written again)
+                __syncwarp();
+                if (w < 0) break;
+            }
+            const int x = works / A.heads - 1 - w / A.heads, i = request_at(A, x, pair);
             if (i < 0) continue;
             Item m;
             m.q0 = A.q_start[i];
@@ -235,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long p = (long long)(x - (m.q0 / pair + i)) * pair;
             if (p >= m.nq) continue;
             m.p = (int)p;
-            m.h = (int)(w % A.heads);
+            m.h = w % A.heads;
             const int seen = max(0, min(m.all, m.all - m.nq + min(m.nq, m.p + pair))), tiles = (seen + kT - 1) / kT;
             const int t0 = SPLIT ? (int)((long long)tiles * rank / C) : 0;
             m.n = (SPLIT ? (int)((long long)tiles * (rank + 1) / C) : tiles) - t0;
@@ -244,9 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m.nk = max(0, min(m.all - m.before, m.n * kT));
             m.ring = ring;
             m.stop = 0;
-            if (put >= 2) ok = __all_sync(0xffffffffu, wait(S, &S.item_empty[put & 1], put / 2 - 1));
-            if (!ok) break;
-            if (lane == 0) {
+            if (lane == 0) {                               // (the one before the last in this place has been taken by all)
                 S.item[put & 1] = m;
                 mbar_arrive(&S.item_full[put & 1]);
             }
@@ -254,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++put;
             ring += 2 * m.n;
         }
-        if (put >= 2) wait(S, &S.item_empty[put & 1], put / 2 - 1);
+        if (put > 0) wait(S, &S.item_empty[(put - 1) & 1], (put - 1) / 2);
         if (lane == 0) {
             S.any = put > 0;
             S.item[put & 1].stop = 1;
@@ -309,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t k0 = sw128_desc(S.ring[0]), v0 = value_desc(S.ring[0]);
         const uint32_t sS = tS(s), sO = tO(s);
         bool ok = true;
-        int at = 0, queries = 0, tiles = 0, outs = 0;    // ring tiles, items, this stream's tiles and results so far
+        int at = 0, queries = 0, outs = 0, part0 = 0, part1 = 0;   // ring tiles, items, results, first and second parts of tiles of this stream so far
         while (next()) {
             if (!ok || aborted() || it.n == 0) continue;
             const bool two = it.p + np < it.nq;
@@ -325,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto release = [&](int i) {                  // when all products so far are done
                 if (ok) commit(on, &S.empty[i % NS]);
             };
-            // scores of part b of the tile in place i
-            auto score = [&](int b, int i) {
-                if (!ok) return;
+            // scores of part b of the tile in place i, of which `valid` keys are seen
+            auto score = [&](int b, int i, int valid) {
+                if (!ok || valid <= kStep * b) return;
                 tc_fence_after();
                 const uint64_t k = k0 + (uint64_t)((uint32_t)(i % NS) * (C_::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
 #pragma unroll
@@ -339,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // nth: tiles of this stream before in this item; valid: its keys of the tile
             auto values = [&](int b, int nth, int i, int valid) {
-                if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.p_ready[s][b], tiles));
+                if (!ok || valid <= kStep * b) return;
+                ok = __all_sync(0xffffffffu, wait(S, &S.p_ready[s][b], b ? part1++ : part0++));
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t v = v0 + (uint64_t)((uint32_t)(i % NS) * (C_::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
@@ -365,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < min(L, it.n); ++t) {
                 slot_full(k_place(t));
                 if (mine(t))
-                    for (int b = 0; b < kSteps; ++b) score(b, k_place(t));
+                    for (int b = 0; b < kSteps; ++b) score(b, k_place(t), keys - t * kT);
                 release(k_place(t));
             }
             if (it.n <= L && ok) commit(on, &S.q_empty);
@@ -383,12 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int b = 0; b < kSteps; ++b) {
                     if (values_mine) values(b, nth, v, keys - t * kT);
-                    if (scores_mine) score(b, k);
+                    if (scores_mine) score(b, k, keys - (t + L) * kT);
                 }
                 release(v);
                 if (more) release(k);
                 if (t + L + 1 == it.n && ok) commit(on, &S.q_empty);   // the item's last scores
-                if (values_mine) { ++nth; ++tiles; }
+                if (values_mine) ++nth;
             }
         }
         // everything issued is done before TMEM is given back
@@ -400,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
         const float c2 = A.qscale;
         const int prow = row / G, g = row - prow * G;    // position and head of the row within its tile
-        int tiles = 0, meets = 0;                        // of this stream so far
+        int part0 = 0, part1 = 0, meets = 0;             // first and second parts of tiles of this stream so far
+        auto parts = [&](int b) { return b ? part1 : part0; };
         bool ok = true;
         // all softmax warps, and what they have written
         auto meet = [&]() {
@@ -420,12 +461,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nt = n > first ? (n - first + stride - 1) / stride : 0;    // this stream's tiles
             float m = -INFINITY, l = 0.f;
             if (ok && aborted()) ok = false;
-            for (int i = 0; i < kSteps * nt && ok; ++i) {
+            // (a last part that no row sees is left out)
+            const int ni = kSteps * nt - (nt > 0 && keys - (first + (nt - 1) * stride) * kT <= kStep ? 1 : 0);
+            for (int i = 0; i < ni && ok; ++i) {
                 const int nth = i / kSteps, b = i % kSteps, t = first + nth * stride, j0 = t * kT + kStep * b;
                 const uint32_t at = tS(s) + lanes + (uint32_t)(kStep * b);
                 // (a part's last product is done before its new scores are made, so the second look never waits; it is there to
                 // see every phase)
-                ok = __all_sync(0xffffffffu, wait(S, &S.s_ready[s][b], tiles + nth) && (nth == 0 || wait(S, &S.pv_done[s][b], tiles + nth - 1)));
+                ok = __all_sync(0xffffffffu, wait(S, &S.s_ready[s][b], parts(b) + nth) && (nth == 0 || wait(S, &S.pv_done[s][b], parts(b) + nth - 1)));
                 if (!ok) break;
                 tc_fence_after();
                 constexpr int NC = kStep / 32;
@@ -466,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (i > 0) {
                         // (all products but the last are done)
-                        ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][(i - 1) % kSteps], tiles + (i - 1) / kSteps));
+                        ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][(i - 1) % kSteps], parts((i - 1) % kSteps) + (i - 1) / kSteps));
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -513,10 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.p_ready[s][b]);
             }
+            part0 += (ni + 1) / 2;
+            part1 += ni / 2;
             for (int b = 0; b < kSteps; ++b)
-                if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][b], tiles + nt - 1));
+                if (ok && ni > b) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][b], parts(b) - 1));
             tc_fence_after();
-            tiles += nt;
 
             // ------------------------------------------------ results
             // One query tile: both streams' sums, half of the channels each.
@@ -552,40 +596,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool fine = ok && !aborted();
             const float f = l == 0.f ? 0.f : 1.f / l;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out) + (long long)(it.q0 + pos) * A.out_stride + (it.h * G + g) * D;
-            bool odd = false;
-            const int c0 = two ? 0 : s * (D / 2), c1 = two ? D : c0 + D / 2;
+            // A warp's rows go through shared memory, 64 channels at a time, and leave as one box of all their positions
+            // and heads where all are there and fill it (the threads do not wait for it: an SM writes about 32 bytes a cycle,
+            // and storing 16 bytes of each row took 6000 cycles an item), else 128 bytes of four rows a store.
+            const unsigned lives = __ballot_sync(0xffffffffu, live);
+            const bool box = boxes && lives == 0xffffffffu;
+            const long long at = (long long)(it.q0 + pos) * A.out_stride + (it.h * G + g) * D;
+            uint8_t* stage = S.out[warp - 4];
+            float2 odd2 = make_float2(0.f, 0.f);                                // 0 times every result
+            const uint32_t keep = l == 0.f || !fine ? 0u : ~0u, fill = fine ? 0u : 0x7fff7fffu;   // (no weight: zero; a wait that ran out: NaN)
+            const int c0 = two ? 0 : s * 64, c1 = two ? D : min(D, c0 + 64);    // (one tile: both streams' sums, 64 channels each)
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 32) {
-                uint32_t o[32];
-                tc_ld32_issue(tO(two ? s : 0) + lanes + (uint32_t)c, o);
-                tc_ld32_wait(o);
-                if (!two && it.n > 1) {
-                    uint32_t y[32];
-                    tc_ld32_issue(tO(1) + lanes + (uint32_t)c, y);
-                    tc_ld32_wait(y);
+            for (int c = c0; c < c1; c += 64) {
+                uint32_t r[32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), a0, __uint_as_float(y[k]) * a1));
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[32];
+                    tc_ld32_issue(tO(two ? s : 0) + lanes + (uint32_t)(c + 32 * h), o);
+                    tc_ld32_wait(o);
+                    if (!two && it.n > 1) {
+                        uint32_t y[32];
+                        tc_ld32_issue(tO(1) + lanes + (uint32_t)(c + 32 * h), y);
+                        tc_ld32_wait(y);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), a0, __uint_as_float(y[k]) * a1));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), make_float2(f, f));
+                        odd2 = __ffma2_rn(x, make_float2(0.f, 0.f), odd2);
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[16 * h + k]) : "f"(x.y), "f"(x.x));
+                        r[16 * h + k] = (r[16 * h + k] & keep) | fill;
+                    }
                 }
-                uint32_t r[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float x = l == 0.f ? 0.f : __uint_as_float(o[2 * k]) * f, y = l == 0.f ? 0.f : __uint_as_float(o[2 * k + 1]) * f;
-                    odd |= !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY);
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[k]) : "f"(y), "f"(x));
-                    if (!fine) r[k] = 0x7fff7fffu;
+                if (two && c + 64 == c1) {                 // the sums have been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && nt > 0) mbar_arrive(&S.o_free[s]);
                 }
-                if (live)
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // what left the stage before has been read
+                __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) *reinterpret_cast<uint4*>(out + c + 2 * k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                if (box) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&mapO, stage, c, it.h * G, it.q0 + pos);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                } else {
+                    __syncwarp();
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        const int x = 4 * k + (lane >> 3), i = lane & 7;
+                        const long long to = __shfl_sync(0xffffffffu, at, x);
+                        const uint4 y = *reinterpret_cast<const uint4*>(stage + x * 128 + ((i ^ (x & 7)) << 4));
+                        if (lives >> x & 1u) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.out) + to + c + i * 8) = y;
+                    }
+                    __syncwarp();
+                }
             }
-            tc_fence_before();
-            // the sums have been read: by the other stream's threads too
-            if (!two) meet();
-            __syncwarp();
-            if (lane == 0 && nt > 0) mbar_arrive(&S.o_free[s]);
-            // rows whose result is no number: what they do not see may have made it so
+            const bool odd = !(odd2.x == 0.f && odd2.y == 0.f) && l != 0.f;
             unsigned redo = __ballot_sync(0xffffffffu, live && odd && fine);
+            if (redo || !two) {                            // (rows made again are written after what they replace)
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                __syncwarp();
+            }
+            if (!two) {
+                meet();                                    // (the sums have been read by the other stream's threads too)
+                if (lane == 0 && nt > 0) mbar_arrive(&S.o_free[s]);
+            }
+            __syncwarp();
+            // rows whose result is no number: what they do not see may have made it so
             while (redo) {
                 const int r = __ffs(redo) - 1;
                 redo &= redo - 1;
@@ -597,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              static_cast<__nv_bfloat16*>(A.out) + qrow * A.out_stride + (it.h * G + rg) * D);
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -674,8 +759,9 @@ template <int D>
 cudaError_t go(const PackedArgs& a, cudaStream_t st)
 {
     const int np = kT / a.G;
-    CUtensorMap mq, mk, mv;
-    if (!rows_map(&mq, a.q, D, a.heads * a.G, a.rows, a.q_stride, a.G, np) || !rows_map(&mk, a.k, D, a.heads, a.k_rows, a.k_stride, 1, kT) ||
+    CUtensorMap mq, mk, mv, mo;
+    const int boxes = (a.G & (a.G - 1)) == 0;              // a warp's 32 rows are whole positions
+    if (!rows_map(&mo, a.out, D, a.heads * a.G, a.rows, a.out_stride, a.G, 32 / a.G) || !rows_map(&mq, a.q, D, a.heads * a.G, a.rows, a.q_stride, a.G, np) || !rows_map(&mk, a.k, D, a.heads, a.k_rows, a.k_stride, 1, kT) ||
         !rows_map(&mv, a.v, D, a.heads, a.k_rows, a.v_stride, 1, kT))
         return cudaErrorInvalidValue;
     const int smem = (int)sizeof(Smem<D>);
@@ -701,13 +787,13 @@ cudaError_t go(const PackedArgs& a, cudaStream_t st)
         cfg.stream = st;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, np, (int)works);
+        return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, mo, a, np, boxes, (int)works);
     }
     const auto kernel = prompt_tc_kernel<D, false>;
     static SmemOnce once;
     const cudaError_t e = once.allow(kernel);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)std::min<long long>(works, kSMs), kThreads, smem, st>>>(mq, mk, mv, a, np, (int)works);
+    kernel<<<(unsigned)works, kThreads, smem, st>>>(mq, mk, mv, mo, a, np, boxes, (int)works);
     return cudaGetLastError();
 }
 
