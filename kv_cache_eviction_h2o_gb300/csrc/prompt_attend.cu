@@ -4,7 +4,7 @@
 // x = h + m + l, each the bf16 nearest to what is left, holds all 24 bits of x at
 // any exponent.  Of the nine products of two such sums the six from h h' to 2^-16
 // of it (h h', h m', m h', h l', m m', l h') are made, and the others are below
-// 2^-23 of the product; the sums are fp32's.  (Three products of tf32 halves took
+// 2^-23 of the product; sums of 16 products are added up in fp32.  (Three products of tf32 halves took
 // 1.7 times as long: an SM makes a quarter as many of them.)
 //
 // A CTA of four warps takes tiles of 16 query rows (a request's positions, the
@@ -60,15 +60,22 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& h, uint32_t& m
     y -= __uint_as_float(m & 0xffff0000u);
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(l) : "f"(y), "f"(x));
 }
-// c[i] += a b[i] for a and b in three parts, the small products first and those of one sum apart from one another
+// c[i] += a b[i] for a and b in three parts.  The tensor cores cut a sum's bits off where an addition rounds, which adds up
+// over long sums (20000 keys: 8e-6 off), so sums of 16 terms are added up by the FMA pipe; the small products come first
+// and those of one sum apart from one another.
 template <int N>
 __device__ __forceinline__ void mma_six(float (*c)[4], const uint32_t (&a)[3][4], const uint32_t (&b)[N][3][2])
 {
     constexpr int pa[6] = {2, 1, 0, 1, 0, 0}, pb[6] = {0, 1, 2, 0, 1, 0};
+    float s[N][4] = {};
 #pragma unroll
     for (int p = 0; p < 6; ++p)
 #pragma unroll
-        for (int i = 0; i < N; ++i) mma16(c[i], a[pa[p]], b[i][pb[p]]);
+        for (int i = 0; i < N; ++i) mma16(s[i], a[pa[p]], b[i][pb[p]]);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[i][e] += s[i][e];
 }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
 {

@@ -191,6 +191,22 @@ struct Core {
         return hfma2(u, BITS == 4 && HI ? 0x64006400u : 0x74007400u, BITS == 8 ? 0xb000b000u : 0xa000a000u);
     }
 
+    // c += a b[..][n][k].  With two parts sums of 16 products are added up by the FMA pipe: the tensor cores cut a sum's bits
+    // off where an addition rounds, which adds up over many keys.
+    template <int K>
+    __device__ __forceinline__ static void mma_parts(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[PARTS][NT][K][2], int n, int k)
+    {
+        if constexpr (PARTS == 1) {
+            mma16(c, a[0], a[1], a[2], a[3], b[0][n][k][0], b[0][n][k][1]);
+        } else {
+            float s[4] = {};
+#pragma unroll
+            for (int p = PARTS - 1; p >= 0; --p) mma16(s, a[0], a[1], a[2], a[3], b[p][n][k][0], b[p][n][k][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] += s[e];
+        }
+    }
+
     // Channel of code i of word j of a row's part t (the words are one step of K, or two with 4 bits).
     __device__ __forceinline__ static int channel(int t, int j, int i)
     {
@@ -351,9 +367,7 @@ struct Core {
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int p = 0; p < PARTS; ++p) mma16(s[n][x], a[0], a[1], a[2], a[3], q[p][n][k][0], q[p][n][k][1]);
+                for (int n = 0; n < NT; ++n) mma_parts(s[n][x], a, q, n, k);
             }
         }
         float kf[TILES][2], v[TILES][2];
@@ -438,9 +452,7 @@ struct Core {
                         }
                         const int k = (c + h) * (CP / 2) + j;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < PARTS; ++i) mma16(o[n][k], a[0], a[1], a[2], a[3], b[i][n][x][0], b[i][n][x][1]);
+                        for (int n = 0; n < NT; ++n) mma_parts(o[n][k], a, b, n, x);
                     }
             }
         }
