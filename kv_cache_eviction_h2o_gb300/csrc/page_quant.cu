@@ -9,6 +9,8 @@
 //
 // Bound: HBM.  A lane holds 16 bytes of a row of K and of the same row of V, so
 // a row's head is 8 to 32 lanes.
+#include <type_traits>
+
 #include "common.cuh"
 #include "prompts.h"
 
@@ -23,13 +25,6 @@ template <typename T> struct Lane {
     static constexpr int E = 16 / sizeof(T);
     float x[E];
     __device__ __forceinline__ void load(const T* p) { load_vec<T, E>(p, x); }
-    __device__ __forceinline__ uint32_t amax_bits() const
-    {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < E; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-        return m;
-    }
     __device__ __forceinline__ void store(T* p) const
     {
         if constexpr (sizeof(T) == 2) {
@@ -43,16 +38,81 @@ template <typename T> struct Lane {
     }
 };
 
-// E codes at p
-template <int BITS, int E>
-__device__ __forceinline__ void put_codes(unsigned char* p, const float* x, float inv)
+// The largest |x| of a row's L lanes of 16 bytes, of keys and of values, as fp32's bits.  (bf16: both in one word.)
+template <typename T, int L>
+__device__ __forceinline__ void amax_bits(const uint4 (&v)[2], uint32_t (&m)[2])
 {
-    if constexpr (BITS == 8) {
-        if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q8_pack4(x, inv), q8_pack4(x + 4, inv));
-        else *reinterpret_cast<uint32_t*>(p) = q8_pack4(x, inv);
+    if constexpr (sizeof(T) == 2) {
+        uint32_t a[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            a[i] = v[i].x & 0x7fff7fffu;
+            asm("max.u16x2 %0, %0, %1;" : "+r"(a[i]) : "r"(v[i].y & 0x7fff7fffu));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(a[i]) : "r"(v[i].z & 0x7fff7fffu));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(a[i]) : "r"(v[i].w & 0x7fff7fffu));
+        }
+        uint32_t both = __byte_perm(a[0], a[1], 0x5410);
+        asm("max.u16x2 %0, %0, %1;" : "+r"(both) : "r"(__byte_perm(a[0], a[1], 0x7632)));
+#pragma unroll
+        for (int d = L / 2; d > 0; d >>= 1) asm("max.u16x2 %0, %0, %1;" : "+r"(both) : "r"(__shfl_xor_sync(0xffffffffu, both, d)));
+        m[0] = both << 16;
+        m[1] = both & 0xffff0000u;
     } else {
-        if constexpr (E == 8) *reinterpret_cast<uint32_t*>(p) = q4_pack<4>(x, inv);
-        else *reinterpret_cast<unsigned short*>(p) = (unsigned short)q4_pack<2>(x, inv);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            m[i] = max(max(v[i].x & 0x7fffffffu, v[i].y & 0x7fffffffu), max(v[i].z & 0x7fffffffu, v[i].w & 0x7fffffffu));
+#pragma unroll
+            for (int d = L / 2; d > 0; d >>= 1) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
+        }
+    }
+}
+// four bytes, the lowest of each
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// E codes as q8_pack4 and q4_pack make them, for a finite inv: |x inv| is below 2^22, so adding 1.5 2^23 (and the 4-bit
+// offset, which is even) rounds it to the nearest whole number, half to even, and leaves it in the low bits; and it is
+// within the codes' range, since the largest |x| inv is 127 or 7 but for two roundings.
+template <int BITS, int E>
+__device__ __forceinline__ uint2 make_codes(const float* x, float inv)
+{
+    uint32_t u[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) u[i] = __float_as_uint(__fadd_rn(__fmul_rn(x[i], inv), BITS == 8 ? 12582912.f : 12582920.f));
+    if constexpr (BITS == 8) {
+        return make_uint2(low_bytes(u[0], u[1], u[2], u[3]), E == 8 ? low_bytes(u[E - 4], u[E - 3], u[E - 2], u[E - 1]) : 0u);
+    } else if constexpr (E == 8) {
+        return make_uint2(low_bytes(u[0], u[2], u[4], u[6]) + 16u * low_bytes(u[1], u[3], u[5], u[7]), 0u);
+    } else {
+        return make_uint2((u[0] & 15u) | (u[1] & 15u) << 4 | (u[2] & 15u) << 8 | (u[3] & 15u) << 12, 0u);
+    }
+}
+// the same whatever inv is
+template <int BITS, int E>
+__device__ __forceinline__ uint2 make_codes_any(const float* x, float inv)
+{
+    if constexpr (BITS == 8) return make_uint2(q8_pack4(x, inv), E == 8 ? q8_pack4(x + E - 4, inv) : 0u);
+    else return make_uint2(q4_pack<E / 2>(x, inv), 0u);
+}
+template <int BITS, int E>
+__device__ __forceinline__ void put_codes(unsigned char* p, uint2 w)
+{
+    if constexpr (BITS * E == 64) *reinterpret_cast<uint2*>(p) = w;
+    else if constexpr (BITS * E == 32) *reinterpret_cast<uint32_t*>(p) = w.x;
+    else *reinterpret_cast<unsigned short*>(p) = (unsigned short)w.x;
+}
+// B bytes of codes into registers
+template <int B>
+__device__ __forceinline__ void get_raw(const unsigned char* p, uint32_t (&r)[2])
+{
+    if constexpr (B == 8) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        r[0] = w.x; r[1] = w.y;
+    } else if constexpr (B == 4) {
+        r[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+        r[0] = *reinterpret_cast<const unsigned short*>(p);
     }
 }
 template <int BITS, int E>
@@ -78,77 +138,140 @@ __device__ __forceinline__ void get_codes(const unsigned char* p, float* x)
     }
 }
 
-// This thread's row, head and place in the pool; false: none.
+// A thread's i-th row of head h among RPT, and its place in the pool.  Units (row, head) lie one after another, a CTA has
+// RPT * 256 / L of them.
 template <typename T, int D>
 struct Place {
-    static constexpr int E = 16 / sizeof(T), L = D / E;    // lanes of a row's head
-    int row, h, c;                                         // c: lane of the row's head
+    static constexpr int E = 16 / sizeof(T), L = D / E, kUnits = kThreads / L;    // L: lanes of a row's head
+    int row, h;
+    bool in;
     size_t at;                                             // its row of codes, and its scale
-    __device__ __forceinline__ bool find(const QuantPool& p, const int* slot, int rows)
-    {
-        const long long x = (long long)blockIdx.x * kThreads + threadIdx.x;
-        const unsigned u = (unsigned)(x / L);
-        c = (int)(x % L);
-        row = (int)(u / (unsigned)p.heads);
-        h = (int)(u - (unsigned)row * p.heads);
-        const int s = row < rows ? slot[row] : -1, sh = __ffs(p.ps) - 1;
-        if (s < 0 || s >= (long long)p.pages * p.ps) return false;
-        at = ((size_t)(s >> sh) * p.heads + h) * p.ps + (s & (p.ps - 1));
-        return true;
-    }
 };
+template <typename T, int D, int RPT>
+__device__ __forceinline__ void find(Place<T, D> (&w)[RPT], const QuantPool& p, const int* slot, int rows)
+{
+    using P = Place<T, D>;
+    const unsigned u = blockIdx.x * (unsigned)(RPT * P::kUnits) + threadIdx.x / P::L, heads = (unsigned)p.heads;
+    const unsigned by = P::kUnits / heads, over = P::kUnits - by * heads;   // a step of kUnits: rows, heads
+    unsigned row = u / heads, h = u - row * heads;
+    const int sh = __ffs(p.ps) - 1;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        w[i].row = (int)row;
+        w[i].h = (int)h;
+        const int s = row < (unsigned)rows ? slot[row] : -1;
+        w[i].in = s >= 0 && s < (long long)p.pages * p.ps;
+        w[i].at = w[i].in ? ((size_t)(s >> sh) * heads + h) * p.ps + (s & (p.ps - 1)) : 0;
+        row += by;
+        h += over;
+        if (h >= heads) { h -= heads; ++row; }
+    }
+}
 
-template <typename T, int D, int BITS>
+template <typename T, int D, int BITS, int RPT>
 __global__ void __launch_bounds__(kThreads) page_quant_write_kernel(const QuantPool p, const T* __restrict__ k, const T* __restrict__ v,
                                                                     const long long k_stride, const long long v_stride,
                                                                     const int* __restrict__ slot, const int rows)
 {
     using P = Place<T, D>;
     constexpr int E = P::E, L = P::L;
-    P w;
-    const bool in = w.find(p, slot, rows);
-    Lane<T> x[2] = {};
-    if (in) {
-        x[0].load(k + w.row * k_stride + w.h * D + w.c * E);
-        x[1].load(v + w.row * v_stride + w.h * D + w.c * E);
+    const int c = threadIdx.x % L;
+    P w[RPT];
+    uint4 raw[RPT][2];
+    find(w, p, slot, rows);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (w[i].in) {
+            raw[i][0] = *reinterpret_cast<const uint4*>(k + w[i].row * k_stride + w[i].h * D + c * E);
+            raw[i][1] = *reinterpret_cast<const uint4*>(v + w[i].row * v_stride + w[i].h * D + c * E);
+        }
+    }
+    // The quotients of a row's lanes' 2 RPT items (keys and values of RPT rows), inv then scale, are made a lane each.
+    constexpr int N = 2 * RPT;
+    const float top = BITS == 8 ? 127.f : 7.f;
+    uint32_t m[N];
+    bool odd = false;                                      // a row that holds no number, or whose inv is out of range
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        uint32_t x[2];
+        amax_bits<T, L>(raw[i], x);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            m[2 * i + j] = x[j];
+            odd |= x[j] - 1u < 0x03ffffffu || x[j] >= 0x7f800000u;   // (0 < largest < 2^-119)
+        }
+    }
+    odd = __any_sync(0xffffffffu, odd);
+    float quotient[(2 * N + L - 1) / L];
+#pragma unroll
+    for (int j = 0; j < (2 * N + L - 1) / L; ++j) {
+        const int task = c + j * L, item = task % N;
+        uint32_t mine = m[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) mine = item == i ? m[i] : mine;
+        const bool finite = mine < 0x7f800000u, scale = task >= N;
+        const float amax = finite ? __uint_as_float(mine) : 0.f;
+        quotient[j] = __fdiv_rn(scale ? amax : top, scale ? top : amax);
+        if (!scale && amax == 0.f) quotient[j] = 0.f;
+        if (scale && task < 2 * N) {
+            const int row = item >> 1;
+            P x = w[0];
+#pragma unroll
+            for (int i = 1; i < RPT; ++i)
+                if (row == i) x = w[i];
+            if (x.in) (item & 1 ? p.vs : p.ks)[x.at] = finite ? quotient[j] : NAN;
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t m = x[i].amax_bits();
+    for (int i = 0; i < N; ++i) {
+        const P& x = w[i / 2];
+        const float inv = __shfl_sync(0xffffffffu, quotient[i / L], i % L, L);
+        Lane<T> y;
+        y.load(reinterpret_cast<const T*>(&raw[i / 2][i & 1]));
+        uint2 code;
+        if (!odd) {
+            code = make_codes<BITS, E>(y.x, inv);
+        } else {
+            if (m[i] >= 0x7f800000u)
 #pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const bool finite = m < 0x7f800000u;
-        const float amax = finite ? __uint_as_float(m) : 0.f;
-        const float inv = BITS == 8 ? q8_inv(amax) : q4_inv(amax), scale = finite ? (BITS == 8 ? q8_scale(amax) : q4_scale(amax)) : NAN;
-        if (!finite)
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[i].x[e] = 0.f;
-        if (in) {
-            put_codes<BITS, E>(static_cast<unsigned char*>(i ? p.V : p.K) + (w.at * D + w.c * E) * BITS / 8, x[i].x, inv);
-            if (w.c == i) (i ? p.vs : p.ks)[w.at] = scale;
+                for (int e = 0; e < E; ++e) y.x[e] = 0.f;
+            code = make_codes_any<BITS, E>(y.x, inv);
         }
+        if (x.in) put_codes<BITS, E>(static_cast<unsigned char*>(i & 1 ? p.V : p.K) + (x.at * D + c * E) * BITS / 8, code);
     }
 }
 
-template <typename T, int D, int BITS>
+template <typename T, int D, int BITS, int RPT>
 __global__ void __launch_bounds__(kThreads) page_quant_read_kernel(const QuantPool p, const int* __restrict__ slot, const int rows,
                                                                    T* __restrict__ k, const long long k_stride, T* __restrict__ v,
                                                                    const long long v_stride)
 {
     using P = Place<T, D>;
-    constexpr int E = P::E;
-    P w;
-    if (!w.find(p, slot, rows)) return;
-    Lane<T> x[2];
-    const float s[2] = {p.ks[w.at], p.vs[w.at]};
+    constexpr int E = P::E, B = E * BITS / 8;              // B: bytes of this lane's codes
+    const int c = threadIdx.x % P::L;
+    P w[RPT];
+    uint32_t raw[RPT][2][2];
+    float s[RPT][2];
+    find(w, p, slot, rows);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        get_codes<BITS, E>(static_cast<const unsigned char*>(i ? p.V : p.K) + (w.at * D + w.c * E) * BITS / 8, x[i].x);
+    for (int i = 0; i < 2 * RPT; ++i) {
+        const P& x = w[i / 2];
+        const bool values = i & 1;
+        if (x.in) {
+            get_raw<B>(static_cast<const unsigned char*>(values ? p.V : p.K) + x.at * (D * BITS / 8) + c * B, raw[i / 2][i & 1]);
+            s[i / 2][i & 1] = (values ? p.vs : p.ks)[x.at];
+        }
+    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * RPT; ++i) {
+        const P& x = w[i / 2];
+        if (!x.in) continue;
+        Lane<T> y;
+        get_codes<BITS, E>(reinterpret_cast<const unsigned char*>(raw[i / 2][i & 1]), y.x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[i].x[e] *= s[i];
-        x[i].store((i ? v + w.row * v_stride : k + w.row * k_stride) + w.h * D + w.c * E);
+        for (int e = 0; e < E; ++e) y.x[e] *= s[i / 2][i & 1];
+        y.store((i & 1 ? v + x.row * v_stride : k + x.row * k_stride) + x.h * D + c * E);
     }
 }
 
@@ -169,6 +292,15 @@ cudaError_t by_type(const QuantPool& p, F f)
     return cudaGetLastError();
 }
 
+// f(rows a thread, CTAs): four where that still makes eight CTAs an SM
+template <class F>
+void by_rows(long long units, int each, F f)
+{
+    const long long four = (units + 4 * each - 1) / (4 * each);
+    if (four >= 8 * kSMs) f(std::integral_constant<int, 4>(), (unsigned)four);
+    else f(std::integral_constant<int, 1>(), (unsigned)((units + each - 1) / each));
+}
+
 }  // namespace
 
 cudaError_t launch_page_quant_write(const QuantPool& p, const void* k, const void* v, long long k_stride, long long v_stride,
@@ -176,10 +308,11 @@ cudaError_t launch_page_quant_write(const QuantPool& p, const void* k, const voi
 {
     return by_type(p, [&](auto t, auto d, auto bits) {
         using T = decltype(t);
-        constexpr int D = decltype(d)::value;
-        const long long threads = (long long)rows * p.heads * Place<T, D>::L;
-        page_quant_write_kernel<T, D, decltype(bits)::value><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, st>>>(
-            p, static_cast<const T*>(k), static_cast<const T*>(v), k_stride, v_stride, slot, rows);
+        constexpr int D = decltype(d)::value, B = decltype(bits)::value;
+        by_rows((long long)rows * p.heads, Place<T, D>::kUnits, [&](auto rpt, unsigned grid) {
+            page_quant_write_kernel<T, D, B, decltype(rpt)::value><<<grid, kThreads, 0, st>>>(
+                p, static_cast<const T*>(k), static_cast<const T*>(v), k_stride, v_stride, slot, rows);
+        });
     });
 }
 
@@ -188,10 +321,11 @@ cudaError_t launch_page_quant_read(const QuantPool& p, const int* slot, int rows
 {
     return by_type(p, [&](auto t, auto d, auto bits) {
         using T = decltype(t);
-        constexpr int D = decltype(d)::value;
-        const long long threads = (long long)rows * p.heads * Place<T, D>::L;
-        page_quant_read_kernel<T, D, decltype(bits)::value><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, st>>>(
-            p, slot, rows, static_cast<T*>(k), k_stride, static_cast<T*>(v), v_stride);
+        constexpr int D = decltype(d)::value, B = decltype(bits)::value;
+        by_rows((long long)rows * p.heads, Place<T, D>::kUnits, [&](auto rpt, unsigned grid) {
+            page_quant_read_kernel<T, D, B, decltype(rpt)::value><<<grid, kThreads, 0, st>>>(
+                p, slot, rows, static_cast<T*>(k), k_stride, static_cast<T*>(v), v_stride);
+        });
     });
 }
 
