@@ -29,10 +29,10 @@ constexpr int kKeys = 32;                              // of a tile
 constexpr int kMaxCluster = 16;
 
 template <int D, int WK> struct alignas(16) Smem {
-    static constexpr int kRows = 16 * kWarps / WK;
+    static constexpr int kRows = 16 * kWarps / WK, kStages = 2;
     float q[kRows][D + 16];
-    float k[2][kKeys][D + 16];
-    float v[2][kKeys][D + 4];
+    float k[kStages][kKeys][D + 16];
+    float v[kStages][kKeys][D + 4];
     float2 ml[kWarps][16];                             // of each warp's rows
     float2 sum_ml[kRows];
 };
@@ -45,7 +45,7 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool fill
 
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
@@ -95,7 +95,7 @@ template <int D, int WK>
 __global__ void __launch_bounds__(kThreads) prompt_f32_kernel(const PackedArgs A, const int np, const int works)
 {
     using M = Smem<D, WK>;
-    constexpr int R = M::kRows, NT = kKeys / 8 / WK;       // NT: steps of eight keys of a warp's part of a tile
+    constexpr int R = M::kRows, NS = M::kStages, NT = kKeys / 8 / WK;       // NT: steps of eight keys of a warp's part of a tile
     extern __shared__ __align__(16) unsigned char raw[];
     M& S = *reinterpret_cast<M*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kThreads) prompt_f32_kernel(const PackedArgs A
             }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    ask(t_0, 0);
+#pragma unroll 1
+    for (int s = 0; s < NS - 1; ++s) ask(t_0 + s, s);
 
     const int wr = warp / WK, wk = warp % WK;              // which rows, which keys of a tile
     // keys that rows g and g + 8 of this warp see
@@ -146,14 +147,14 @@ __global__ void __launch_bounds__(kThreads) prompt_f32_kernel(const PackedArgs A
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     for (int tile = t_0; tile < t_1; ++tile) {
-        const int stage = (tile - t_0) & 1;
-        ask(tile + 1, stage ^ 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const int stage = (tile - t_0) % NS;
+        ask(tile + NS - 1, (tile - t_0 + NS - 1) % NS);
+        asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
         __syncthreads();
         float z[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
-#pragma unroll 1
+#pragma unroll (NT == 1 ? 4 : 1)
         for (int j = 0; j < D / 16; ++j) {                 // channels 16 j + 4 t + (0, 1) and (2, 3): product indexes 2 t, + 1 and + 8, + 9
             const float4 x0 = *reinterpret_cast<const float4*>(&S.q[wr * 16 + g][16 * j + 4 * t]);
             const float4 x1 = *reinterpret_cast<const float4*>(&S.q[wr * 16 + g + 8][16 * j + 4 * t]);
@@ -350,8 +351,10 @@ cudaError_t launch_prompt_attend(const PackedArgs& a, int D, int dtype, cudaStre
         return cudaGetLastError();
     }
     if (dtype) return launch_prompt_tc(a, D, st);
-    // few rows a request: the warps share keys
-    if ((long long)a.rows * a.G <= 24LL * a.requests) return D == 64 ? go<64, 4>(a, st) : go<128, 4>(a, st);
+    // Few rows a request, or so few tiles of 64 that tiles of 16 rows do not fill the GPU either: the warps share keys (128
+    // tokens of 4 heads: 16.6 us by rows, 10.4 so).
+    const long long most = (a.rows + a.requests - 1) / a.requests * (long long)a.G, tiles = (most + 63) / 64 * a.requests * a.heads;
+    if (most <= 24 || tiles * 4 <= kSMs) return D == 64 ? go<64, 4>(a, st) : go<128, 4>(a, st);
     return D == 64 ? go<64, 1>(a, st) : go<128, 1>(a, st);
 }
 
