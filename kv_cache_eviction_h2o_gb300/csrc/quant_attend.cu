@@ -224,15 +224,23 @@ struct Core {
             const T* row = qrow + (size_t)(head < G ? head : 0) * D;
             uint32_t big = 0u;
             float x[KS][4];                                // of step k: those for b0's halves, then b1's
+            // a word's channels lie side by side: 4 or 8 of them at a time
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                int c[4];
-                if constexpr (BITS == 8) { c[0] = channel(t, k, 0); c[1] = channel(t, k, 2); c[2] = channel(t, k, 1); c[3] = channel(t, k, 3); }
-                else { const int i = (k & 1) * 2; c[0] = channel(t, k / 2, i); c[1] = channel(t, k / 2, i + 4); c[2] = channel(t, k / 2, i + 1); c[3] = channel(t, k / 2, i + 5); }
+            for (int j = 0; j < KS / (BITS == 8 ? 1 : 2); ++j) {
+                constexpr int N = BITS == 8 ? 4 : 8;
+                float y[N];
+                load_vec<T, 4>(row + channel(t, j, 0), y);
+                if constexpr (N == 8) load_vec<T, 4>(row + channel(t, j, 0) + 4, y + 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[k][e] = head < G ? Elem<T>::to_f(row[c[e]]) : 0.f;
-                    big = max(big, __float_as_uint(x[k][e]) & 0x7fffffffu);
+                for (int e = 0; e < N; ++e) {
+                    if (head >= G) y[e] = 0.f;
+                    big = max(big, __float_as_uint(y[e]) & 0x7fffffffu);
+                }
+                if constexpr (BITS == 8) {
+                    x[j][0] = y[0]; x[j][1] = y[2]; x[j][2] = y[1]; x[j][3] = y[3];
+                } else {
+                    x[2 * j][0] = y[0]; x[2 * j][1] = y[4]; x[2 * j][2] = y[1]; x[2 * j][3] = y[5];
+                    x[2 * j + 1][0] = y[2]; x[2 * j + 1][1] = y[6]; x[2 * j + 1][2] = y[3]; x[2 * j + 1][3] = y[7];
                 }
             }
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
@@ -566,6 +574,14 @@ __global__ void __launch_bounds__(kThreads, NT == 2 && sizeof(T) == 4 ? 2 : NT =
     __syncthreads();
     float* sums = reinterpret_cast<float*>(raw);           // in the place of warp 0's
     constexpr int V4 = D / 32;                             // a lane's channels of a head
+    T* orow = static_cast<T*>(R.out) + (size_t)row * R.out_stride + (size_t)h * G * D;
+    // no key at all, or none of weight: zero; a bad table entry has made l NaN
+    auto leave = [&](int g, float l, float (&o)[V4]) {
+        const float f = 1.f / l;
+#pragma unroll
+        for (int e = 0; e < V4; ++e) o[e] = l == 0.f ? 0.f : o[e] * f;
+        store_out<V4>(orow + g * D + lane * V4, o);
+    };
     for (int g = warp; g < G; g += kWarps) {
         float m = -INFINITY, l = 0.f, o[V4] = {};
 #pragma unroll
@@ -580,13 +596,17 @@ __global__ void __launch_bounds__(kThreads, NT == 2 && sizeof(T) == 4 ? 2 : NT =
 #pragma unroll
             for (int e = 0; e < V4; ++e) o[e] = fmaf(a, x[e], o[e]);
         }
-        store_out<V4>(sums + g * D + lane * V4, o);
-        if (lane == 0) S.ml[g] = make_float2(m, l);
+        if (C == 1) {
+            leave(g, l, o);
+        } else {
+            store_out<V4>(sums + g * D + lane * V4, o);
+            if (lane == 0) S.ml[g] = make_float2(m, l);
+        }
     }
+    if (C == 1) return;
     cluster_arrive();
     cluster_wait();
     // a warp joins a head's sums of all CTAs
-    T* orow = static_cast<T*>(R.out) + (size_t)row * R.out_stride + (size_t)h * G * D;
 #pragma unroll 1
     for (int g = rank * kWarps + warp; g < G; g += C * kWarps) {
         const float2 x = lane < C ? ld_cluster_f2(map_to_rank(&S.ml[g], lane)) : make_float2(-INFINITY, 0.f);
@@ -601,11 +621,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 && sizeof(T) == 4 ? 2 : NT =
 #pragma unroll
             for (int e = 0; e < V4; ++e) o[e] = fmaf(a, v[e], o[e]);
         }
-        // no key at all, or none of weight: zero; a bad table entry has made l NaN
-        const float f = 1.f / l;
-#pragma unroll
-        for (int e = 0; e < V4; ++e) o[e] = l == 0.f ? 0.f : o[e] * f;
-        store_out<V4>(orow + g * D + lane * V4, o);
+        leave(g, l, o);
     }
     cluster_arrive();
     cluster_wait();                                        // no CTA leaves while another reads its sums
