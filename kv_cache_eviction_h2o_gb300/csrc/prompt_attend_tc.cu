@@ -42,10 +42,11 @@ constexpr float kRaise = 8.f;
 constexpr int kMaxCluster = 16;
 constexpr int kSteps = 2, kStep = kT / kSteps;     // S and P go by two parts of a tile
 
-template <int D> struct Cfg {
+template <int D, bool SPLIT> struct Cfg {
     static constexpr int kBoxes = D / 64;
     static constexpr uint32_t kTile = kBoxes * kBox;
-    static constexpr int kSlots = D == 128 ? 4 : 6;    // K and V tiles in flight
+    static constexpr int kSlots = SPLIT ? (D == 128 ? 5 : 8) : D == 128 ? 4 : 6;    // K and V tiles in flight
+    static constexpr int kStage = SPLIT ? 16 : 32 * 128;   // bytes of a softmax warp's rows on their way out: 64 channels of each
     static constexpr int kPitch = D * 4 + 16;          // of a row of sums (16 bytes more: no bank conflicts)
     static_assert(2 * kT * kPitch <= (2 + kSlots) * (int)kTile, "the queries' and keys' place holds them");
 };
@@ -57,12 +58,13 @@ struct Item {
     int q0, nq, p, k0, before, nk, h, n, ring, all, stop;
 };
 
-template <int D>
+template <int D, bool SPLIT>
 struct alignas(1024) Smem {
-    uint8_t q[2][Cfg<D>::kTile];
-    uint8_t ring[Cfg<D>::kSlots][Cfg<D>::kTile];
-    uint8_t out[8][32 * 128];          // of each softmax warp: 64 channels of its rows on their way out
-    uint64_t full[Cfg<D>::kSlots], empty[Cfg<D>::kSlots];
+    using C = Cfg<D, SPLIT>;
+    uint8_t q[2][C::kTile];
+    uint8_t ring[C::kSlots][C::kTile];
+    uint8_t out[8][C::kStage];
+    uint64_t full[C::kSlots], empty[C::kSlots];
     uint64_t q_full, q_empty, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2][kSteps], o_free[2], last;   // [stream][part of the tile]
     uint64_t item_full[2], item_empty[2], joined, taken;
     alignas(16) uint4 taken_at;
@@ -71,7 +73,7 @@ struct alignas(1024) Smem {
     uint32_t tmem;
     int abort, any;                    // any: there was an item
 };
-static_assert(sizeof(Smem<128>) <= 227 * 1024, "one CTA's shared memory");
+static_assert(sizeof(Smem<128, false>) <= 227 * 1024 && sizeof(Smem<128, true>) <= 227 * 1024, "one CTA's shared memory");
 
 // accumulator fp32, bf16 A and B, A K-major, B K-major or (bit 16) N-major
 template <int N, bool BMN>
@@ -163,8 +165,8 @@ __device__ __forceinline__ uint64_t value_desc(const void* p)
 // every barrier's phases are seen.  V(t)'s place:
 __device__ __forceinline__ int v_at(int t, int n, int L) { return t + min(n, t + L); }
 
-template <int D>
-__device__ __forceinline__ bool wait(Smem<D>& S, uint64_t* bar, int count)
+template <class Shared>
+__device__ __forceinline__ bool wait(Shared& S, uint64_t* bar, int count)
 {
     // the barrier's phase number `count` (from 0)
     if (mbar_wait(bar, (uint32_t)count & 1u)) return true;
@@ -178,10 +180,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                      const __grid_constant__ CUtensorMap mapO, const PackedArgs A, const int np, const int boxes, const int works)
 {
-    using C_ = Cfg<D>;
+    using C_ = Cfg<D, SPLIT>;
     constexpr int NS = C_::kSlots;
     extern __shared__ __align__(1024) unsigned char raw[];
-    Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
+    Smem<D, SPLIT>& S = *reinterpret_cast<Smem<D, SPLIT>*>(raw);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (known to be uniform)
     const int G = A.G;
 
@@ -764,7 +766,6 @@ cudaError_t go(const PackedArgs& a, cudaStream_t st)
     if (!rows_map(&mo, a.out, D, a.heads * a.G, a.rows, a.out_stride, a.G, 32 / a.G) || !rows_map(&mq, a.q, D, a.heads * a.G, a.rows, a.q_stride, a.G, np) || !rows_map(&mk, a.k, D, a.heads, a.k_rows, a.k_stride, 1, kT) ||
         !rows_map(&mv, a.v, D, a.heads, a.k_rows, a.v_stride, 1, kT))
         return cudaErrorInvalidValue;
-    const int smem = (int)sizeof(Smem<D>);
     const long long works = ((long long)a.rows / (2 * np) + a.requests) * a.heads;
     // Where there are fewer items than SMs, a cluster of CTAs for each, with at least four key tiles a CTA.
     const long long items = (long long)a.heads * a.requests * (((long long)a.rows / a.requests + 2 * np - 1) / (2 * np) + (a.rows < a.requests));
@@ -783,7 +784,7 @@ cudaError_t go(const PackedArgs& a, cudaStream_t st)
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(works * C));
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = sizeof(Smem<D, true>);
         cfg.stream = st;
         cfg.attrs = at;
         cfg.numAttrs = 1;
@@ -793,7 +794,7 @@ cudaError_t go(const PackedArgs& a, cudaStream_t st)
     static SmemOnce once;
     const cudaError_t e = once.allow(kernel);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)works, kThreads, smem, st>>>(mq, mk, mv, mo, a, np, boxes, (int)works);
+    kernel<<<(unsigned)works, kThreads, sizeof(Smem<D, false>), st>>>(mq, mk, mv, mo, a, np, boxes, (int)works);
     return cudaGetLastError();
 }
 
