@@ -26,7 +26,6 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kKeys = 32;                              // of a tile
-constexpr int kMaxCluster = 16;
 
 template <int D, int WK> struct alignas(16) Smem {
     static constexpr int kRows = 16 * kWarps / WK, kStages = 2;
@@ -108,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) prompt_f32_kernel(const PackedArgs A
     if (q0 < 0 || q1 <= q0 || q1 > A.rows || k0 < 0 || k1 < k0 || k1 > A.k_rows) return;
     const int nq = q1 - q0, nk = k1 - k0;
     const long long first = (long long)(x - (q0 / np + i)) * np;
-    if (first >= nq) return;
+    if (first < 0 || first >= nq) return;
     const int p = (int)first, end = max(0, min(nk, nk - nq + min(nq, p + np)));   // keys that any of its rows sees
     const int tiles = (end + kKeys - 1) / kKeys, t_0 = (int)((long long)tiles * rank / C), t_1 = (int)((long long)tiles * (rank + 1) / C);
     const float* const Q = static_cast<const float*>(A.q);
@@ -304,10 +303,8 @@ cudaError_t go(const PackedArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const int np = M::kRows / a.G;
     const long long works = ((long long)a.rows / np + a.requests) * a.heads;
-    // CTAs of a tile: as many, up to sixteen, as fill the GPU twice with four key tiles each
     const long long tiles = (long long)a.heads * a.requests * (((long long)a.rows / a.requests + np - 1) / np + (a.rows < a.requests));
-    int C = 1;
-    while (C < kMaxCluster && tiles * 2 * C <= 2 * kSMs && (long long)a.k_rows / a.requests >= 4 * kKeys * 2 * C) C *= 2;
+    const int C = key_cluster(tiles, (long long)a.k_rows / a.requests, 2, 4 * kKeys);
     if (works * C > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -39,7 +39,6 @@ constexpr int kT = 128;
 constexpr int kThreads = 384;
 constexpr uint32_t kBox = kT * 64 * 2;             // 128 rows x 64 channels: 16 KB
 constexpr float kRaise = 8.f;
-constexpr int kMaxCluster = 16;
 constexpr int kSteps = 2, kStep = kT / kSteps;     // S and P go by two parts of a tile
 
 template <int D, bool SPLIT> struct Cfg {
@@ -210,6 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         S.abort = (smem_u32(raw) & 1023u) != 0;          // (the swizzle goes by address bits; there is no other shared memory, so it is 0)
         fence_mbar_init();
     }
+    if (warp == 0 && lane < 4) {
+        const CUtensorMap* map = lane == 0 ? &mapQ : lane == 1 ? &mapK : lane == 2 ? &mapV : &mapO;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+    }
     if (warp == 1) {
         tmem_alloc(&S.tmem, 512);
         tmem_relinquish();
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m.nq = q1 - m.q0;
             m.all = k1 - m.k0;
             const long long p = (long long)(x - (m.q0 / pair + i)) * pair;
-            if (p >= m.nq) continue;
+            if (p < 0 || p >= m.nq) continue;
             m.p = (int)p;
             m.h = w % A.heads;
             const int seen = max(0, min(m.all, m.all - m.nq + min(m.nq, m.p + pair))), tiles = (seen + kT - 1) / kT;
@@ -767,10 +770,9 @@ cudaError_t go(const PackedArgs& a, cudaStream_t st)
         !rows_map(&mv, a.v, D, a.heads, a.k_rows, a.v_stride, 1, kT))
         return cudaErrorInvalidValue;
     const long long works = ((long long)a.rows / (2 * np) + a.requests) * a.heads;
-    // Where there are fewer items than SMs, a cluster of CTAs for each, with at least four key tiles a CTA.
+    // where there are fewer items than SMs, a cluster of CTAs for each
     const long long items = (long long)a.heads * a.requests * (((long long)a.rows / a.requests + 2 * np - 1) / (2 * np) + (a.rows < a.requests));
-    int C = 1;
-    while (C < kMaxCluster && items * 2 * C <= kSMs && (long long)a.k_rows / a.requests >= 4 * kT * 2 * C) C *= 2;
+    const int C = key_cluster(items, (long long)a.k_rows / a.requests, 1, 2 * kT);
     if (works * C > INT32_MAX) return cudaErrorInvalidValue;
     if (C > 1) {
         const auto kernel = prompt_tc_kernel<D, true>;

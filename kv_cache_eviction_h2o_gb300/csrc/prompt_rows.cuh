@@ -49,7 +49,7 @@ __device__ __forceinline__ int request_at(const PackedArgs& A, int x, int per)
     const int lane = threadIdx.x & 31;
     auto f = [&](int i) { return min(max(A.q_start[i], 0), A.rows) / per + i; };
     int lo = 0, hi = A.requests;
-    if (f(0) > x) return -1;
+    if (hi > 1 && f(0) > x) return -1;                     // (one request: its caller sees to it)
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, i = lo + lane * step;
         const unsigned in = __ballot_sync(0xffffffffu, i < hi && f(i) <= x);
@@ -58,6 +58,18 @@ __device__ __forceinline__ int request_at(const PackedArgs& A, int x, int per)
         hi = min(hi, lo + step);
     }
     return lo;
+}
+
+// CTAs of a cluster that shares a tile's keys: as many as leave all `items` clusters at once on the GPU, per_sm CTAs an
+// SM, and each CTA `least` keys.  (A cluster's CTAs are on one group of SMs, of which there are eight: 16 of 7 or more CTAs, or
+// 32 of 5, take turns.  5 queries behind 20000 tokens of 8 heads: 138 us with one CTA, 26 with eight, 24 with twelve, 45 with
+// sixteen.)
+inline int key_cluster(long long items, long long keys, int per_sm, int least)
+{
+    constexpr int size[] = {16, 12, 8, 6, 4, 3, 2}, fit[] = {7, 8, 15, 22, 36, 48, 76};
+    for (int i = 0; i < 7; ++i)
+        if (items <= (long long)fit[i] * per_sm && keys >= (long long)least * size[i]) return size[i];
+    return 1;
 }
 
 }  // namespace h2o
