@@ -618,8 +618,10 @@ int h2o_rope(const void* q, long long q_stride, void* q_out, long long q_out_str
  *   or keys are none of the call's.  With starts that descend, which rows are
  *   written is not defined; nothing else is.
  * A row all of whose logits are -inf is zero.  Keys and values a query does not
- * see do not touch it, whatever they hold.  rows, k_rows <= 2^24, rows * kv_heads
- * * groups and k_rows * kv_heads <= 2^28, 1 <= requests <= 16384.
+ * see do not touch it, whatever they hold (a row that an infinity or NaN among its
+ * tile's values makes no number is made again from its own keys, by one warp).
+ * rows, k_rows <= 2^24, rows * kv_heads * groups and k_rows * kv_heads <= 2^28,
+ * 1 <= requests <= 16384, requests * kv_heads <= 2^22.
  */
 int h2o_prompt_attend(const void* q, long long q_stride, int rows, const void* k, long long k_stride, const void* v,
                       long long v_stride, int k_rows, int kv_heads, int groups, int head_dim, int dtype,
@@ -658,12 +660,14 @@ int h2o_page_quant_read(const void* K, const void* V, const float* kscale, const
  * h2o_page_quant_attend -- attention over whole quantised paged caches: row r
  * sees the tokens 0..row_pos[r] of request row_seq[r],
  *   out = softmax(scale q.K) V,  K = kscale * codes, V = vscale * codes.
- * Codes are multiplied as they are (exact in fp16, scales apart in fp32); queries are multiplied
- * as fp16 numbers with a power of two apart, two of them where dtype is H2O_F32
- * (off by 2^-23 of the row's largest at most; bf16 by 2^-25), and weights, with the value's
- * scale and a power of two apart, as one fp16 number (2^-12 of each off at most) or,
- * with H2O_F32, two (2^-23).  Other arguments,
- * padding rows, empty rows and bad entries as h2o_page_attend.
+ * Codes are multiplied as they are (exact in fp16), scales apart in fp32 (none is
+ * negative); queries as fp16 numbers with a power of two of the row apart, two of
+ * them where dtype is H2O_F32 (off by 2^-23 of the row's largest at most), and
+ * weights, with the value's scale and a power of two apart, as one fp16 number
+ * (2^-12 of each off at most) or, with H2O_F32, two (2^-23).  A query head that
+ * holds an infinity or a NaN, or whose largest value times scale passes 2^114, is
+ * NaN.  Other arguments, padding rows, empty rows and bad entries as
+ * h2o_page_attend.
  */
 int h2o_page_quant_attend(const void* q, long long q_stride, const int* row_seq, const int* row_pos, int rows,
                           const void* K, const void* V, const float* kscale, const float* vscale, int num_pages,

@@ -167,6 +167,7 @@ int h2o_prompt_attend(const void* q, long long q_stride, int rows, const void* k
         return set_last_error(H2O_ERR_ARG, "requests must be in [1, %d] (got %d)", kMaxPromptRequests, requests);
     if ((long long)rows * kv_heads > (1 << 28) / groups || (long long)k_rows * kv_heads > 1 << 28)
         return set_last_error(H2O_ERR_ARG, "rows * kv_heads * groups and k_rows * kv_heads must be at most 2^28");
+    if ((long long)requests * kv_heads > 1 << 22) return set_last_error(H2O_ERR_ARG, "requests * kv_heads must be at most 2^22");
     PackedArgs a = {};
     a.qscale = (float)(scale * 1.4426950408889634);
     if (!(scale > 0.0) || !std::isfinite(scale)) return set_last_error(H2O_ERR_ARG, "scale must be finite and > 0");

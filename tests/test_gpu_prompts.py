@@ -177,8 +177,7 @@ def _softmax_rows(q, k, v, scale, seen):
     else:
         for x in range(n):
             m = int(seen[x])
-            y[x] = p[x, :m] @ v0[:m]
-        av = y.abs()
+            y[x], av[x] = p[x, :m] @ v0[:m], p[x, :m] @ v0[:m].abs()
     s = scale * (q.abs() @ k0.abs().T).masked_fill(hide, 0.0).amax(1, keepdim=True)
     return y, av, z.masked_fill(hide, 0.0).abs().amax(1, keepdim=True), s
 
@@ -374,6 +373,28 @@ def test_prompt_few_queries_behind_many_keys(dtype, before, new):
         _inside(_prompt(q, k, v, [0, new], [0, before + new], d ** -0.5), *_prompt_ref(q, k, v, [0, new], [0, before + new], d ** -0.5))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("G,d", [(1, 128), (4, 64), (7, 128)])
+def test_prompt_few_unequal_requests_with_many_keys(dtype, G, d):
+    # long and short key ranges shared by several CTAs, requests without queries, keys or either, rows that see none
+    new, keys = [5, 10, 0, 3, 1, 40], [6000, 4, 100, 0, 3001, 777]
+    q, k, v = _packed(sum(new), sum(keys) + 30, 1, G, d, dtype, G)
+    k[-30:], v[-30:] = float("nan"), float("inf")
+    qs, ks = _starts(new), _starts(keys)
+    out = _prompt(q, k, v, qs, ks, d ** -0.5)
+    _inside(out, *_prompt_ref(q, k, v, qs, ks, d ** -0.5))
+    assert (out[5:11] == 0).all() and (out[15:18] == 0).all()
+    # values that are no numbers, before and after what a row sees
+    v[5998], v[9105 + 770] = float("inf"), float("nan")
+    y, tol = _prompt_ref(q, k, v, qs, ks, d ** -0.5)
+    out = _prompt(q, k, v, qs, ks, d ** -0.5)
+    clean = torch.ones(sum(new), dtype=torch.bool)
+    clean[3:5] = False                                     # the rows from those keys on
+    clean[19 + 33:] = False
+    _inside(out[clean], y[clean], tol[clean])
+    assert not out[3:5].isfinite().any()
+
+
 def test_prompt_offsets_beyond_32_bits():
     # 2^31 elements lie before the request's keys
     keys, heads, d, n = (1 << 19) + 300, 32, 128, 200
@@ -486,6 +507,43 @@ def test_quantised_write_and_read(dtype, bits, heads, d, ps, rows):
     fine = amax.isfinite() & (amax > 1e-36)
     near = step * (0.5 + 2.0 ** -14) + (2.0 ** -8 * (k[live].double().abs() + step) if dtype is BF16 else 0)
     assert (torch.where(fine, off - near, torch.full_like(off, -1.0)) <= 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("heads,d,ps,rows", [(7, 128, 64, 24000), (100, 64, 16, 3100), (1, 64, 32, 200001), (8, 128, 128, 20003)])
+def test_quantised_many_rows(dtype, bits, heads, d, ps, rows):
+    # several rows a thread; the rule's steps as torch's (a tensor over a tensor is one rounding)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    pages = -(-rows // ps) + 1
+    slot = torch.randperm(pages * ps, generator=g, device="cuda")[:rows].to(torch.int32)
+    slot[::97] = -1
+    k, v = (torch.randn(rows, heads, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    k[5], v[7, 0, 3], k[11, 0, 0], v[13] = 0.0, float("nan"), float("inf"), 1e-38
+    p = Pool(pages, heads, ps, d, bits)
+    L.h2o_page_quant_write(k, v, slot, *p.args())
+    live = slot >= 0
+    at = slot[live].long()
+    back = [torch.full_like(k, 7.0) for _ in range(2)]
+    L.h2o_page_quant_read(*p.args(), slot, *back)
+    for x, pool, scales, got in ((k, p.K, p.ks, back[0]), (v, p.V, p.vs, back[1])):
+        x = x[live].float()
+        amax = x.abs().amax(-1, keepdim=True)
+        odd = ~amax.isfinite()
+        top = torch.full_like(amax, 2 ** (bits - 1) - 1)
+        inv = torch.where(amax > 0, top / amax, 0.0)
+        code = torch.where(odd, 0.0, torch.round(x * inv).nan_to_num().clamp(-top, top))
+        scale = torch.where(odd, torch.nan, amax / top)[..., 0]
+        stored = pool[at // ps, :, at % ps]
+        if bits == 4:
+            stored = torch.stack([stored & 15, stored >> 4], -1).flatten(-2).float() - 8
+        assert torch.equal(stored.float(), code)
+        assert torch.equal(scales[at // ps, :, at % ps].nan_to_num(-1.0), scale.nan_to_num(-1.0))
+        assert torch.equal(got[live].nan_to_num(-1.0), (code * scale[..., None]).to(dtype).nan_to_num(-1.0))
+        assert (got[~live] == 7).all()
+    rest = torch.ones(pages * ps, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert (p.ks.transpose(1, 2).reshape(-1, heads)[rest] == 9.0).all() and (p.K.transpose(1, 2).reshape(pages * ps, -1)[rest] == 0x55).all()
 
 
 def test_quantised_rows_strided_on_another_stream():
@@ -673,6 +731,37 @@ def test_attend_large_logits_and_special_values(dtype, bits):
     q[0, 1, 3], q[1, 0, 0] = float("nan"), float("inf")
     out = _attend(c, q[:2], [0, 0], [90, 90], 0.5)
     assert out[0, 1].isnan().all() and out[1, 0].isnan().all() and out[0, [0, 2, 3]].isfinite().all() and out[1, 1:].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", [300, 4096, 16384])
+@pytest.mark.parametrize("requests,heads", [(2, 3), (40, 4), (150, 8)])
+def test_attend_tables_much_wider_than_the_requests(dtype, width, requests, heads):
+    lengths = [(i * 53) % 700 + 1 for i in range(requests)]
+    c = Cache(lengths, heads, 64, 16, 4, seed=width, width=width)
+    q = _queries(requests, 2 * heads, 64, dtype, 3)
+    pos = [n - 1 for n in lengths]
+    out = _attend(c, q, list(range(requests)), pos, 0.1)
+    at = list(range(0, requests, 17))
+    y, tol = _attend_ref(c, q[at], at, [pos[i] for i in at], 0.1)
+    _inside(out[at], y, tol)
+
+
+def test_attend_captured_and_replayed():
+    c = Cache([400, 90], 2, 128, 32, 8, seed=3, width=40)
+    pool, table = c.pool(), _i32(c.table)
+    q, seq, pos = _queries(2, 8, 128, BF16, 1).cuda(), _i32([0, 1]), _i32([10, 20])
+    out = torch.empty_like(q)
+    L.h2o_page_quant_attend(q, seq, pos, *pool, table, 0.1, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.h2o_page_quant_attend(q, seq, pos, *pool, table, 0.1, out)
+    for a, b in ((399, 89), (0, -1), (200, 33)):
+        pos.copy_(_i32([a, b]))
+        graph.replay()
+        torch.cuda.synchronize()
+        _inside(out, *_attend_ref(c, q.cpu(), [0, 1], [a, b], 0.1))
 
 
 @pytest.mark.parametrize("bits,pages", [(8, 70000), (4, 140000)])

@@ -72,7 +72,7 @@ def test_rope_takes_slices_of_one_buffer(L):
     (dict(dtype=3), "dtype"), (dict(d=80), "head_dim"), (dict(rows=-1), "rows"), (dict(krows=-1), "rows"), (dict(heads=0), "kv_heads"),
     (dict(heads=65536), "kv_heads"), (dict(groups=0), "groups"), (dict(groups=17), "groups"), (dict(n=0), "requests"), (dict(n=16385), "requests"),
     (dict(rows=(1 << 24) + 1), "2^24"), (dict(krows=(1 << 24) + 1), "2^24"), (dict(rows=1 << 23, groups=16, heads=4), "2^28"),
-    (dict(krows=1 << 24, heads=32), "2^28"), (dict(scale=0.0), "scale"), (dict(scale=float("inf")), "scale"),
+    (dict(krows=1 << 24, heads=32), "2^28"), (dict(n=16384, heads=257, rows=1, krows=1, qs=257 * 512, os=257 * 512, ks=257 * 128, vs=257 * 128), "2^22"), (dict(scale=0.0), "scale"), (dict(scale=float("inf")), "scale"),
     (dict(scale=1e-60), "scale"), (dict(qst=None), "q_start"), (dict(kst=FAKE + 2), "k_start"), (dict(q=None), "non-NULL"), (dict(v=None), "non-NULL"),
     (dict(out=4 * MB + 8), "aligned"), (dict(qs=1000), "apart"), (dict(vs=257), "boundaries"), (dict(out=1 * MB), "overlaps"),
     (dict(out=2 * MB + 512), "overlaps"), (dict(out=3 * MB), "overlaps"),
