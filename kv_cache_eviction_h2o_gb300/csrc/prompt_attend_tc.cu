@@ -7,10 +7,11 @@
 //   S = Q K^T        (SMEM x SMEM -> TMEM, M = 128, K = D)
 //   P = 2^(c S - m)  (128 threads a stream, thread = TMEM lane = query row)
 //   O += P V         (TMEM x SMEM -> TMEM, M = 128, N = D)
-// one for each query tile over the same keys; where a request has queries for one tile only,
-// for the even and the odd key tiles of that one, joined at the end.  S and P go
-// by halves of 64 keys, so that neither the threads nor the products wait for
-// the other's latency.
+// one for each query tile over the same keys; where a request has queries for one
+// tile only, for the even and the odd key tiles of that one, joined at the end.  S
+// and P go by parts of 64 keys: S has one place, given back as soon as the threads
+// have it in registers, and P two, so that the next part's scores are made while
+// the threads are at this one's weights.
 //
 // CTAs are persistent, one an SM: warp 3 finds the items (a request's longest
 // rows first), warp 0 loads queries, keys and values with TMA, warps 1 and 2
@@ -64,7 +65,7 @@ struct alignas(1024) Smem {
     uint8_t ring[C::kSlots][C::kTile];
     uint8_t out[8][C::kStage];
     uint64_t full[C::kSlots], empty[C::kSlots];
-    uint64_t q_full, q_empty, s_ready[2][kSteps], p_ready[2][kSteps], pv_done[2][kSteps], o_free[2], last;   // [stream][part of the tile]
+    uint64_t q_full, q_empty, s_ready[2], s_free[2], p_ready[2][2], pv_done[2][2], o_free[2], last;   // [stream][place of P]
     uint64_t item_full[2], item_empty[2], joined, taken;
     alignas(16) uint4 taken_at;
     float2 ml[2][kT];
@@ -194,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&S.q_full, 1);
         mbar_init(&S.q_empty, 2);
         for (int s = 0; s < 2; ++s) {
-            for (int b = 0; b < kSteps; ++b) {
-                mbar_init(&S.s_ready[s][b], 1);
+            mbar_init(&S.s_ready[s], 1);
+            mbar_init(&S.s_free[s], 4);
+            for (int b = 0; b < 2; ++b) {
                 mbar_init(&S.p_ready[s][b], 4);
                 mbar_init(&S.pv_done[s][b], 1);
             }
@@ -221,7 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
+    // a stream's scores of one part, its weights of two, its sums
     auto tS = [&](int s) { return tmem + (uint32_t)(s * kT); };
+    auto tP = [&](int s, int i) { return tmem + (uint32_t)(s * kT + kStep + (i & 1) * (kStep / 2)); };
     auto tO = [&](int s) { return tmem + (uint32_t)(2 * kT + s * D); };
 
     // each role's walk through the items; false: no more
@@ -241,6 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto keys_of = [&](int s) {
         const int end = min(it.nq, it.p + (it.p + np < it.nq ? s + 1 : 1) * np);
         return max(0, min(it.nk, it.all - it.nq + end - it.before));
+    };
+    // parts of the tiles first, first + stride, .. that hold keys
+    auto parts_of = [&](int keys, int first, int stride) {
+        const int n = (keys + kT - 1) / kT, nt = n > first ? (n - first + stride - 1) / stride : 0;
+        return kSteps * nt - (nt > 0 && keys - (first + (nt - 1) * stride) * kT <= kStep ? 1 : 0);
     };
     const int C = SPLIT ? (int)cluster_nctarank() : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
 
@@ -353,45 +362,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t k0 = sw128_desc(S.ring[0]), v0 = value_desc(S.ring[0]);
         const uint32_t sS = tS(s), sO = tO(s);
         bool ok = true;
-        int at = 0, queries = 0, outs = 0, part0 = 0, part1 = 0;   // ring tiles, items, results, first and second parts of tiles of this stream so far
+        int at = 0, queries = 0, outs = 0, done = 0;     // ring tiles, items, results and parts of this stream so far
         while (next()) {
             if (!ok || aborted() || it.n == 0) continue;
             const bool two = it.p + np < it.nq;
             const uint64_t q0 = sw128_desc(S.q[two ? s : 0]);
-            const int L = two ? 1 : 2, keys = keys_of(s), n = (keys + kT - 1) / kT;
+            const int L = two ? 1 : 2, first = two ? 0 : s, stride = two ? 1 : 2, keys = keys_of(s), ni = parts_of(keys, first, stride);
             const int base = at;
             at += 2 * it.n;
             ok = __all_sync(0xffffffffu, wait(S, &S.q_full, queries));
             ++queries;
-            auto slot_full = [&](int i) {
-                if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.full[i % NS], i / NS));
-            };
             auto release = [&](int i) {                  // when all products so far are done
                 if (ok) commit(on, &S.empty[i % NS]);
             };
-            // scores of part b of the tile in place i, of which `valid` keys are seen
-            auto score = [&](int b, int i, int valid) {
-                if (!ok || valid <= kStep * b) return;
+            // The ring's tiles in their order: those before x that are the other stream's, or whose keys no row of this one sees, go back.
+            int r = base;
+            auto reach = [&](int x) {
+                for (; ok && r <= x; ++r) {
+                    ok = __all_sync(0xffffffffu, wait(S, &S.full[r % NS], r / NS));
+                    if (r < x) release(r);
+                }
+            };
+            // where in the ring: K(t) and V(t)
+            auto k_place = [&](int t) { return base + (t < L ? t : v_at(t - L, it.n, L) + 1); };
+            auto v_place = [&](int t) { return base + v_at(t, it.n, L); };
+            // scores of part i, in the place of those of part i - 1
+            auto score = [&](int i) {
+                const int b = i % kSteps, k_at = k_place(first + i / kSteps * stride);
+                reach(k_at);
+                if (ok && done + i > 0) ok = __all_sync(0xffffffffu, wait(S, &S.s_free[s], done + i - 1));
+                if (!ok) return;
                 tc_fence_after();
-                const uint64_t k = k0 + (uint64_t)((uint32_t)(i % NS) * (C_::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
+                const uint64_t k = k0 + (uint64_t)((uint32_t)(k_at % NS) * (C_::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const uint64_t off = (uint64_t)(((uint32_t)(x / 4) * kBox + (uint32_t)(x % 4) * 32u) >> 4);
-                    mma_ss(on, sS + (uint32_t)(kStep * b), q0 + off, k + off, kIdesc<kStep, false>, x > 0);
+                    mma_ss(on, sS, q0 + off, k + off, kIdesc<kStep, false>, x > 0);
                 }
-                commit(on, &S.s_ready[s][b]);
+                commit(on, &S.s_ready[s]);
+                if (b == kSteps - 1 || i + 1 == ni) release(k_at);
+                if (i + 1 == ni) commit(on, &S.q_empty);
             };
-            // nth: tiles of this stream before in this item; valid: its keys of the tile
-            auto values = [&](int b, int nth, int i, int valid) {
-                if (!ok || valid <= kStep * b) return;
-                ok = __all_sync(0xffffffffu, wait(S, &S.p_ready[s][b], b ? part1++ : part0++));
+            auto values = [&](int i) {
+                const int b = i % kSteps, t = first + i / kSteps * stride, v_at_ = v_place(t), gi = done + i;
+                reach(v_at_);
+                if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.p_ready[s][gi & 1], gi >> 1));
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t v = v0 + (uint64_t)((uint32_t)(i % NS) * (C_::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
-                const int nk = (min(kStep, valid - kStep * b) + 15) / 16;
+                const uint64_t v = v0 + (uint64_t)((uint32_t)(v_at_ % NS) * (C_::kTile >> 4) + (uint32_t)b * (kStep * 128u >> 4));
+                const uint32_t p = tP(s, gi);
+                const int nk = (min(kStep, keys - t * kT - kStep * b) + 15) / 16;
                 auto one = [&](int x) {
-                    mma_ts(on, sO, sS + (uint32_t)(kStep * b + 8 * x), v + (uint64_t)((uint32_t)x * 2048u >> 4), kIdesc<D, true>,
-                           nth > 0 || b > 0 || x > 0);
+                    mma_ts(on, sO, p + (uint32_t)(8 * x), v + (uint64_t)((uint32_t)x * 2048u >> 4), kIdesc<D, true>, i > 0 || x > 0);
                 };
                 if (nk == kStep / 16) {
 #pragma unroll
@@ -399,42 +421,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     for (int x = 0; x < nk; ++x) one(x);
                 }
-                commit(on, &S.pv_done[s][b]);
+                commit(on, &S.pv_done[s][gi & 1]);
+                if (b == kSteps - 1 || i + 1 == ni) release(v_at_);
             };
-            // where in the ring: K(t) and V(t)
-            auto k_place = [&](int t) { return base + (t < L ? t : v_at(t - L, it.n, L) + 1); };
-            auto v_place = [&](int t) { return base + v_at(t, it.n, L); };
-            // The tiles in the ring's order; those that are the other stream's, or whose keys no row of this one sees, go back at once.
-            auto mine = [&](int t) { return t < n && (two || (t & 1) == s); };
-            bool freed = false;                          // the last result has left O
-            for (int t = 0; t < min(L, it.n); ++t) {
-                slot_full(k_place(t));
-                if (mine(t))
-                    for (int b = 0; b < kSteps; ++b) score(b, k_place(t), keys - t * kT);
-                release(k_place(t));
-            }
-            if (it.n <= L && ok) commit(on, &S.q_empty);
-            int nth = 0;
-            for (int t = 0; t < it.n; ++t) {
-                const bool more = t + L < it.n;
-                const int v = v_place(t), k = v + 1;
-                slot_full(v);
-                if (more) slot_full(k);
-                const bool values_mine = mine(t), scores_mine = more && mine(t + L);
-                if (values_mine && !freed) {
+            if (ni > 0) score(0);
+            for (int i = 0; i < ni; ++i) {
+                if (i + 1 < ni) score(i + 1);
+                if (i == 0) {                            // the last result has left O
                     if (ok && outs) ok = __all_sync(0xffffffffu, wait(S, &S.o_free[s], outs - 1));
-                    freed = true;
                     ++outs;
                 }
-                for (int b = 0; b < kSteps; ++b) {
-                    if (values_mine) values(b, nth, v, keys - t * kT);
-                    if (scores_mine) score(b, k, keys - (t + L) * kT);
-                }
-                release(v);
-                if (more) release(k);
-                if (t + L + 1 == it.n && ok) commit(on, &S.q_empty);   // the item's last scores
-                if (values_mine) ++nth;
+                values(i);
             }
+            done += ni;
+            reach(base + 2 * it.n - 1);
+            // (reach leaves the last tile to its caller; it is V's last, this stream's or not)
+            if (ok && (ni == 0 || v_place(first + (ni - 1) / kSteps * stride) != base + 2 * it.n - 1)) release(base + 2 * it.n - 1);
+            if (ni == 0 && ok) commit(on, &S.q_empty);
         }
         // everything issued is done before TMEM is given back
         commit(on, &S.last);
@@ -445,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
         const float c2 = A.qscale;
         const int prow = row / G, g = row - prow * G;    // position and head of the row within its tile
-        int part0 = 0, part1 = 0, meets = 0;             // first and second parts of tiles of this stream so far
-        auto parts = [&](int b) { return b ? part1 : part0; };
+        int done = 0, meets = 0;                         // parts of this stream so far
         bool ok = true;
         // all softmax warps, and what they have written
         auto meet = [&]() {
@@ -462,26 +464,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = it.p + (two ? s * np : 0) + prow;
             const bool live = row < np * G && pos < it.nq;
             const int sees = min(it.nk, it.all - it.nq + pos + 1 - it.before);    // keys of this row in the range (not live: of no matter)
-            const int keys = keys_of(s), n = (keys + kT - 1) / kT, first = two ? 0 : s, stride = two ? 1 : 2;
-            const int nt = n > first ? (n - first + stride - 1) / stride : 0;    // this stream's tiles
+            const int keys = keys_of(s), first = two ? 0 : s, stride = two ? 1 : 2, nt = parts_of(keys, first, stride);
             float m = -INFINITY, l = 0.f;
             if (ok && aborted()) ok = false;
-            // (a last part that no row sees is left out)
-            const int ni = kSteps * nt - (nt > 0 && keys - (first + (nt - 1) * stride) * kT <= kStep ? 1 : 0);
-            for (int i = 0; i < ni && ok; ++i) {
-                const int nth = i / kSteps, b = i % kSteps, t = first + nth * stride, j0 = t * kT + kStep * b;
-                const uint32_t at = tS(s) + lanes + (uint32_t)(kStep * b);
-                // (a part's last product is done before its new scores are made, so the second look never waits; it is there to
-                // see every phase)
-                ok = __all_sync(0xffffffffu, wait(S, &S.s_ready[s][b], parts(b) + nth) && (nth == 0 || wait(S, &S.pv_done[s][b], parts(b) + nth - 1)));
+            for (int i = 0; i < nt && ok; ++i) {
+                const int b = i % kSteps, t = first + i / kSteps * stride, j0 = t * kT + kStep * b, gi = done + i;
+                ok = __all_sync(0xffffffffu, wait(S, &S.s_ready[s], gi));
                 if (!ok) break;
                 tc_fence_after();
                 constexpr int NC = kStep / 32;
                 uint32_t z[NC][32];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) tc_ld32_issue(at + 32u * c, z[c]);
+                for (int c = 0; c < NC; ++c) tc_ld32_issue(tS(s) + lanes + 32u * c, z[c]);
 #pragma unroll
                 for (int c = 0; c < NC; ++c) tc_ld32_wait(z[c]);
+                // the next part's scores may take their place
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.s_free[s]);
                 const int valid = sees - j0;
                 if (__any_sync(0xffffffffu, valid < kStep)) {
 #pragma unroll
@@ -504,6 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     top = max3f(top, mx[0], mx[1]);
                 }
+                // the weights' place: those of the part before the last have been multiplied
+                if (i > 1) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][gi & 1], (gi >> 1) - 1));
+                if (!ok) break;
                 top *= c2;
                 const bool raise = top > m + kRaise;                 // (m = -inf: any finite logit)
                 if (__any_sync(0xffffffffu, raise)) {
@@ -513,8 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l *= a;
                     }
                     if (i > 0) {
-                        // (all products but the last are done)
-                        ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][(i - 1) % kSteps], parts((i - 1) % kSteps) + (i - 1) / kSteps));
+                        ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][(gi - 1) & 1], (gi - 1) >> 1));   // (all before it are done)
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[k & 1] = __fadd2_rn(sum[k & 1], x);
                         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[k]) : "f"(x.y), "f"(x.x));
                     }
-                    tc_st16(at + 16u * c, p);
+                    tc_st16(tP(s, gi) + lanes + 16u * c, p);
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 // value rows behind the request's last key in its group of 16: zeros (both streams may write them, each before
@@ -559,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&S.p_ready[s][b]);
+                if (lane == 0) mbar_arrive(&S.p_ready[s][gi & 1]);
             }
-            part0 += (ni + 1) / 2;
-            part1 += ni / 2;
-            for (int b = 0; b < kSteps; ++b)
-                if (ok && ni > b) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][b], parts(b) - 1));
+            // all products are done (each phase is looked at)
+            for (int i = max(0, nt - 2); i < nt; ++i)
+                if (ok) ok = __all_sync(0xffffffffu, wait(S, &S.pv_done[s][(done + i) & 1], (done + i) >> 1));
             tc_fence_after();
+            done += nt;
 
             // ------------------------------------------------ results
             // One query tile: both streams' sums, half of the channels each.
