@@ -619,7 +619,8 @@ int h2o_rope(const void* q, long long q_stride, void* q_out, long long q_out_str
  *   written is not defined; nothing else is.
  * A row all of whose logits are -inf is zero.  Keys and values a query does not
  * see do not touch it, whatever they hold (a row that an infinity or NaN among its
- * tile's values makes no number is made again from its own keys, by one warp).
+ * tile's values makes no number is made again from its own keys, by one warp).  The
+ * sum of a row's values by weights whose largest is 1 has to stay within fp32.
  * rows, k_rows <= 2^24, rows * kv_heads * groups and k_rows * kv_heads <= 2^28,
  * 1 <= requests <= 16384, requests * kv_heads <= 2^22.
  */

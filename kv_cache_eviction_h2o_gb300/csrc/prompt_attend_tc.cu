@@ -22,10 +22,10 @@
 // l are of the unrounded weights.
 //
 // Keys that a row does not see have the weight 0, which leaves a row as it is
-// unless their values are infinite or NaN: a row whose result is no number is
-// made again from the keys it sees alone (prompt_row).  Value rows behind a
-// request's last, which may be anything, are zeroed in shared memory.  Waits are
-// bounded; one that runs out leaves NaN.
+// unless their values are infinite or NaN: a row whose result is no number, and
+// not by its own values' doing, is made again from the keys it sees alone
+// (prompt_row).  Value rows behind a request's last, which may be anything, are
+// zeroed in shared memory.  Waits are bounded; one that runs out leaves NaN.
 #include <algorithm>
 
 #include "paged.h"
@@ -72,6 +72,7 @@ struct alignas(1024) Smem {
     Item item[2];
     uint32_t tmem;
     int abort, any;                    // any: there was an item
+    int patience;                      // log2 of the cycles that a wait may take
 };
 static_assert(sizeof(Smem<128, false>) <= 227 * 1024 && sizeof(Smem<128, true>) <= 227 * 1024, "one CTA's shared memory");
 
@@ -165,11 +166,17 @@ __device__ __forceinline__ uint64_t value_desc(const void* p)
 // every barrier's phases are seen.  V(t)'s place:
 __device__ __forceinline__ int v_at(int t, int n, int L) { return t + min(n, t + L); }
 
+// At most a second, or 2^39 cycles once rows have been made again, which takes up to 32 x 2^24 keys of 270 to 820 cycles.
 template <class Shared>
 __device__ __forceinline__ bool wait(Shared& S, uint64_t* bar, int count)
 {
     // the barrier's phase number `count` (from 0)
-    if (mbar_wait(bar, (uint32_t)count & 1u)) return true;
+    const uint32_t parity = (uint32_t)count & 1u;
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+    } while ((clock64() - t0) >> *(volatile int*)&S.patience == 0);
     *(volatile int*)&S.abort = 1;
     return false;
 }
@@ -208,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&S.last, 2);
         mbar_init(&S.joined, 8);
         mbar_init(&S.taken, 1);
+        S.patience = 31;
         S.abort = (smem_u32(raw) & 1023u) != 0;          // (the swizzle goes by address bits; there is no other shared memory, so it is 0)
         fence_mbar_init();
     }
@@ -676,16 +684,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0 && nt > 0) mbar_arrive(&S.o_free[s]);
             }
             __syncwarp();
-            // rows whose result is no number: what they do not see may have made it so
-            while (redo) {
-                const int r = __ffs(redo) - 1;
-                redo &= redo - 1;
-                const int rp = __shfl_sync(0xffffffffu, pos, r), rg = __shfl_sync(0xffffffffu, g, r), rn = __shfl_sync(0xffffffffu, sees, r);
-                const long long qrow = it.q0 + rp;
-                prompt_row<__nv_bfloat16, D>(static_cast<const __nv_bfloat16*>(A.q) + qrow * A.q_stride + (it.h * G + rg) * D,
-                                             static_cast<const __nv_bfloat16*>(A.k) + it.k0 * A.k_stride + it.h * D, A.k_stride,
-                                             static_cast<const __nv_bfloat16*>(A.v) + it.k0 * A.v_stride + it.h * D, A.v_stride, rn, c2,
-                                             static_cast<__nv_bfloat16*>(A.out) + qrow * A.out_stride + (it.h * G + rg) * D);
+            // Rows whose result is no number: values that they do not see may have made it so, or the sum of finite ones, whose
+            // weights here are up to 2^8, passed fp32's range.  Where neither is the case it stands.
+            if (redo) {
+                *(volatile int*)&S.patience = 39;
+                const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v) + it.k0 * A.v_stride + it.h * D;
+                const int last = last_odd<__nv_bfloat16, D>(v, A.v_stride, min(it.all, (keys + 15) & ~15));
+                if (last >= 0) redo &= __ballot_sync(0xffffffffu, sees <= last);
+                while (redo) {
+                    const int r = __ffs(redo) - 1;
+                    redo &= redo - 1;
+                    const int rp = __shfl_sync(0xffffffffu, pos, r), rg = __shfl_sync(0xffffffffu, g, r), rn = __shfl_sync(0xffffffffu, sees, r);
+                    const long long qrow = it.q0 + rp;
+                    prompt_row<__nv_bfloat16, D>(static_cast<const __nv_bfloat16*>(A.q) + qrow * A.q_stride + (it.h * G + rg) * D,
+                                                 static_cast<const __nv_bfloat16*>(A.k) + it.k0 * A.k_stride + it.h * D, A.k_stride, v, A.v_stride,
+                                                 rn, c2, static_cast<__nv_bfloat16*>(A.out) + qrow * A.out_stride + (it.h * G + rg) * D);
+                }
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

@@ -41,6 +41,27 @@ __device__ __noinline__ void prompt_row(const T* q, const T* k, long long kstrid
     }
 }
 
+// The last of the rows 0 .. n - 1 from v on that holds an infinity or a NaN, or -1: by one warp.
+template <typename T, int D>
+__device__ __noinline__ int last_odd(const T* v, long long stride, int n)
+{
+    constexpr int E = D / 32, U = 8;
+    const int lane = threadIdx.x & 31;
+    for (int j = n - 1; j >= 0; j -= U) {
+        unsigned odd = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float x[E];
+            load_vec<T, E>(v + (long long)max(j - u, 0) * stride + lane * E, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) odd |= fabsf(x[e]) < INFINITY ? 0u : 1u << u;
+        }
+        odd = __reduce_or_sync(0xffffffffu, odd);
+        if (odd) return max(j - (__ffs(odd) - 1), 0);
+    }
+    return -1;
+}
+
 // The request of work index x, by the whole warp: the last i with f(i) = q_start[i] / per + i <= x, or -1.  f's values
 // leave room for every tile of `per` positions of a request before the next one's, f(i + 1) - f(i) >= ceil(length / per),
 // so x - f(i) is the tile of request i if it has as many, and all requests' tiles are within rows / per + requests.

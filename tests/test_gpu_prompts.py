@@ -295,6 +295,49 @@ def test_prompt_flat_and_large_logits(dtype, spread):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_prompt_numbers_that_are_none_stay_in_their_channel(dtype):
+    # NaN among a row's own values, and among those of its tile that it does not see
+    n, d, heads, G = 700, 64, 2, 4
+    q, k, v = _packed(n, n, heads, G, d, dtype, 12)
+    y, tol = _prompt_ref(q, k, v, [0, n], [0, n], d ** -0.5)
+    none = torch.zeros(n, heads, d, dtype=torch.bool)
+    for token, h, c in ((3, 0, 5), (130, 0, 6), (131, 1, 0), (132, 1, 63), (500, 0, 5), (n - 1, 1, 30)):
+        v[token, h, c] = float("nan")
+        none[token:, h, c] = True
+    none = none.repeat_interleave(G, 1)
+    out = _prompt(q, k, v, [0, n], None, d ** -0.5)
+    assert torch.equal(out.isnan().cpu(), none)
+    _inside(out.cpu()[~none], y[~none], tol[~none])
+
+
+def test_prompt_values_near_the_end_of_the_range():
+    # weights are up to 2^8 before they are divided: 64 of 2^7.5 times 1e36 are no number, their mean is
+    n, d = 128, 64
+    q, k, v = _packed(n, n, 1, 1, d, BF16, 13)
+    q[:], k[:], v = 0.0, 0.0, v * 1e36
+    q[:, :, 0], k[64:, :, 0] = 1.0, 41.5
+    _inside(_prompt(q, k, v, [0, n], None, 0.125), *_prompt_ref(q, k, v, [0, n], [0, n], 0.125))
+
+
+def test_prompt_rows_made_again_for_longer_than_a_wait():
+    # 256 queries behind 400000 keys without a number: two seconds of one CTA, whose next requests are as they should be
+    n, few, d = 400_000, 400, 64
+    g = _gen(14)
+    q = torch.randn(256 + few, 1, d, generator=g).to(BF16)
+    kv = torch.zeros(2, n + few, 1, d, dtype=BF16, device="cuda")
+    kv[1, :n] = float("nan")
+    v = torch.randn(few, 1, d, generator=g).to(BF16)
+    kv[1, n:] = v.cuda()
+    for first in (True, False):                            # (the long request before the others, or behind them)
+        if not first:
+            kv = torch.cat([kv[:, n:], kv[:, :n]], 1)
+        out = _prompt(q, kv[0], kv[1], _starts([256] + [1] * few if first else [1] * few + [256]),
+                      _starts([n] + [1] * few if first else [1] * few + [n]), 0.125).cpu()
+        long, short = (out[:256], out[256:]) if first else (out[few:], out[:few])
+        assert long.isnan().all() and torch.equal(short, v)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_prompt_rows_without_weight_are_zero(dtype):
     n, d = 140, 64
     q, k, v = _packed(n, n, 1, 1, d, dtype, 3)
