@@ -7,8 +7,10 @@
 // infinities and then NaN above all: one comparison tells rows that have
 // either, which get the scale NaN.
 //
-// Bound: HBM.  A lane holds 16 bytes of a row of K and of the same row of V, so
-// a row's head is 8 to 32 lanes.
+// Bound: HBM, and issue when writing.  A lane holds 16 bytes of a row of K and of the
+// same row of V, so a row's head is 8 to 32 lanes.  32768 rows of 8 heads of 128, bf16,
+// to 4-bit codes: 35 us, 4.9 TB/s (the pipe that compares and packs is busy for 64 %);
+// rows of 32 heads back from 4-bit codes: 109 us, 6.2 TB/s.
 #include <type_traits>
 
 #include "common.cuh"

@@ -4,8 +4,9 @@
 // x = h + m + l, each the bf16 nearest to what is left, holds all 24 bits of x at
 // any exponent.  Of the nine products of two such sums the six from h h' to 2^-16
 // of it (h h', h m', m h', h l', m m', l h') are made, and the others are below
-// 2^-23 of the product; sums of 16 products are added up in fp32.  (Three products of tf32 halves took
-// 1.7 times as long: an SM makes a quarter as many of them.)
+// 2^-23 of the product; sums of 16 products are added up in fp32.  (Three products
+// of tf32 halves took as long: 8 x 2048 tokens of 8 x 4 heads of 128, 3.4 ms, of 3.3
+// before sums of 16 and 3.8 with them.)
 //
 // A CTA of four warps takes tiles of 16 query rows (a request's positions, the
 // heads of a group side by side) and key tiles of 32 through a ring of two in
@@ -15,7 +16,10 @@
 // paired with product indexes so that every operand is read 16 bytes at a time
 // from rows whose length lets 8 lanes meet no bank twice.
 //
-// Bound: the products.
+// Bound: issue, of the products and of the splits: 8 x 2048 tokens of 8 x 4 heads of
+// 128 take 3.84 ms, 45 TFLOP/s of the formula's products and six times that made.
+// Each warp splits the keys it reads, four times a CTA.  128 tokens of 4 heads of 64
+// take 9.5 us, the latency of four key tiles a warp and of the launch.
 #include <algorithm>
 
 #include "prompt_rows.cuh"

@@ -22,7 +22,10 @@
 // fp16 numbers with 2^eq apart (the row's largest is between 2^13 and 2^14); fp32
 // rows take two for q and two for w.
 //
-// Bound: HBM (d bits / 8 + 4 bytes a row, twice a token).
+// Bound: HBM (d bits / 8 + 4 bytes a row, twice a token), and with 4-bit codes issue,
+// of widening them.  64 requests of up to 24576 tokens, 8 x 4 heads of 128, bf16: int8
+// 379 us, 6.6 TB/s; 4 bits 239 us, 5.4 TB/s (the integer pipe is busy for 58 %, its
+// warps take turns at it).  One request of 32768, 32 heads, int8: 51 us, 5.4 TB/s.
 #include <algorithm>
 #include <cfloat>
 
