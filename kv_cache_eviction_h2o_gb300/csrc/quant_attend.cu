@@ -249,7 +249,7 @@ struct Core {
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
             // 2^13 <= largest 2^-eq < 2^14 (of numbers below 2^-126, a little less)
-            const int eq = big ? max((int)(big >> 23), 1) - 127 - 13 : 0;
+            const int eq = max((int)(big >> 23), 1) - 127 - 13;
             const float down0 = pow2(-(eq / 2)), down1 = pow2(eq / 2 - eq);
             float sum = 0.f;
 #pragma unroll
@@ -271,8 +271,10 @@ struct Core {
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const int up = (kRaw ? 24 : 10) + eq;          // (at most 138; a factor out of range makes the row NaN)
-            const float a = big < 0x7f800000u ? pow2(up / 2) * qscale * pow2(up - up / 2) : NAN;
+            const int up = (kRaw ? 24 : 10) + eq;
+            // A row whose largest value times scale passes 2^114, or that holds an infinity or a NaN, is NaN; up to there the factor
+            // is below 2^11 2^114 log2(e).
+            const float a = __uint_as_float(big) * qscale <= 0x1.715476p114f ? pow2(up / 2) * qscale * pow2(up - up / 2) : NAN;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int from = (2 * t + i) * 4;          // a lane of head 2t + i

@@ -1,0 +1,40 @@
+"""Attention over quantised pages at the ends of fp32's range: queries beyond
+what the call takes.  Bounds as in test_gpu_prompts.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import test_gpu_prompts as P   # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_queries_beyond_the_range_are_nan(dtype, bits, sign):
+    # one key, whose product with the queries has either sign
+    c = P.Cache([1], 1, 64, 16, bits)
+    c.kc[:], c.ks[:] = sign * 5, 1.0
+    q = torch.ones(5, 1, 64)
+    for i, x in enumerate((2.0 ** 113, 1.5 * 2.0 ** 114, 1e36, 3e38, float("inf"))):
+        q[i] *= x
+    out = P._attend(c, q.to(dtype), [0] * 5, [0] * 5, 1.0).cpu()
+    assert out[1:].isnan().all()
+    # within the range: the only key's value
+    v = c.rows(0, 0, 1)[1][0]
+    assert ((out[0, 0].double() - v).abs() <= 2.0 ** -8 * v.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_queries_of_zeros_whatever_the_scale(dtype, bits):
+    n, d = 40, 64
+    c = P.Cache([n], 1, d, 16, bits)
+    q = torch.zeros(1, 2, d, dtype=dtype)
+    for scale in (1e-30, 1.0, 1e36):
+        P._inside(P._attend(c, q, [0], [n - 1], scale), *P._attend_ref(c, q, [0], [n - 1], scale))
