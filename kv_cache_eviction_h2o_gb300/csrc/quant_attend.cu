@@ -173,7 +173,7 @@ struct Core {
     uint32_t q[PARTS][NT][KS][2];
     float o[NT][KS][4];
     float zero[NT][2];                                     // what the scores of heads 2t, 2t + 1 start from
-    float2 zf[NT];                                         // 2^(24 + eq) scale log2(e) (2^(10 + eq))
+    float2 zf[NT];                                         // 2^(24 + eq) scale log2(e)
     float2 m[NT], l[NT], f[NT];                            // f = 2^(m - E)
     int unit[NT][2];                                       // E - m
 
@@ -194,10 +194,10 @@ struct Core {
         return hfma2(u, BITS == 4 && HI ? 0x64006400u : 0x74007400u, BITS == 8 ? 0xb000b000u : 0xa000a000u);
     }
 
-    // c += a b[..][n][k].  With two parts sums of 16 products are added up by the FMA pipe: the tensor cores cut a sum's bits
-    // off where an addition rounds, which adds up over many keys.
+    // c += a b[..][n][k].  With two parts sums of 16 products are added up by the FMA pipe, times `unit`: the tensor cores cut a
+    // sum's bits off where an addition rounds, which adds up over many keys.
     template <int K>
-    __device__ __forceinline__ static void mma_parts(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[PARTS][NT][K][2], int n, int k)
+    __device__ __forceinline__ static void mma_parts(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[PARTS][NT][K][2], int n, int k, float unit = 1.f)
     {
         if constexpr (PARTS == 1) {
             mma16(c, a[0], a[1], a[2], a[3], b[0][n][k][0], b[0][n][k][1]);
@@ -206,7 +206,7 @@ struct Core {
 #pragma unroll
             for (int p = PARTS - 1; p >= 0; --p) mma16(s, a[0], a[1], a[2], a[3], b[p][n][k][0], b[p][n][k][1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] += s[e];
+            for (int e = 0; e < 4; ++e) c[e] = fmaf(s[e], unit, c[e]);
         }
     }
 
@@ -271,7 +271,7 @@ struct Core {
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const int up = (kRaw ? 24 : 10) + eq;
+            const int up = 24 + eq;
             // A row whose largest value times scale passes 2^114, or that holds an infinity or a NaN, is NaN; up to there the factor
             // is below 2^11 2^114 log2(e).
             const float a = __uint_as_float(big) * qscale <= 0x1.715476p114f ? pow2(up / 2) * qscale * pow2(up - up / 2) : NAN;
@@ -380,7 +380,7 @@ struct Core {
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_parts(s[n][x], a, q, n, k);
+                for (int n = 0; n < NT; ++n) mma_parts(s[n][x], a, q, n, k, 0x1p-14f);   // (q.c 2^-24 2^-eq either way: times any ks that a write makes, a number)
             }
         }
         float kf[TILES][2], v[TILES][2];

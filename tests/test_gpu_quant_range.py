@@ -1,5 +1,5 @@
 """Attention over quantised pages at the ends of fp32's range: queries beyond
-what the call takes.  Bounds as in test_gpu_prompts.py."""
+what the call takes, scales near the largest there are.  Bounds as in test_gpu_prompts.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -38,3 +38,16 @@ def test_queries_of_zeros_whatever_the_scale(dtype, bits):
     q = torch.zeros(1, 2, d, dtype=dtype)
     for scale in (1e-30, 1.0, 1e36):
         P._inside(P._attend(c, q, [0], [n - 1], scale), *P._attend_ref(c, q, [0], [n - 1], scale))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("heads,G,d,n", [(2, 2, 64, 300), (1, 16, 128, 2000)])
+def test_keys_near_the_largest_there_are(dtype, bits, heads, G, d, n):
+    # keys up to 1.3e38 and queries of 1e-38: their products are of any size
+    c = P.Cache([n], heads, d, 16, bits, seed=3)
+    c.ks[:] = 1.3e38 / (2 ** (bits - 1) - 1)
+    for size in (1e-38, 3e-38, 1e-30):
+        q = size * P._queries(2, heads * G, d, F32, 4)
+        q = q.to(dtype)
+        P._inside(P._attend(c, q, [0, 0], [n - 1, n // 2], 0.5), *P._attend_ref(c, q, [0, 0], [n - 1, n // 2], 0.5))
