@@ -667,7 +667,8 @@ int h2o_page_quant_read(const void* K, const void* V, const float* kscale, const
  * weights, with the value's scale and a power of two apart, as one fp16 number
  * (2^-12 of each off at most) or, with H2O_F32, two (2^-23).  A query head that
  * holds an infinity or a NaN, or whose largest value times scale passes 2^114, is
- * NaN.  Other arguments, padding rows, empty rows and bad entries as
+ * NaN.  The sum of a row's values by weights whose largest is 1 has to stay within
+ * fp32.  Other arguments, padding rows, empty rows and bad entries as
  * h2o_page_attend.
  */
 int h2o_page_quant_attend(const void* q, long long q_stride, const int* row_seq, const int* row_pos, int rows,

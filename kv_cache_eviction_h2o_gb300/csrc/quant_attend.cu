@@ -16,9 +16,9 @@
 // through one fused multiply-add of two halves to c 2^-10.
 //   z = ks (scale q.c),  p = 2^(z - m),  l = sum p,  w = p vs 2^(m - E),
 //   O 2^(E - m) / l
-// with whole numbers m and E for each query head: m is raised when a logit passes it
-// by 8, E, the exponent of the sums' unit, when a weight with its value's scale passes 2^15,
-// so that w keeps fp16's bits however far the scales are apart.  Queries are
+// with whole numbers m and E for each query head: m is raised, to 8 above the logit, when one passes
+// it (so that p is at most 1, and sums are no larger than the values'), E, the exponent of the sums' unit, when a
+// weight with its value's scale passes 2^15, so that w keeps fp16's bits however far the scales are apart.  Queries are
 // fp16 numbers with 2^eq apart (the row's largest is between 2^13 and 2^14); fp32
 // rows take two for q and two for w.
 //
@@ -169,7 +169,7 @@ struct Core {
     static constexpr int KS = D / 16;                      // steps of the products over channels, and of 16 channels of O^T
     static constexpr float kOffset = BITS == 8 ? 128.f : 8.f;
     static constexpr bool kRaw = PARTS == 1;               // key codes as subnormals
-    static constexpr int kLowest = -118;                   // of E - m: p f is within fp32 for p <= 2^8
+    static constexpr int kLowest = -126;                   // of E - m: f = 2^(m - E) is within fp32
     uint32_t q[PARTS][NT][KS][2];
     float o[NT][KS][4];
     float zero[NT][2];                                     // what the scores of heads 2t, 2t + 1 start from
@@ -300,7 +300,7 @@ struct Core {
         }
     }
 
-    // m to the largest of these logits z = d + m where they pass it by 8, and the sums' unit to what w asks for; d anew
+    // m to 8 above the largest of these logits z = d + m where they pass it, and the sums' unit to what w asks for; d anew
     template <int TILES>
     __device__ __forceinline__ void raise(const float2 (&z)[TILES][2], const float (&v)[TILES][2], int n)
     {
@@ -313,8 +313,8 @@ struct Core {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             float& mi = at(m[n], i);
-            if (top > mi + 8.f && top < INFINITY) {
-                const float to = ceilf(top), by = to - mi;
+            if (top > mi && top < INFINITY) {
+                const float to = ceilf(top) + 8.f, by = to - mi;
                 at(l[n], i) *= ex2_approx(-by);
                 mi = to;
                 unit[n][i] -= (int)fminf(by, 1000.f);
@@ -412,7 +412,7 @@ struct Core {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) most = max3f(most, w[x][r].x, w[x][r].y);
             }
-            if (__any_sync(0xffffffffu, over > 8.f || most > 32768.f)) {
+            if (__any_sync(0xffffffffu, over > 0.f || most > 32768.f)) {
                 raise<TILES>(z, v, n);
 #pragma unroll
                 for (int x = 0; x < TILES; ++x) {

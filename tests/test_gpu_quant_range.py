@@ -1,5 +1,6 @@
 """Attention over quantised pages at the ends of fp32's range: queries beyond
-what the call takes, scales near the largest there are.  Bounds as in test_gpu_prompts.py."""
+what the call takes, scales near the largest there are, weights and values whose
+products are near it.  Bounds as in test_gpu_prompts.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -51,3 +52,22 @@ def test_keys_near_the_largest_there_are(dtype, bits, heads, G, d, n):
         q = size * P._queries(2, heads * G, d, F32, 4)
         q = q.to(dtype)
         P._inside(P._attend(c, q, [0, 0], [n - 1, n // 2], 0.5), *P._attend_ref(c, q, [0, 0], [n - 1, n // 2], 0.5))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("logit", [1.0, 5.0, 5.5, 40.0])
+def test_values_near_the_largest_there_are(dtype, bits, logit):
+    # one key of larger weight than the many before it, and its value times that weight beyond the range
+    n, d, top = 4000, 128, 2 ** (bits - 1) - 1
+    c = P.Cache([n], 1, d, 16, bits, seed=5)
+    c.kc[:], c.ks[:], c.vs[:] = 0, 1.0, 1e-3
+    q = torch.zeros(1, 3, d)
+    q[:, :, 7] = 1.0
+    at = 3203
+    page = int(c.table[0, at // 16])
+    c.kc[page, 0, at % 16, 7], c.ks[page, 0, at % 16], c.vs[page, 0, at % 16] = top, logit / top, 2.5e38 / top
+    q = q.to(dtype)
+    y, tol = P._attend_ref(c, q, [0], [n - 1], 1.0)
+    assert y.isfinite().all()
+    P._inside(P._attend(c, q, [0], [n - 1], 1.0), y, tol)
