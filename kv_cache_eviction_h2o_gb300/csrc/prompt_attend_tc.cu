@@ -22,10 +22,13 @@
 // l are of the unrounded weights.
 //
 // Keys that a row does not see have the weight 0, which leaves a row as it is
-// unless their values are infinite or NaN: a row whose result is no number, and
-// not by its own values' doing, is made again from the keys it sees alone
-// (prompt_row).  Value rows behind a request's last, which may be anything, are
-// zeroed in shared memory.  Waits are bounded; one that runs out leaves NaN.
+// unless their values are infinite or NaN: a row whose weights are numbers, whose
+// result is none, and not by its own values' doing (row_stands), is made again
+// from the keys it sees alone (prompt_row), once the CTA is through its items (no
+// wait stands behind such rows, and the call keeps registers from the loop: in
+// there 8 x 2048 tokens take 6 % longer).  Value rows behind a request's last,
+// which may be anything, are zeroed in shared memory.  Waits are bounded; one that
+// runs out leaves NaN.
 //
 // Bound: the softmax threads' way from scores to weights, 1500 cycles for 64 keys of
 // 128 rows a stream, 640 of them the exponentials; the tensor pipe is busy for 56 %
@@ -79,7 +82,8 @@ struct alignas(1024) Smem {
     Item item[2];
     uint32_t tmem;
     int abort, any;                    // any: there was an item
-    int patience;                      // log2 of the cycles that a wait may take
+    int odd;                           // there are rows to be looked at again:
+    uint32_t again[2][8];              // those of the last two items' softmax warps
 };
 static_assert(sizeof(Smem<128, false>) <= 227 * 1024 && sizeof(Smem<128, true>) <= 227 * 1024, "one CTA's shared memory");
 
@@ -173,7 +177,7 @@ __device__ __forceinline__ uint64_t value_desc(const void* p)
 // every barrier's phases are seen.  V(t)'s place:
 __device__ __forceinline__ int v_at(int t, int n, int L) { return t + min(n, t + L); }
 
-// At most a second, or 2^39 cycles once rows have been made again, which takes up to 32 x 2^24 keys of 270 to 820 cycles.
+// At most a second or so, 2^31 cycles.
 template <class Shared>
 __device__ __forceinline__ bool wait(Shared& S, uint64_t* bar, int count)
 {
@@ -183,16 +187,51 @@ __device__ __forceinline__ bool wait(Shared& S, uint64_t* bar, int count)
     const long long t0 = clock64();
     do {
         if (mbar_try_wait(bar, parity)) return true;
-    } while ((clock64() - t0) >> *(volatile int*)&S.patience == 0);
+    } while (clock64() - t0 < 1ll << 31);
     *(volatile int*)&S.abort = 1;
     return false;
+}
+
+// Rows `redo` of a warp's 32 of an item, whose results are no number though the sums of their weights are (pos and g: this
+// lane's row's position and head of the group).  Values that such a row does not see may have made it so, or the sum of
+// finite ones, whose weights here are up to 2^8, passed fp32's range: it is made again.  Where its own infinities and NaN did, it stands.
+template <int D>
+__device__ __noinline__ void look_again(const PackedArgs& A, unsigned redo, const Item& it, int pos, int g, int end)
+{
+    using T = __nv_bfloat16;
+    const T* const K = static_cast<const T*>(A.k) + it.k0 * A.k_stride + it.h * D;
+    const T* const V = static_cast<const T*>(A.v) + it.k0 * A.v_stride + it.h * D;
+    const int head = it.h * A.G + g, sees = min(it.all, it.all - it.nq + pos + 1);
+    T* const out = static_cast<T*>(A.out) + (it.q0 + (long long)pos) * A.out_stride + head * D;
+    auto row = [&](int r) { return reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r)); };
+    OddRows<D> looked;
+    // all of them at once: the channels that are no number in any of them, and what the first of them sees
+    constexpr int U = 8;
+    unsigned odd = 0, rest = redo;
+#pragma unroll 1
+    while (rest) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = __ffs(rest ? rest : redo) - 1;   // (the first once more where fewer than U are left)
+            rest &= rest - 1;
+            odd |= odd_channels<T, D>(row(r));
+        }
+    }
+    if (row_stands(looked, odd, V, A.v_stride, __shfl_sync(0xffffffffu, sees, __ffs(redo) - 1), end)) return;
+#pragma unroll 1
+    for (; redo; redo &= redo - 1) {
+        const int r = __ffs(redo) - 1, n = __shfl_sync(0xffffffffu, sees, r);
+        T* const o = row(r);
+        const T* const q = static_cast<const T*>(A.q) + (it.q0 + (long long)__shfl_sync(0xffffffffu, pos, r)) * A.q_stride + __shfl_sync(0xffffffffu, head, r) * D;
+        if (!row_stands(looked, odd_channels<T, D>(o), V, A.v_stride, n, end)) prompt_row<T, D>(q, K, A.k_stride, V, A.v_stride, n, A.qscale, o);
+    }
 }
 
 // SPLIT: a cluster takes one item, its CTAs ranges of the item's keys, and their sums are joined at the end.
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                     const __grid_constant__ CUtensorMap mapO, const PackedArgs A, const int np, const int boxes, const int works)
+                     const __grid_constant__ CUtensorMap mapO, const __grid_constant__ PackedArgs A, const int np, const int boxes, const int works)
 {
     using C_ = Cfg<D, SPLIT>;
     constexpr int NS = C_::kSlots;
@@ -222,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&S.last, 2);
         mbar_init(&S.joined, 8);
         mbar_init(&S.taken, 1);
-        S.patience = 31;
+        S.odd = 0;
+        for (int w = 0; w < 8; ++w) S.again[0][w] = S.again[1][w] = 0u;
         S.abort = (smem_u32(raw) & 1023u) != 0;          // (the swizzle goes by address bits; there is no other shared memory, so it is 0)
         fence_mbar_init();
     }
@@ -280,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k > 0) {
                 if (SPLIT) break;
                 if (put > 0) ok = __all_sync(0xffffffffu, wait(S, &S.item_empty[(put - 1) & 1], (put - 1) / 2));
-                if (!ok) break;
+                if (!ok || __any_sync(0xffffffffu, *(volatile int*)&S.odd)) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&S.taken, 16);
                     take_cta(&S.taken_at, &S.taken);
@@ -680,34 +720,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
-            const bool odd = !(odd2.x == 0.f && odd2.y == 0.f) && l != 0.f;
-            unsigned redo = __ballot_sync(0xffffffffu, live && odd && fine);
-            if (redo || !two) {                            // (rows made again are written after what they replace)
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                __syncwarp();
+            // rows whose result is no number though the sum of their weights is one
+            const unsigned again = __ballot_sync(0xffffffffu, live && fine && !(odd2.x == 0.f && odd2.y == 0.f) && l != 0.f && l == l);
+            if (lane == 0) {
+                S.again[(nth_item - 1) & 1][warp - 4] = again;
+                if (again) S.odd = 1;
             }
             if (!two) {
                 meet();                                    // (the sums have been read by the other stream's threads too)
                 if (lane == 0 && nt > 0) mbar_arrive(&S.o_free[s]);
             }
             __syncwarp();
-            // Rows whose result is no number: values that they do not see may have made it so, or the sum of finite ones, whose
-            // weights here are up to 2^8, passed fp32's range.  Where neither is the case it stands.
-            if (redo) {
-                *(volatile int*)&S.patience = 39;
-                const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v) + it.k0 * A.v_stride + it.h * D;
-                const int last = last_odd<__nv_bfloat16, D>(v, A.v_stride, min(it.all, (keys + 15) & ~15));
-                if (last >= 0) redo &= __ballot_sync(0xffffffffu, sees <= last);
-                while (redo) {
-                    const int r = __ffs(redo) - 1;
-                    redo &= redo - 1;
-                    const int rp = __shfl_sync(0xffffffffu, pos, r), rg = __shfl_sync(0xffffffffu, g, r), rn = __shfl_sync(0xffffffffu, sees, r);
-                    const long long qrow = it.q0 + rp;
-                    prompt_row<__nv_bfloat16, D>(static_cast<const __nv_bfloat16*>(A.q) + qrow * A.q_stride + (it.h * G + rg) * D,
-                                                 static_cast<const __nv_bfloat16*>(A.k) + it.k0 * A.k_stride + it.h * D, A.k_stride, v, A.v_stride,
-                                                 rn, c2, static_cast<__nv_bfloat16*>(A.out) + qrow * A.out_stride + (it.h * G + rg) * D);
-                }
-            }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
@@ -715,6 +738,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(S.tmem, 512);
+    if constexpr (!SPLIT) {
+        // (items that both streams worked on are looked at by the even one's warps; the item warp has taken none after the next)
+        if (S.odd && warp >= 4) {
+            const int s = (warp - 4) >> 2, w = warp & 3, row = w * 32 + lane, prow = row / G;
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const Item& it = S.item[i];
+                const bool two = it.p + np < it.nq;
+                const unsigned again = two ? S.again[i][warp - 4] : s == 0 ? S.again[i][w] | S.again[i][w + 4] : 0u;
+                const int seen = min(it.all, it.all - it.nq + min(it.nq, it.p + (two ? s + 1 : 1) * np));
+                if (again) look_again<D>(A, again, it, it.p + (two ? s * np : 0) + prow, row - prow * G, min(it.all, (seen + 15) & ~15));
+            }
+        }
+    }
     if constexpr (SPLIT) {
         // the cluster's sums, a warp a row: of both streams where they had one tile's keys in turn
         cluster_arrive();
