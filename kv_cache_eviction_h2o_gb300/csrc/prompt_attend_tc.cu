@@ -761,8 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool two = it.p + np < it.nq;
             const int rows = min(it.nq - it.p, 2 * np) * G;
             constexpr int V4 = D / 32;
+            unsigned again = 0;                                  // (rows <= 256, so there are at most 11 turns)
+            int turn = 0;
 #pragma unroll 1
-            for (int x = rank * (kThreads / 32) + warp; x < rows; x += C * (kThreads / 32)) {
+            for (int x = rank * (kThreads / 32) + warp; x < rows; x += C * (kThreads / 32), ++turn) {
                 const int s = x / (np * G), r = x - s * np * G, pos = it.p + x / G, g = x % G;
                 float m = -INFINITY, l = 0.f, o[V4] = {};
 #pragma unroll 1
@@ -785,21 +787,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o[e] = l == 0.f ? 0.f : o[e] * f;
                     odd |= !(fabsf(o[e]) < INFINITY);
                 }
-                const long long qrow = it.q0 + pos, k0 = it.k0 - it.before;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out) + qrow * A.out_stride + (it.h * G + g) * D;
-                if (__any_sync(0xffffffffu, odd) && l == l) {
-                    // no number, though the weights are: what the row does not see may have made it so
-                    prompt_row<__nv_bfloat16, D>(static_cast<const __nv_bfloat16*>(A.q) + qrow * A.q_stride + (it.h * G + g) * D,
-                                                 static_cast<const __nv_bfloat16*>(A.k) + k0 * A.k_stride + it.h * D, A.k_stride,
-                                                 static_cast<const __nv_bfloat16*>(A.v) + k0 * A.v_stride + it.h * D, A.v_stride,
-                                                 min(it.all, it.all - it.nq + pos + 1), A.qscale, out);
-                    continue;
-                }
+                if (__any_sync(0xffffffffu, odd) && l == l) again |= 1u << turn;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out) + (it.q0 + (long long)pos) * A.out_stride + (it.h * G + g) * D;
                 uint32_t w[V4 / 2];
 #pragma unroll
                 for (int i = 0; i < V4 / 2; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(o[2 * i + 1]), "f"(o[2 * i]));
                 if constexpr (V4 == 4) *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(w[0], w[1]);
                 else *reinterpret_cast<uint32_t*>(out + lane * 2) = w[0];
+            }
+            // no number, though the weights are: as look_again
+            if (again) {
+                const long long k0 = it.k0 - it.before;
+                const __nv_bfloat16* const K = static_cast<const __nv_bfloat16*>(A.k) + k0 * A.k_stride + it.h * D;
+                const __nv_bfloat16* const V = static_cast<const __nv_bfloat16*>(A.v) + k0 * A.v_stride + it.h * D;
+                const int end = min(it.all, (it.all - it.nq + min(it.nq, it.p + 2 * np) + 15) & ~15);
+                OddRows<D> looked;
+#pragma unroll 1
+                for (; again; again &= again - 1) {
+                    const int x = rank * (kThreads / 32) + warp + (__ffs(again) - 1) * C * (kThreads / 32), pos = it.p + x / G, head = it.h * G + x % G;
+                    const int seen = min(it.all, it.all - it.nq + pos + 1);
+                    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(A.out) + (it.q0 + (long long)pos) * A.out_stride + head * D;
+                    if (!row_stands(looked, odd_channels<__nv_bfloat16, D>(out), V, A.v_stride, seen, end))
+                        prompt_row<__nv_bfloat16, D>(static_cast<const __nv_bfloat16*>(A.q) + (it.q0 + (long long)pos) * A.q_stride + head * D, K, A.k_stride, V,
+                                                     A.v_stride, seen, A.qscale, out);
+                }
             }
         }
         cluster_arrive();
