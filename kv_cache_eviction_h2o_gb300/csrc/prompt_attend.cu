@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(kThreads) prompt_f32_kernel(const PackedArgs A
     cluster_wait();
     // each row by D / 4 lanes: the parts of WK warps of every CTA
     constexpr int LR = D / 4;
+    OddRows<D> looked;
 #pragma unroll 1
     for (int r0 = (rank * kThreads + tid) / LR; r0 < (R + 31) / 32 * 32; r0 += C * kThreads / LR) {   // (whole warps)
         const int r = min(r0, R - 1), e = (tid % LR) * 4, pos = p + r / G;
@@ -281,16 +282,20 @@ __global__ void __launch_bounds__(kThreads) prompt_f32_kernel(const PackedArgs A
         y = ll == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
         float* out = static_cast<float*>(A.out) + (long long)(q0 + pos) * A.out_stride + (h * G + r % G) * D;
         if (in) *reinterpret_cast<float4*>(out + e) = y;
-        // rows whose result is no number: what they do not see may have made it so
+        // Rows whose result is no number: what they do not see may have made it so, or values of theirs whose bf16 parts are
+        // none.  They are made again unless a NaN among what they see has.
         const bool odd = in && !(fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY);
         unsigned redo = __ballot_sync(0xffffffffu, odd);
         __syncwarp();
         while (redo) {
             const int from = (__ffs(redo) - 1) / LR * LR;
             redo &= LR == 32 ? 0u : ~(((1u << LR % 32) - 1u) << from);
-            const int rr = __shfl_sync(0xffffffffu, r, from), rpos = p + rr / G;
-            prompt_row<float, D>(Q + (long long)(q0 + rpos) * A.q_stride + (h * G + rr % G) * D, K, A.k_stride, V, A.v_stride,
-                                 min(nk, nk - nq + rpos + 1), A.qscale, static_cast<float*>(A.out) + (long long)(q0 + rpos) * A.out_stride + (h * G + rr % G) * D);
+            const int rr = __shfl_sync(0xffffffffu, r, from), rpos = p + rr / G, seen = min(nk, nk - nq + rpos + 1);
+            const float rl = __shfl_sync(0xffffffffu, ll, from);
+            const float* q = Q + (long long)(q0 + rpos) * A.q_stride + (h * G + rr % G) * D;
+            float* to = static_cast<float*>(A.out) + (long long)(q0 + rpos) * A.out_stride + (h * G + rr % G) * D;
+            if (rl != rl ? nan_logit(looked, q, K, A.k_stride, seen) : row_stands(looked, odd_channels<float, D>(to), V, A.v_stride, seen, nk)) continue;
+            prompt_row<float, D>(q, K, A.k_stride, V, A.v_stride, seen, A.qscale, to);
         }
     }
     cluster_arrive();

@@ -134,6 +134,7 @@ template <int D> struct OddRows {
     static constexpr int E = D / 32;
     int last = -2;                                         // the last value row behind what the first row sees that holds an infinity or a NaN, or -1; -2: not looked for
     int to[2] = {0, 0}, first[2][E];                       // rows looked at, and the first that holds a NaN [0], either [1], in this lane's channels
+    int keys = 0, key = INT_MAX;                           // key rows looked at, and the first that holds a NaN
     __device__ __forceinline__ OddRows()
     {
 #pragma unroll
@@ -203,6 +204,32 @@ __device__ __noinline__ bool row_stands(OddRows<D>& R, unsigned odd, const T* v,
     for (int e = 0; e < E; ++e) R.first[either][e] = first[e];
     R.to[either] = to;
     return stands;
+}
+
+// Whether the query or one of the first `sees` keys holds a NaN, which makes a row NaN as a whole.
+template <typename T, int D>
+__device__ __noinline__ bool nan_logit(OddRows<D>& R, const T* q, const T* k, long long stride, int sees)
+{
+    constexpr int E = D / 32, U = 16;
+    const int lane = threadIdx.x & 31;
+    float x[U][E];
+    load_vec<T, E>(q + lane * E, x[0]);
+    bool none = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) none |= x[0][e] != x[0][e];
+    if (__any_sync(0xffffffffu, none)) return true;
+    for (; R.key >= sees && R.keys < sees; R.keys = min(R.keys + U, sees)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) load_vec<T, E>(k + min(R.keys + u, sees - 1) * stride + lane * E, x[u]);
+        int at = INT_MAX;
+#pragma unroll
+        for (int u = U - 1; u >= 0; --u)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (x[u][e] != x[u][e]) at = min(R.keys + u, sees - 1);
+        R.key = __reduce_min_sync(0xffffffffu, at);
+    }
+    return R.key < sees;
 }
 
 // The request of work index x, by the whole warp: the last i with f(i) = q_start[i] / per + i <= x, or -1.  f's values

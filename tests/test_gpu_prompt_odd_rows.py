@@ -91,7 +91,7 @@ def _time(f):
 
 
 # (rows were made again key by key before: hundreds of times the call)
-TIMED = [(BF16, 8, 2048, 2048, 8, 4, 128), (BF16, 1, 5, 20005, 8, 1, 128)]
+TIMED = [(BF16, 8, 2048, 2048, 8, 4, 128), (BF16, 1, 5, 20005, 8, 1, 128), (F32, 2, 1024, 1024, 8, 4, 128), (F32, 1, 5, 20005, 8, 1, 128)]
 
 
 @pytest.mark.parametrize("case", range(len(TIMED)))
