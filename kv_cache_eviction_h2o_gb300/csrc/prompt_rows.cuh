@@ -36,7 +36,7 @@ template <typename T, int N> struct Raw {
 template <typename T, int D>
 __device__ __noinline__ void prompt_row(const T* q, const T* k, long long kstride, const T* v, long long vstride, int n, float qscale, T* out)
 {
-    constexpr int E = D / 8, U = (sizeof(T) == 2 ? 32 : 16) / (E * (int)sizeof(T) / 4);   // (32 or 16 registers of keys, and as many of values)
+    constexpr int E = D / 8, U = 32 / (E * (int)sizeof(T) / 4);        // (32 registers of keys, and as many of values)
     const int lane = threadIdx.x & 31, group = lane >> 3, c = (lane & 7) * E;
     float o[E] = {}, m = -INFINITY, l = 0.f;
     Raw<T, E> x;
