@@ -610,7 +610,8 @@ int h2o_rope(const void* q, long long q_stride, void* q_out, long long q_out_str
  *   q, out [rows][kv_heads * groups][head_dim], k, v [k_rows][kv_heads][head_dim]
  *   of dtype H2O_F32 or H2O_BF16; query head h * groups + g to key head h, 1 <=
  *   groups <= 16.  Sums and statistics in fp32; with bf16 each softmax weight is
- *   rounded to bf16 for its product (2^-8 of it off at most) and outputs once.
+ *   rounded to bf16 for its product (2^-8 of it off at most) and outputs once; with
+ *   fp32 numbers below 2^-110 are off by 2^-134 at most.
  *   out may not overlap q, k or v.
  *   q_start, k_start [requests + 1]: device int32, ascending, within rows and
  *   k_rows; k_start NULL: the same as q_start.  Rows of out outside all
@@ -618,9 +619,11 @@ int h2o_rope(const void* q, long long q_stride, void* q_out, long long q_out_str
  *   or keys are none of the call's.  With starts that descend, which rows are
  *   written is not defined; nothing else is.
  * A row all of whose logits are -inf is zero.  Keys and values a query does not
- * see do not touch it, whatever they hold (a row that an infinity or NaN among its
- * tile's values makes no number is made again from its own keys, by one warp).  The
- * sum of a row's values by weights whose largest is 1 has to stay within fp32.
+ * see do not touch it, whatever they hold.  A row that an infinity or NaN among the
+ * values just behind its own makes no number is made again from its own keys by
+ * one warp, a few hundred cycles a key, and so is one with fp32 that sees an infinity
+ * or a number that bf16 rounds to one.  Rows that their own NaN make NaN cost nothing.
+ * The sum of a row's values by weights whose largest is 1 has to stay within fp32.
  * rows, k_rows <= 2^24, rows * kv_heads * groups and k_rows * kv_heads <= 2^28,
  * 1 <= requests <= 16384, requests * kv_heads <= 2^22.
  */
@@ -662,10 +665,14 @@ int h2o_page_quant_read(const void* K, const void* V, const float* kscale, const
  * sees the tokens 0..row_pos[r] of request row_seq[r],
  *   out = softmax(scale q.K) V,  K = kscale * codes, V = vscale * codes.
  * Codes are multiplied as they are (exact in fp16), scales apart in fp32 (none is
- * negative); queries as fp16 numbers with a power of two of the row apart, two of
- * them where dtype is H2O_F32 (off by 2^-23 of the row's largest at most), and
- * weights, with the value's scale and a power of two apart, as one fp16 number
- * (2^-12 of each off at most) or, with H2O_F32, two (2^-23).  A query head that
+ * negative).  With H2O_BF16 a query is one fp16 number a channel, with a power of
+ * two of the head apart (off by 2^-34 of the head's largest |q| at most), its product
+ * with a code is cut at 2^-13 of that largest |q| by the tensor cores' sums, and a
+ * weight, with the value's scale and a power of two apart, is one fp16 number (2^-11
+ * of it off at most).  With H2O_F32 both are two such numbers (off by 2^-23 of the
+ * head's largest |q| and by 2^-22 of the weight), and sums of 16 products are added
+ * up in fp32.  A weight is off by 2^-30 of the head's largest besides, each times its
+ * value's scale.  A query head that
  * holds an infinity or a NaN, or whose largest value times scale passes 2^114, is
  * NaN.  The sum of a row's values by weights whose largest is 1 has to stay within
  * fp32.  Other arguments, padding rows, empty rows and bad entries as

@@ -1,8 +1,8 @@
 // prompt_attend.cu -- causal attention over packed prompts in fp32, on the
 // tensor cores' bf16 products, six to one.
 //
-// x = h + m + l, each the bf16 nearest to what is left, holds all 24 bits of x at
-// any exponent.  Of the nine products of two such sums the six from h h' to 2^-16
+// x = h + m + l, each the bf16 nearest to what is left, holds all 24 bits of x from
+// 2^-110 on (below, what is left is half of bf16's last step, 2^-134).  Of the nine products of two such sums the six from h h' to 2^-16
 // of it (h h', h m', m h', h l', m m', l h') are made, and the others are below
 // 2^-23 of the product; sums of 16 products are added up in fp32.  (Three products
 // of tf32 halves took as long: 8 x 2048 tokens of 8 x 4 heads of 128, 3.4 ms, of 3.3

@@ -19,7 +19,10 @@
 // The next item's queries, keys and scores are under way while the last one's
 // rows leave.  A row's maximum m is raised, and O scaled, only when a logit
 // passes it by more than 2^8.  P is rounded to bf16 for the product, the sums
-// l are of the unrounded weights.
+// l are of the unrounded weights: outputs are 0.0021 off (8 x 2048 tokens) to 0.0023
+// (behind 15500), where their own rounding is 0.0016.  Two parts of P and two
+// products bring that down to the rounding, and take 206 -> 261 us for 8 x 2048 tokens
+// of 8 x 4 heads, 768 -> 1013 for 2048 behind 30000 of 32.
 //
 // Keys that a row does not see have the weight 0, which leaves a row as it is
 // unless their values are infinite or NaN: a row whose weights are numbers, whose

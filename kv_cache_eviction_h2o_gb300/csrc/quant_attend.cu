@@ -16,11 +16,14 @@
 // through one fused multiply-add of two halves to c 2^-10.
 //   z = ks (scale q.c),  p = 2^(z - m),  l = sum p,  w = p vs 2^(m - E),
 //   O 2^(E - m) / l
-// with whole numbers m and E for each query head: m is raised, to 8 above the logit, when one passes
-// it (so that p is at most 1, and sums are no larger than the values'), E, the exponent of the sums' unit, when a
-// weight with its value's scale passes 2^15, so that w keeps fp16's bits however far the scales are apart.  Queries are
-// fp16 numbers with 2^eq apart (the row's largest is between 2^13 and 2^14); fp32
-// rows take two for q and two for w.
+// with whole numbers m and E for each query head: m is raised, to 8 above the logit,
+// when one passes it (so that p is at most 1, and sums are no larger than the
+// values'), E, the exponent of the sums' unit, when a weight with its value's scale
+// passes 2^15, so that w keeps fp16's bits however far the scales are apart.
+// Queries are fp16 numbers with 2^eq apart (the row's largest is between 2^13 and
+// 2^14); fp32 rows take two for q and two for w.  (One for w with bf16 rows: up to 2^-11
+// of each weight, of either sign, is not to be seen beside the output's own
+// rounding: 0.0017 off, as a form with fp32 weights.)
 //
 // Bound: HBM (d bits / 8 + 4 bytes a row, twice a token), and with 4-bit codes issue,
 // of widening them.  64 requests of up to 24576 tokens, 8 x 4 heads of 128, bf16: int8
