@@ -16,10 +16,10 @@
 // paired with product indexes so that every operand is read 16 bytes at a time
 // from rows whose length lets 8 lanes meet no bank twice.
 //
-// Bound: issue, of the products and of the splits: 8 x 2048 tokens of 8 x 4 heads of
-// 128 take 3.84 ms, 45 TFLOP/s of the formula's products and six times that made.
+// Bound: issue, of the products and of the splits: 8 prompts of up to 2048 tokens of 8 x 4 heads of
+// 128 take 3.82 ms, 45 TFLOP/s of the formula's products and six times that made.
 // Each warp splits the keys it reads, four times a CTA.  128 tokens of 4 heads of 64
-// take 9.5 us, the latency of four key tiles a warp and of the launch.
+// take 9.1 us, the latency of four key tiles a warp and of the launch.
 #include <algorithm>
 
 #include "prompt_rows.cuh"

@@ -34,11 +34,11 @@
 // runs out leaves NaN.
 //
 // Bound: the softmax threads' way from scores to weights, 1500 cycles for 64 keys of
-// 128 rows a stream, 640 of them the exponentials; the tensor pipe is busy for 56 %
-// and the exponentials' for 29 % of the time.  8192 tokens of 8 x 4 heads of 128: 343
-// us, 1.60 PFLOP/s of the products that the mask leaves, 8 x 2048: 143 us, 1.21 (4400
-// cycles an item before its first weights and after its last).  (Two places for a
-// part's scores and one for its weights: 144 us.)
+// 128 rows a stream, 640 of them the exponentials; the tensor pipe is busy for 58 %
+// and the exponentials' for 29 % of the time.  8192 tokens of 8 x 4 heads of 128: 350
+// us, 1.57 PFLOP/s of the products that the mask leaves, 8 prompts of up to 2048: 142 us,
+// 1.22 (4400 cycles an item before its first weights and after its last).  (Two places
+// for a part's scores and one for its weights: 144 us.)
 #include <algorithm>
 
 #include "paged.h"
