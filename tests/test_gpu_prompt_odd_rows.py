@@ -124,8 +124,8 @@ def test_rows_without_a_number_take_no_longer(case, what):
 
 
 def test_rows_made_again_for_longer_than_a_second():
-    # 128 queries behind 800000 keys, whose last value is no number and seen by the last query alone: the others are made again
-    # while the rest of the CTA waits, and the next requests are as they should be
+    # 128 queries behind 800000 keys, whose last value is no number and seen by the last query alone: the others are made again,
+    # which takes longer than any wait of the kernel may, and the other requests are as they should be
     n, new, few, d = 800_000, 128, 400, 64
     g = P._gen(14)
     q = torch.randn(new + few, 1, d, generator=g).to(BF16)
