@@ -622,7 +622,7 @@ int h2o_rope(const void* q, long long q_stride, void* q_out, long long q_out_str
  * see do not touch it, whatever they hold.  A row that an infinity or NaN among the
  * values just behind its own makes no number is made again from its own keys by
  * one warp, a few hundred cycles a key, and so is one with fp32 that sees an infinity
- * or a number that bf16 rounds to one.  Rows that their own NaN make NaN cost nothing.
+ * or a number that bf16 rounds to one.  Rows that their own NaN make NaN cost little more than others.
  * The sum of a row's values by weights whose largest is 1 has to stay within fp32.
  * rows, k_rows <= 2^24, rows * kv_heads * groups and k_rows * kv_heads <= 2^28,
  * 1 <= requests <= 16384, requests * kv_heads <= 2^22.

@@ -37,7 +37,6 @@ template <int D, int WK> struct alignas(16) Smem {
     float k[kStages][kKeys][D + 16];
     float v[kStages][kKeys][D + 4];
     float2 ml[kWarps][16];                             // of each warp's rows
-    float2 sum_ml[kRows];
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool fill)
